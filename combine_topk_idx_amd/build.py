@@ -30,7 +30,8 @@ ROOT = os.path.dirname(HERE)
 CONSUMER_SRC = os.path.join(ROOT, "tests", "c_abi", "ep_consumer.c")
 CONSUMER = os.path.join(ROOT, "tests", "c_abi", "ep_consumer")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
-SOURCES = ["layout.hip", "dispatch.hip", "combine.hip", "moe.hip", "static_ws.hip", "ep_api.cpp"]
+SOURCES = ["layout.hip", "dispatch.hip", "combine.hip", "moe.hip", "moe_layer.hip", "router.hip", "lora.hip",
+           "static_ws.hip", "ep_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

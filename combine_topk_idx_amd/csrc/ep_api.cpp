@@ -14,7 +14,10 @@
 
 #include "common.hpp"
 #include "dispatch.hpp"
+#include "lora.hpp"
 #include "moe.hpp"
+#include "moe_layer.hpp"
+#include "router.hpp"
 #include "static_ws.hpp"
 
 namespace {
@@ -456,6 +459,265 @@ ep_status_t ep_moe_gmm2(const ep_handle_t *handle, const int64_t *recv_count, co
     return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: a_buf needs %zu bytes, out_buf %zu", fn, need_a, need_o);
   const hipError_t e = ep::launch_moe_gmm2(*handle, recv_count, (const char *)a_buf, inter, hidden, w2, w2_scales,
                                            (char *)out_buf, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+namespace {
+
+bool valid_weight_quant(int q) { return q == EP_QUANT_NONE || q == EP_QUANT_MXFP8 || q == EP_QUANT_MXFP4; }
+bool valid_idx(int d) { return d == EP_IDX_INT32 || d == EP_IDX_INT64; }
+size_t idx_bytes(int d) { return d == EP_IDX_INT64 ? 8 : 4; }
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
+}  // namespace
+
+ep_status_t ep_moe_packed_bytes_ex(int32_t num_experts, int32_t rows, int32_t k, ep_quant_t quant,
+                                   size_t *weight_bytes, size_t *scales_bytes) {
+  const char *fn = "ep_moe_packed_bytes_ex";
+  if (num_experts <= 0 || num_experts > ep::kMaxExperts || rows <= 0 || rows % 32 != 0 || k <= 0 || k % 64 != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: need 0 < experts <= 512, rows %% 32 == 0, k %% 64 == 0", fn);
+  if (!valid_weight_quant(quant))
+    return fail(EP_ERR_INVALID_ARG, "%s: weights are EP_QUANT_NONE, EP_QUANT_MXFP8 or EP_QUANT_MXFP4 (got %d)", fn,
+                (int)quant);
+  size_t c, sc;
+  ep::moe_packed_bytes(num_experts, rows, k, &c, &sc);
+  if (weight_bytes) *weight_bytes = c / 2048 * ep::fragment_bytes(quant);
+  if (scales_bytes) *scales_bytes = quant == EP_QUANT_NONE ? 0 : sc;
+  return EP_OK;
+}
+
+ep_status_t ep_moe_pack_weights_ex(const void *weights, const void *scales, int32_t num_experts, int32_t rows,
+                                   int32_t k, ep_quant_t quant, int32_t gate_up, void *packed_weights,
+                                   void *packed_scales, void *stream) {
+  const char *fn = "ep_moe_pack_weights_ex";
+  const ep_status_t st = ep_moe_packed_bytes_ex(num_experts, rows, k, quant, nullptr, nullptr);
+  if (st != EP_OK)
+    return fail(st, "%s: need 0 < experts <= 512, rows %% 32 == 0, k %% 64 == 0, bf16 / MXFP8 / MXFP4 weights", fn);
+  if (gate_up != 0 && gate_up != 1) return fail(EP_ERR_INVALID_ARG, "%s: gate_up must be 0 or 1", fn);
+  if (gate_up && rows % 64 != 0) return fail(EP_ERR_INVALID_ARG, "%s: gate/up weights need rows %% 64 == 0", fn);
+  if (!weights || !packed_weights || !aligned(weights, 16) || !aligned(packed_weights, 16))
+    return fail(EP_ERR_INVALID_ARG, "%s: NULL or misaligned buffer", fn);
+  if (quant != EP_QUANT_NONE && (!scales || !packed_scales || !aligned(packed_scales, 16)))
+    return fail(EP_ERR_INVALID_ARG, "%s: scales NULL or misaligned", fn);
+  const hipError_t e = ep::launch_pack_ex(weights, scales, quant, num_experts, rows, k, gate_up, packed_weights,
+                                          packed_scales, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+size_t ep_moe_layer_workspace_bytes(int64_t num_tokens, int32_t num_topk, int32_t num_experts, int32_t hidden,
+                                    int32_t inter) {
+  if (num_tokens < 0 || num_topk <= 0 || num_topk > ep::kMaxTopk || num_experts <= 0 ||
+      num_experts > ep::kMaxExperts || num_tokens > ep::kLayerMaxPairs / num_topk || hidden <= 0 || hidden % 64 != 0 ||
+      hidden > kMaxHidden || inter <= 0 || inter % 64 != 0 || inter > kMaxHidden)
+    return 0;
+  return ep::layer_ws(num_tokens, num_topk, hidden, inter).total;
+}
+
+ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, const void *topk_idx,
+                         ep_idx_dtype_t idx_dtype, const float *topk_weights, int32_t num_topk,
+                         int32_t num_experts, int32_t inter, ep_quant_t w_quant, const void *w1,
+                         const void *w1_scales, const void *w2, const void *w2_scales, void *workspace,
+                         size_t workspace_bytes, void *out, void *stream) {
+  const char *fn = "ep_moe_layer";
+  if (num_topk <= 0 || num_topk > ep::kMaxTopk)
+    return fail(EP_ERR_INVALID_ARG, "%s: num_topk must be in (0, 16] (got %d)", fn, num_topk);
+  if (num_experts <= 0 || num_experts > ep::kMaxExperts)
+    return fail(EP_ERR_INVALID_ARG, "%s: num_experts must be in (0, 512] (got %d)", fn, num_experts);
+  if (num_tokens < 0) return fail(EP_ERR_INVALID_ARG, "%s: negative token count", fn);
+  if (num_tokens > ep::kLayerMaxPairs / num_topk)
+    return fail(EP_ERR_UNSUPPORTED, "%s: more than %lld (token, j) pairs; use dispatch, the expert GEMMs and combine",
+                fn, (long long)ep::kLayerMaxPairs);
+  if (hidden <= 0 || hidden % 64 != 0 || inter <= 0 || inter % 64 != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: hidden and inter must be positive multiples of 64 (got %d, %d)", fn, hidden,
+                inter);
+  if (hidden > kMaxHidden || inter > kMaxHidden)
+    return fail(EP_ERR_UNSUPPORTED, "%s: hidden / inter above %d", fn, kMaxHidden);
+  if (!valid_idx(idx_dtype)) return fail(EP_ERR_INVALID_ARG, "%s: topk_idx dtype must be int32 or int64", fn);
+  if (!valid_weight_quant(w_quant))
+    return fail(EP_ERR_INVALID_ARG, "%s: weights are EP_QUANT_NONE, EP_QUANT_MXFP8 or EP_QUANT_MXFP4 (got %d)", fn,
+                (int)w_quant);
+  if (num_tokens > 0) {
+    if (!topk_idx || !aligned(topk_idx, idx_bytes(idx_dtype)))
+      return fail(EP_ERR_INVALID_ARG, "%s: topk_idx is NULL or not aligned to its dtype", fn);
+    if (!topk_weights || !aligned(topk_weights, 4))
+      return fail(EP_ERR_INVALID_ARG, "%s: topk_weights is NULL or misaligned (it is required)", fn);
+    if (!x || !aligned(x, 16) || !out || !aligned(out, 16))
+      return fail(EP_ERR_INVALID_ARG, "%s: x / out NULL or not 16-byte aligned", fn);
+    const size_t bytes = (size_t)num_tokens * hidden * 2;
+    if (overlap(x, bytes, out, bytes)) return fail(EP_ERR_INVALID_ARG, "%s: out overlaps x", fn);
+  }
+  if (!w1 || !w2 || !aligned(w1, 16) || !aligned(w2, 16))
+    return fail(EP_ERR_INVALID_ARG, "%s: w1 / w2 NULL or not 16-byte aligned", fn);
+  if (w_quant != EP_QUANT_NONE && (!w1_scales || !w2_scales || !aligned(w1_scales, 16) || !aligned(w2_scales, 16)))
+    return fail(EP_ERR_INVALID_ARG, "%s: w1_scales / w2_scales NULL or not 16-byte aligned", fn);
+  if (!workspace || !aligned(workspace, ep::kWsAlign))
+    return fail(EP_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
+  const size_t need = ep::layer_ws(num_tokens, num_topk, hidden, inter).total;
+  if (workspace_bytes < need)
+    return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
+  const ep::LayerArgs a{x, num_tokens, num_topk, num_experts, hidden, inter, w_quant, topk_idx,
+                        idx_dtype == EP_IDX_INT64, topk_weights, (const uint8_t *)w1, (const uint8_t *)w1_scales,
+                        (const uint8_t *)w2, (const uint8_t *)w2_scales, (char *)workspace, out};
+  const hipError_t e = ep::launch_moe_layer(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+ep_status_t check_router(const char *fn, const void *logits, int dtype, int64_t T, int32_t E, int32_t k, int score,
+                         int32_t renormalize, const void *idx, int idx_dtype) {
+  if (dtype < EP_FLOAT_F32 || dtype > EP_FLOAT_F16)
+    return fail(EP_ERR_INVALID_ARG, "%s: logits dtype must be float32, bfloat16 or float16", fn);
+  if (E <= 0 || E > ep::kMaxExperts)
+    return fail(EP_ERR_INVALID_ARG, "%s: num_experts must be in (0, 512] (got %d)", fn, E);
+  if (k <= 0 || k > ep::kMaxTopk || k > E)
+    return fail(EP_ERR_INVALID_ARG, "%s: num_topk must be in (0, 16] and at most num_experts (got %d)", fn, k);
+  if (T < 0 || T > INT32_MAX) return fail(EP_ERR_INVALID_ARG, "%s: num_tokens out of range", fn);
+  if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID)
+    return fail(EP_ERR_INVALID_ARG, "%s: unknown score %d", fn, score);
+  if (renormalize != 0 && renormalize != 1) return fail(EP_ERR_INVALID_ARG, "%s: renormalize must be 0 or 1", fn);
+  if (!valid_idx(idx_dtype)) return fail(EP_ERR_INVALID_ARG, "%s: topk_idx dtype must be int32 or int64", fn);
+  if (T > 0 && (!logits || !aligned(logits, dtype == EP_FLOAT_F32 ? 4 : 2)))
+    return fail(EP_ERR_INVALID_ARG, "%s: logits is NULL or not aligned to its dtype", fn);
+  if (T > 0 && (!idx || !aligned(idx, idx_bytes(idx_dtype))))
+    return fail(EP_ERR_INVALID_ARG, "%s: topk_idx is NULL or not aligned to its dtype", fn);
+  return EP_OK;
+}
+
+ep_status_t check_lora(const char *fn, const ep_handle_t *h, int32_t in, int32_t out, int32_t rank, const void *a,
+                       const void *b, const float *scale, const void *workspace, size_t workspace_bytes,
+                       int backward) {
+  const ep_status_t st = check_handle(h, fn);
+  if (st != EP_OK) return st;
+  if (h->num_topk != 1) return fail(EP_ERR_INVALID_ARG, "%s: the layout must have one adapter per token (num_topk 1)", fn);
+  if (in <= 0 || in % 32 != 0 || out <= 0 || out % 32 != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: in and out features must be positive multiples of 32 (got %d, %d)", fn, in, out);
+  if (in > kMaxHidden || out > kMaxHidden)
+    return fail(EP_ERR_UNSUPPORTED, "%s: in / out features above %d", fn, kMaxHidden);
+  if (rank < 8 || rank > ep::kMaxRank || rank % 8 != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: rank must be a multiple of 8 in [8, %d] (got %d)", fn, ep::kMaxRank, rank);
+  if (!a || !aligned(a, 16) || !b || !aligned(b, 16))
+    return fail(EP_ERR_INVALID_ARG, "%s: a / b NULL or not 16-byte aligned", fn);
+  if (scale && !aligned(scale, 4)) return fail(EP_ERR_INVALID_ARG, "%s: scale is misaligned", fn);
+  if (!workspace || !aligned(workspace, ep::kWsAlign))
+    return fail(EP_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
+  const size_t need = ep::lora_ws(h->num_tokens, in, out, rank, h->num_experts, backward).total;
+  if (workspace_bytes < need)
+    return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
+  return EP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status_t ep_router(const void *logits, ep_float_t dtype, int64_t num_tokens, int32_t num_experts,
+                      int32_t num_topk, ep_score_t score, const float *bias, int32_t num_groups,
+                      int32_t topk_groups, int32_t group_top, int32_t renormalize, float scale, void *topk_idx,
+                      ep_idx_dtype_t idx_dtype, float *topk_weights, void *stream) {
+  const char *fn = "ep_router";
+  const ep_status_t st = check_router(fn, logits, dtype, num_tokens, num_experts, num_topk, score, renormalize,
+                                      topk_idx, idx_dtype);
+  if (st != EP_OK) return st;
+  if (num_groups <= 0 || num_groups > ep::kMaxGroups || num_experts % num_groups != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: num_groups must divide num_experts and be at most %d (got %d)", fn,
+                ep::kMaxGroups, num_groups);
+  if (topk_groups <= 0 || topk_groups > num_groups)
+    return fail(EP_ERR_INVALID_ARG, "%s: topk_groups must be in (0, num_groups] (got %d)", fn, topk_groups);
+  if (group_top < 1 || group_top > 2 || num_experts / num_groups < group_top)
+    return fail(EP_ERR_INVALID_ARG, "%s: group_top must be 1 or 2 and no more than a group's experts (got %d)", fn,
+                group_top);
+  if (bias && !aligned(bias, 4)) return fail(EP_ERR_INVALID_ARG, "%s: bias is misaligned", fn);
+  if (num_tokens > 0 && (!topk_weights || !aligned(topk_weights, 4)))
+    return fail(EP_ERR_INVALID_ARG, "%s: topk_weights is NULL or misaligned", fn);
+  const ep::RouterArgs a{logits, dtype, num_tokens, num_experts, num_topk, score, bias, num_groups,
+                         topk_groups, group_top, renormalize, scale};
+  const hipError_t e = ep::launch_router(a, topk_idx, idx_dtype == EP_IDX_INT64, topk_weights, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num_tokens, int32_t num_experts,
+                               int32_t num_topk, ep_score_t score, int32_t renormalize, float scale,
+                               const void *topk_idx, ep_idx_dtype_t idx_dtype, const float *grad_weights,
+                               void *grad_logits, void *stream) {
+  const char *fn = "ep_router_backward";
+  const ep_status_t st = check_router(fn, logits, dtype, num_tokens, num_experts, num_topk, score, renormalize,
+                                      topk_idx, idx_dtype);
+  if (st != EP_OK) return st;
+  if (num_tokens > 0 && (!grad_weights || !aligned(grad_weights, 4)))
+    return fail(EP_ERR_INVALID_ARG, "%s: grad_weights is NULL or misaligned", fn);
+  if (num_tokens > 0 && (!grad_logits || !aligned(grad_logits, dtype == EP_FLOAT_F32 ? 4 : 2)))
+    return fail(EP_ERR_INVALID_ARG, "%s: grad_logits is NULL or not aligned to its dtype", fn);
+  const ep::RouterArgs a{logits, dtype, num_tokens, num_experts, num_topk, score, nullptr, 1, 1, 1, renormalize,
+                         scale};
+  const hipError_t e = ep::launch_router_backward(a, topk_idx, idx_dtype == EP_IDX_INT64, grad_weights, grad_logits,
+                                                  (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+size_t ep_lora_workspace_bytes(int64_t num_max_tokens, int32_t in_features, int32_t out_features, int32_t rank,
+                               int32_t num_adapters, int32_t backward) {
+  if (num_max_tokens < 0 || num_max_tokens > INT32_MAX || in_features <= 0 || in_features % 32 != 0 ||
+      in_features > kMaxHidden || out_features <= 0 || out_features % 32 != 0 || out_features > kMaxHidden || rank < 8 ||
+      rank > ep::kMaxRank || rank % 8 != 0 || num_adapters <= 0 || num_adapters > ep::kMaxExperts ||
+      (backward != 0 && backward != 1))
+    return 0;
+  return ep::lora_ws(num_max_tokens, in_features, out_features, rank, num_adapters, backward).total;
+}
+
+ep_status_t ep_lora(const ep_handle_t *handle, const void *x, int32_t in_features, int32_t out_features,
+                    int32_t rank, const void *a, const void *b, const float *scale, const void *base, void *out,
+                    float *down, void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "ep_lora";
+  const ep_status_t st = check_lora(fn, handle, in_features, out_features, rank, a, b, scale, workspace,
+                                    workspace_bytes, 0);
+  if (st != EP_OK) return st;
+  if (handle->num_tokens > 0) {
+    if (!x || !aligned(x, 16) || !out || !aligned(out, 16) || (base && !aligned(base, 16)))
+      return fail(EP_ERR_INVALID_ARG, "%s: x / out NULL, or x / out / base not 16-byte aligned", fn);
+    if (!down || !aligned(down, 16)) return fail(EP_ERR_INVALID_ARG, "%s: down is NULL or not 16-byte aligned", fn);
+    const size_t nx = (size_t)handle->num_tokens * in_features * 2, no = (size_t)handle->num_tokens * out_features * 2;
+    if (overlap(x, nx, out, no) || (base != out && overlap(base, no, out, no)))
+      return fail(EP_ERR_INVALID_ARG, "%s: out overlaps x, or base in part", fn);
+  }
+  const ep::LoraArgs p{*handle, x, in_features, out_features, rank, a, b, scale, base, out, down, (char *)workspace};
+  const hipError_t e = ep::launch_lora(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, const void *x, int32_t in_features,
+                             int32_t out_features, int32_t rank, const void *a, const void *b, const float *scale,
+                             const float *down, const void *grad_base, void *grad_x, float *grad_a, float *grad_b,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "ep_lora_backward";
+  const ep_status_t st = check_lora(fn, handle, in_features, out_features, rank, a, b, scale, workspace,
+                                    workspace_bytes, 1);
+  if (st != EP_OK) return st;
+  if (handle->num_tokens > 0) {
+    if (!grad_out || !aligned(grad_out, 16) || !x || !aligned(x, 16) || !grad_x || !aligned(grad_x, 16) ||
+        (grad_base && !aligned(grad_base, 16)))
+      return fail(EP_ERR_INVALID_ARG, "%s: grad_out / x / grad_x NULL, or a row buffer not 16-byte aligned", fn);
+    if (!down || !aligned(down, 16)) return fail(EP_ERR_INVALID_ARG, "%s: down is NULL or not 16-byte aligned", fn);
+    const size_t nx = (size_t)handle->num_tokens * in_features * 2, no = (size_t)handle->num_tokens * out_features * 2;
+    if (overlap(x, nx, grad_x, nx) || overlap(grad_out, no, grad_x, nx) ||
+        (grad_base != grad_x && overlap(grad_base, nx, grad_x, nx)))
+      return fail(EP_ERR_INVALID_ARG, "%s: grad_x overlaps x, grad_out, or grad_base in part", fn);
+  }
+  if (!grad_a || !aligned(grad_a, 16) || !grad_b || !aligned(grad_b, 16))
+    return fail(EP_ERR_INVALID_ARG, "%s: grad_a / grad_b NULL or not 16-byte aligned", fn);
+  const ep::LoraGradArgs p{*handle, grad_out, x, in_features, out_features, rank, a, b, scale, down, grad_base, grad_x,
+                           grad_a, grad_b, (char *)workspace};
+  const hipError_t e = ep::launch_lora_backward(p, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, fn);
   return EP_OK;
 }

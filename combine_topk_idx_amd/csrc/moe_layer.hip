@@ -1,0 +1,425 @@
+// The whole expert layer of a MoE block for a few tokens, in two launches:
+// no receive rows, no layout, no combine pass.
+//
+// What is computed, for token t with ids e_j = topk_idx[t, j]:
+//   a_j    = silu(G[e_j] x_t) * (U[e_j] x_t)
+//   out[t] = sum over j (ascending) of w[t, j] * (D[e_j] a_j)
+// with W1 = [G; U] and W2 = D in bf16, MXFP8 or MXFP4, x and out in bf16.
+//
+// With few tokens every used expert's weights are read for a handful of
+// rows, so the weights' bytes bound the time.  A workgroup owns (a used
+// expert, a block of 32-row weight groups); its waves split the reduction
+// axis, each streaming its own weight fragments from memory straight into
+// registers, and the waves' partial tiles are summed through LDS in a fixed
+// order.  Weight codes become bf16 in registers (exactly: a power-of-two scale times
+// at most 4 significant bits) and are the A operand of the bf16 matrix
+// cores, up to 32 of the expert's tokens the B operand; sums are float32.
+//
+// Launch 1 ends in SwiGLU and keeps a_j as bf16 rows.  Launch 2 leaves its
+// float32 rows D a_j in the workspace, and the last workgroup to finish a
+// block of output columns (a counter per block, cleared by launch 1) sums
+// them over j in ascending order: the result does not depend on which
+// workgroup that is.
+#include <math.h>
+
+#include "common.hpp"
+#include "formats.hpp"
+#include "moe_layer.hpp"
+
+namespace ep {
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * kWave;
+constexpr int kTile = 32;                         // tokens per pass over an expert's weights
+
+// ---------------------------------------------------------------- packing
+//
+// The fragment order of the MXFP8 packing (see ep_moe_pack_weights) for
+// every weight type: lane l = 32g + r of a fragment holds, of the group's
+// row r, K [16g, 16g + 16) and [32 + 16g, 48 + 16g) of the 64-wide step.  A
+// fragment is 1, 2 or 4 KB (4, 8 or 16 bits a weight) in planes of 1 KB:
+// lane l's 16-byte piece p lies at 1024 p + 16 l.
+__host__ __device__ inline int group_row(int j, int r, int gate_up, int inter) {
+  return gate_up ? (r < 16 ? 16 * j + r : inter + 16 * j + (r - 16)) : 32 * j + r;
+}
+
+template <int Q>
+__global__ void pack_kernel(const uint8_t *__restrict__ w, const uint8_t *__restrict__ scales, int E, int N, int K,
+                            int gate_up, uint8_t *__restrict__ pw, uint8_t *__restrict__ ps) {
+  constexpr int kPieces = fragment_bytes(Q) / 1024;
+  const int ksteps = K / 64, spans = (ksteps + 3) / 4, groups = N / 32, kb = K / 32, inter = N / 2;
+  const int64_t row_bytes = Q == EP_QUANT_NONE ? 2 * (int64_t)K : Q == EP_QUANT_MXFP8 ? (int64_t)K : K / 2;
+  const int64_t pieces = (int64_t)E * groups * ksteps * kPieces * 64;
+  const int64_t first = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = first; i < pieces; i += stride) {
+    const int lane = (int)(i & 63), p = (int)((i >> 6) % kPieces);
+    const int64_t rest = (i >> 6) / kPieces;
+    const int s = (int)(rest % ksteps);
+    const int64_t eg = rest / ksteps;
+    const int j = (int)(eg % groups), e = (int)(eg / groups);
+    const int r = lane & 31, g = lane >> 5;
+    const uint8_t *row = w + ((int64_t)e * N + group_row(j, r, gate_up, inter)) * row_bytes;
+    u32x4 v;
+    if constexpr (Q == EP_QUANT_NONE) {
+      v = *(const u32x4 *)(row + 2 * (s * 64 + (p >> 1) * 32 + g * 16 + (p & 1) * 8));
+    } else if constexpr (Q == EP_QUANT_MXFP8) {
+      v = *(const u32x4 *)(row + s * 64 + p * 32 + g * 16);
+    } else {
+      const uint32_t *lo = (const uint32_t *)(row + s * 32 + g * 8), *hi = lo + 4;
+      v = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+    *(u32x4 *)(pw + ((((int64_t)s * E * groups + eg) * kPieces + p) * 64 + lane) * 16) = v;
+  }
+  if constexpr (Q != EP_QUANT_NONE) {
+    const int64_t words = (int64_t)E * groups * spans * 64;
+    for (int64_t i = first; i < words; i += stride) {
+      const int lane = (int)(i & 63);
+      const int64_t rest = i >> 6;
+      const int t = (int)(rest % spans);
+      const int64_t eg = rest / spans;
+      const int j = (int)(eg % groups), e = (int)(eg / groups);
+      const int r = lane & 31, g = lane >> 5;
+      const uint8_t *row = scales + ((int64_t)e * N + group_row(j, r, gate_up, inter)) * kb;
+      uint32_t word = 0;
+      for (int u = 0; u < 4; ++u)
+        if (4 * t + u < ksteps) word |= (uint32_t)row[(4 * t + u) * 2 + g] << (8 * u);
+      *(uint32_t *)(ps + (((int64_t)t * E * groups + eg) * 64 + lane) * 4) = word;
+    }
+  }
+}
+
+// ------------------------------------------------------ rows of an expert
+
+struct Rows {
+  int used;                                       // experts in use
+  int expert, n;                                  // the unit's expert (-1: none) and its pairs
+};
+
+// The `rank`-th expert in use (ascending id) and its pairs in ascending
+// order, into `list`; every thread of the workgroup takes part.
+template <typename IdxT>
+__device__ __forceinline__ Rows find_rows(const IdxT *__restrict__ idx, int P, int E, int rank, uint16_t *list) {
+  constexpr int kIter = (int)(kLayerMaxPairs / kThreads);
+  __shared__ uint32_t s_used[kMaxExperts / 32];
+  __shared__ int s_cnt[kIter * kWaves];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+  int id[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int p = i * kThreads + tid;
+    const int64_t v = p < P ? (int64_t)idx[p] : -1;
+    id[i] = v >= 0 && v < E ? (int)v : -1;
+  }
+  if (tid < kMaxExperts / 32) s_used[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kIter; ++i)
+    if (id[i] >= 0) atomicOr(&s_used[id[i] >> 5], 1u << (id[i] & 31));
+  __syncthreads();
+  Rows r;
+  r.used = 0;
+  r.expert = -1;
+  r.n = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    uint32_t bits = s_used[w];
+    const int c = __popc(bits);
+    if (rank >= r.used && rank < r.used + c) {
+      for (int d = rank - r.used; d > 0; --d) bits &= bits - 1;
+      r.expert = w * 32 + __ffs(bits) - 1;
+    }
+    r.used += c;
+  }
+  if (r.expert < 0) return r;
+  uint64_t bal[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    bal[i] = __ballot(id[i] == r.expert);
+    if (lane == 0) s_cnt[i * kWaves + wv] = __popcll(bal[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    int before = 0;
+    for (int j = 0; j < kIter * kWaves; ++j) before += j < i * kWaves + wv ? s_cnt[j] : 0;
+    if (id[i] == r.expert) list[before + __popcll(bal[i] & ((1ull << lane) - 1ull))] = (uint16_t)(i * kThreads + tid);
+  }
+  for (int j = 0; j < kIter * kWaves; ++j) r.n += s_cnt[j];
+  __syncthreads();
+  return r;
+}
+
+// -------------------------------------------------------------- fragments
+
+template <int Q>
+struct Frag {
+  u32x4 p[fragment_bytes(Q) / 1024];
+  uint32_t scale;                                 // span dword of this lane's K-block parity
+};
+
+// The four bf16 A operands of a fragment: operand m covers K (m >> 1) * 32 +
+// 16 g + (m & 1) * 8 .. + 8 of the step.  `u`: the step's byte of the span.
+template <int Q>
+__device__ __forceinline__ void operands(const Frag<Q> &f, int u, bf16x8 (&a)[4]) {
+  if constexpr (Q == EP_QUANT_NONE) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) a[m] = __builtin_bit_cast(bf16x8, f.p[m]);
+  } else {
+    // lane (r, g) holds the scales of K-blocks g: swapping the halves gives
+    // both blocks' scales to every lane
+    const auto both = __builtin_amdgcn_permlane32_swap(f.scale, f.scale, false, false);
+    const float s0 = e8m0_decode((both[0] >> (8 * u)) & 0xff), s1 = e8m0_decode((both[1] >> (8 * u)) & 0xff);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float s = m < 2 ? s0 : s1;
+      bf16x2 v0, v1, v2, v3;
+      if constexpr (Q == EP_QUANT_MXFP8) {
+        const uint32_t lo = f.p[m >> 1][2 * (m & 1)], hi = f.p[m >> 1][2 * (m & 1) + 1];
+        v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
+        v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
+        v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
+        v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+      } else {
+        const uint32_t w = f.p[0][m];
+        v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+        v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+        v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+        v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+      }
+      a[m] = bf16x8{v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
+    }
+  }
+}
+
+// Partial products of this wave's share [s0, s1) of the K steps: NG weight
+// groups from `wp` (fragments of one step: groups, then lanes) times the
+// lane's activation row `b` (K bf16 values).
+template <int Q, int NG>
+__device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const uint8_t *sp, size_t sspan,
+                                        const uint16_t *b, int s0, int s1, v16f (&acc)[NG]) {
+  constexpr int kPieces = fragment_bytes(Q) / 1024;
+  constexpr int kRing = 2;
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 5;
+#pragma unroll
+  for (int q = 0; q < NG; ++q) acc[q] = v16f{};
+  if (s0 >= s1) return;                           // uniform
+  Frag<Q> w[kRing][NG];
+  u32x4 bv[kRing][4];
+  auto load = [&](int slot, int s) {
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        w[slot][q].p[p] = __builtin_nontemporal_load(
+            (const u32x4 *)(wp + s * wstep + (size_t)q * fragment_bytes(Q) + p * 1024 + lane * 16));
+      if constexpr (Q != EP_QUANT_NONE)
+        w[slot][q].scale = *(const uint32_t *)(sp + (size_t)(s >> 2) * sspan + q * 256 + lane * 4);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      bv[slot][m] = *(const u32x4 *)(b + (size_t)s * 64 + (m >> 1) * 32 + g * 16 + (m & 1) * 8);
+  };
+#pragma unroll
+  for (int r = 0; r < kRing; ++r) load(r, min(s0 + r, s1 - 1));
+  for (int s = s0; s < s1; s += kRing) {
+#pragma unroll
+    for (int r = 0; r < kRing; ++r) {
+      if (s + r < s1) {                           // uniform
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          bf16x8 a[4];
+          operands<Q>(w[r][q], (s + r) & 3, a);
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m], __builtin_bit_cast(bf16x8, bv[r][m]), acc[q], 0, 0,
+                                                             0);
+        }
+      }
+      load(r, min(s + r + kRing, s1 - 1));        // past the end: the last step again, never used
+    }
+  }
+}
+
+// The waves' partial tiles through LDS: [wave][group][quad of registers][lane][4].
+template <int NG>
+__device__ __forceinline__ void leave_partials(float *tile, const v16f (&acc)[NG]) {
+  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+  f32x4 *to = (f32x4 *)tile + (size_t)wv * NG * 4 * kWave + lane;
+#pragma unroll
+  for (int q = 0; q < NG; ++q)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      to[(q * 4 + b) * kWave] = f32x4{acc[q][4 * b], acc[q][4 * b + 1], acc[q][4 * b + 2], acc[q][4 * b + 3]};
+}
+template <int NG>
+__device__ __forceinline__ f32x4 summed(const float *tile, int q, int b, int lane) {
+  const f32x4 *from = (const f32x4 *)tile + (q * 4 + b) * kWave + lane;
+  f32x4 v = from[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) v += from[(size_t)w * NG * 4 * kWave];
+  return v;
+}
+
+__device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
+
+// Launch 1: act[p] = silu(G x) * (U x) of every pair p; NG groups of 16
+// gate and 16 up rows per workgroup.
+template <int Q, int NG, typename IdxT>
+__global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerArgs a, uint16_t *__restrict__ act,
+                                                            uint32_t *__restrict__ done, int blocks) {
+  __shared__ uint16_t s_list[kLayerMaxPairs];
+  __shared__ __attribute__((aligned(16))) float s_tile[kWaves * NG * 16 * kWave];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < a.hidden / 32; i += kThreads) done[i] = 0;
+  const int blk = blockIdx.x % blocks;
+  const Rows rows = find_rows((const IdxT *)a.idx, (int)a.T * a.k, a.E, blockIdx.x / blocks, s_list);
+  if (rows.expert < 0) return;                    // uniform
+  const int K = a.hidden, ksteps = K / 64, groups = a.inter / 16;
+  const int g0 = min(blk * NG, groups - NG);      // a partial last block repeats groups of the one before
+  const size_t gidx = (size_t)rows.expert * groups + g0;
+  const int s0 = ksteps * wv / kWaves, s1 = ksteps * (wv + 1) / kWaves;
+  for (int r0 = 0; r0 < rows.n; r0 += kTile) {
+    const int n = min(kTile, rows.n - r0);
+    const uint16_t *b = (const uint16_t *)a.x + (size_t)(s_list[r0 + min(lane & 31, n - 1)] / a.k) * K;
+    v16f acc[NG];
+    product<Q, NG>(a.w1 + gidx * fragment_bytes(Q), (size_t)a.E * groups * fragment_bytes(Q), a.w1_scales + gidx * 256,
+                   (size_t)a.E * groups * 256, b, s0, s1, acc);
+    if (r0 > 0) __syncthreads();
+    leave_partials<NG>(s_tile, acc);
+    __syncthreads();
+    // lane l of quad b holds column l % 32, rows 8b + 4 (l / 32) + 0..3: quads
+    // 0 and 1 are gate rows, 2 and 3 the same up rows
+    for (int job = tid; job < NG * 2 * kWave; job += kThreads) {
+      const int l = job & 63, qb = job >> 6, q = qb >> 1, h = qb & 1;
+      const int c = l & 31;
+      if (c >= n) continue;
+      const f32x4 gate = summed<NG>(s_tile, q, h, l), up = summed<NG>(s_tile, q, h + 2, l);
+      const u32x2 v = {pack_bf16x2(silu(gate.x) * up.x, silu(gate.y) * up.y),
+                       pack_bf16x2(silu(gate.z) * up.z, silu(gate.w) * up.w)};
+      *(u32x2 *)(act + (size_t)s_list[r0 + c] * a.inter + 16 * (g0 + q) + 8 * h + 4 * (l >> 5)) = v;
+    }
+  }
+}
+
+// Launch 2: y[p] = D act[p], then out[t] = sum_j w y[t k + j] by the last
+// workgroup of each block of 32 NG columns.
+template <int Q, int NG, typename IdxT>
+__global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const uint16_t *__restrict__ act, float *y,
+                                                              uint32_t *done, int blocks) {
+  __shared__ uint16_t s_list[kLayerMaxPairs];
+  __shared__ __attribute__((aligned(16))) float s_tile[kWaves * NG * 16 * kWave];
+  __shared__ uint32_t s_last;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+  const int blk = blockIdx.x % blocks, rank = blockIdx.x / blocks;
+  const int P = (int)a.T * a.k;
+  const Rows rows = find_rows((const IdxT *)a.idx, P, a.E, rank, s_list);
+  if (rows.expert < 0 && !(rank == 0 && rows.used == 0)) return;   // uniform
+  const int K = a.inter, ksteps = K / 64, groups = a.hidden / 32;
+  const int g0 = min(blk * NG, groups - NG);
+  if (rows.expert >= 0) {
+    const size_t gidx = (size_t)rows.expert * groups + g0;
+    const int s0 = ksteps * wv / kWaves, s1 = ksteps * (wv + 1) / kWaves;
+    for (int r0 = 0; r0 < rows.n; r0 += kTile) {
+      const int n = min(kTile, rows.n - r0);
+      const uint16_t *b = act + (size_t)s_list[r0 + min(lane & 31, n - 1)] * K;
+      v16f acc[NG];
+      product<Q, NG>(a.w2 + gidx * fragment_bytes(Q), (size_t)a.E * groups * fragment_bytes(Q),
+                     a.w2_scales + gidx * 256, (size_t)a.E * groups * 256, b, s0, s1, acc);
+      if (r0 > 0) __syncthreads();
+      leave_partials<NG>(s_tile, acc);
+      __syncthreads();
+      for (int job = tid; job < NG * 4 * kWave; job += kThreads) {
+        const int l = job & 63, qb = job >> 6, q = qb >> 2, h = qb & 3;
+        const int c = l & 31;
+        if (c >= n) continue;
+        const f32x4 v = summed<NG>(s_tile, q, h, l);
+        // agent scope: read by a workgroup that may sit on another die
+        float *to = y + (size_t)s_list[r0 + c] * a.hidden + 32 * (g0 + q) + 8 * h + 4 * (l >> 5);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __hip_atomic_store(to + i, v[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0)
+      s_last = __hip_atomic_fetch_add(done + blk, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+               (uint32_t)rows.used - 1;
+    __syncthreads();
+    if (!s_last) return;
+  }
+  // out[t] over the block's columns, two per thread
+  constexpr int kPairs = 16 * NG;
+  const IdxT *idx = (const IdxT *)a.idx;
+  for (int job = tid; job < (int)a.T * kPairs; job += kThreads) {
+    const int t = job / kPairs, c = 32 * g0 + 2 * (job - t * kPairs);
+    float o0 = 0.0f, o1 = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t e = (int64_t)idx[t * a.k + j];
+      if (e < 0 || e >= a.E) continue;
+      float *from = y + (size_t)(t * a.k + j) * a.hidden + c;
+      const float w = a.weights[t * a.k + j];
+      o0 += w * __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      o1 += w * __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    *(uint32_t *)((uint16_t *)a.out + (size_t)t * a.hidden + c) = pack_bf16x2(o0, o1);
+  }
+}
+
+template <int Q, int NG, typename IdxT>
+hipError_t layer_launch(const LayerArgs &a, hipStream_t s) {
+  const LayerWs ws = layer_ws(a.T, a.k, a.hidden, a.inter);
+  uint16_t *act = (uint16_t *)(a.ws + ws.act);
+  float *y = (float *)(a.ws + ws.y);
+  uint32_t *done = (uint32_t *)(a.ws + ws.done);
+  const int64_t P = a.T * a.k, used = P < a.E ? P : a.E;
+  const int up_blocks = (a.inter / 16 + NG - 1) / NG, down_blocks = (a.hidden / 32 + NG - 1) / NG;
+  hipLaunchKernelGGL((layer_up_kernel<Q, NG, IdxT>), dim3((unsigned)(used * up_blocks)), dim3(kThreads), 0, s, a, act,
+                     done, up_blocks);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((layer_down_kernel<Q, NG, IdxT>), dim3((unsigned)(used * down_blocks)), dim3(kThreads), 0, s, a,
+                     act, y, done, down_blocks);
+  return hipGetLastError();
+}
+template <int Q>
+hipError_t layer_q(const LayerArgs &a, hipStream_t s) {
+  return a.idx64 ? layer_launch<Q, 2, int64_t>(a, s) : layer_launch<Q, 2, int32_t>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_moe_layer(const LayerArgs &a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  switch (a.quant) {
+    case EP_QUANT_NONE: return layer_q<EP_QUANT_NONE>(a, s);
+    case EP_QUANT_MXFP8: return layer_q<EP_QUANT_MXFP8>(a, s);
+    default: return layer_q<EP_QUANT_MXFP4>(a, s);
+  }
+}
+
+hipError_t launch_pack_ex(const void *w, const void *scales, int quant, int E, int N, int K, int gate_up, void *pw,
+                          void *pscales, hipStream_t s) {
+  const uint8_t *from = (const uint8_t *)w, *sc = (const uint8_t *)scales;
+  uint8_t *to = (uint8_t *)pw, *tos = (uint8_t *)pscales;
+  const dim3 grid(2048), block(256);
+  switch (quant) {
+    case EP_QUANT_NONE:
+      hipLaunchKernelGGL(pack_kernel<EP_QUANT_NONE>, grid, block, 0, s, from, sc, E, N, K, gate_up, to, tos);
+      break;
+    case EP_QUANT_MXFP8:
+      hipLaunchKernelGGL(pack_kernel<EP_QUANT_MXFP8>, grid, block, 0, s, from, sc, E, N, K, gate_up, to, tos);
+      break;
+    default:
+      hipLaunchKernelGGL(pack_kernel<EP_QUANT_MXFP4>, grid, block, 0, s, from, sc, E, N, K, gate_up, to, tos);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace ep

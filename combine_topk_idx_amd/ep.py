@@ -5,7 +5,10 @@ The functions ``ep_workspace_bytes``, ``ep_workspace_bytes_ex``,
 ``ep_dispatch``, ``ep_layout_dispatch``, ``ep_layout_dispatch_noalloc``,
 ``ep_combine``, ``ep_combine_backward``,
 ``ep_moe_packed_bytes``, ``ep_moe_pack_weights``, ``ep_moe_gmm1``,
-``ep_moe_gmm2``, ``ep_read_status``,
+``ep_moe_gmm2``, ``ep_moe_packed_bytes_ex``, ``ep_moe_pack_weights_ex``,
+``ep_moe_layer_workspace_bytes``, ``ep_moe_layer``, ``ep_router``,
+``ep_router_backward``, ``ep_lora_workspace_bytes``, ``ep_lora``,
+``ep_lora_backward``, ``ep_read_status``,
 ``ep_last_error`` and ``ep_abi_version`` have the names and arguments of the C ABI in
 ``include/ep.h``; torch tensors stand in for device pointers and torch's
 current stream is used unless one is passed.  Every computation runs in the
@@ -20,6 +23,7 @@ the same entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -38,6 +42,8 @@ EP_IDX_INT32, EP_IDX_INT64 = 0, 1
 QUANT = {"none": 0, "int8_token": 1, "fp8_b128": 2, "mxfp8": 3, "mxfp4": 4, "fp8_b128_pow2": 5,
          "fp8_b128_ue8m0": 6}
 EP_RECV_INTERLEAVED = 0x100
+SCORE = {"softmax": 0, "sigmoid": 1}
+_FLOAT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 EP_STATUS_ID_OUT_OF_RANGE = 1
 EP_STATUS_CAPACITY_OVERFLOW = 2
 EP_STATUS_COMBINE_MISMATCH = 4
@@ -45,6 +51,8 @@ EP_STATUS_COMBINE_MISMATCH = 4
 SYMBOLS = ("ep_workspace_bytes", "ep_workspace_bytes_ex", "ep_layout_rows", "ep_buffer_bytes", "ep_layout",
            "ep_layout_ex", "ep_dispatch", "ep_layout_dispatch", "ep_layout_dispatch_noalloc", "ep_combine",
            "ep_combine_backward", "ep_moe_packed_bytes", "ep_moe_pack_weights", "ep_moe_gmm1", "ep_moe_gmm2",
+           "ep_moe_packed_bytes_ex", "ep_moe_pack_weights_ex", "ep_moe_layer_workspace_bytes", "ep_moe_layer",
+           "ep_router", "ep_router_backward", "ep_lora_workspace_bytes", "ep_lora", "ep_lora_backward",
            "ep_read_status", "ep_last_error", "ep_abi_version")
 STATIC_WORKSPACE_BYTES = 4 << 20   # the static workspace of ep_layout_dispatch_noalloc
 
@@ -103,6 +111,28 @@ _lib.ep_moe_gmm1.argtypes = [ctypes.POINTER(ep_handle_t), _vp, _vp, _sz, _i32, _
 _lib.ep_moe_gmm1.restype = ctypes.c_int
 _lib.ep_moe_gmm2.argtypes = [ctypes.POINTER(ep_handle_t), _vp, _vp, _sz, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
 _lib.ep_moe_gmm2.restype = ctypes.c_int
+_szp, _f32, _int = ctypes.POINTER(_sz), ctypes.c_float, ctypes.c_int
+_hp = ctypes.POINTER(ep_handle_t)
+_lib.ep_moe_packed_bytes_ex.argtypes = [_i32, _i32, _i32, _int, _szp, _szp]
+_lib.ep_moe_packed_bytes_ex.restype = _int
+_lib.ep_moe_pack_weights_ex.argtypes = [_vp, _vp, _i32, _i32, _i32, _int, _i32, _vp, _vp, _vp]
+_lib.ep_moe_pack_weights_ex.restype = _int
+_lib.ep_moe_layer_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
+_lib.ep_moe_layer_workspace_bytes.restype = _sz
+_lib.ep_moe_layer.argtypes = [_vp, _i64, _i32, _vp, _int, _vp, _i32, _i32, _i32, _int, _vp, _vp, _vp, _vp, _vp, _sz,
+                              _vp, _vp]
+_lib.ep_moe_layer.restype = _int
+_lib.ep_router.argtypes = [_vp, _int, _i64, _i32, _i32, _int, _vp, _i32, _i32, _i32, _i32, _f32, _vp, _int, _vp, _vp]
+_lib.ep_router.restype = _int
+_lib.ep_router_backward.argtypes = [_vp, _int, _i64, _i32, _i32, _int, _i32, _f32, _vp, _int, _vp, _vp, _vp]
+_lib.ep_router_backward.restype = _int
+_lib.ep_lora_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32]
+_lib.ep_lora_workspace_bytes.restype = _sz
+_lib.ep_lora.argtypes = [_hp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.ep_lora.restype = _int
+_lib.ep_lora_backward.argtypes = [_hp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                  _vp]
+_lib.ep_lora_backward.restype = _int
 _lib.ep_read_status.argtypes = [ctypes.POINTER(ep_handle_t), ctypes.POINTER(ctypes.c_uint32), _vp]
 _lib.ep_read_status.restype = ctypes.c_int
 _lib.ep_last_error.argtypes = []
@@ -381,9 +411,14 @@ def ep_moe_pack_weights(codes, scales, num_experts: int, rows: int, k: int, gate
                                     _ptr(packed_scales), _stream(stream)))
 
 
-def pack_moe_weights(codes, scales, gate_up: bool, *, stream=None):
+def pack_moe_weights(codes, scales, gate_up: bool, *, quant="mxfp8", stream=None):
     """Device tensors codes [E, N, K] uint8 and scales [E, N, K/32] uint8 ->
-    (packed codes, packed scales) uint8 device tensors."""
+    (packed codes, packed scales) uint8 device tensors.  With ``quant``
+    "mxfp4" (codes [E, N, K/2] uint8) or "none" (bf16 [E, N, K], scales None):
+    the packed weights ep_moe_layer takes; packed bf16 weights have no scales
+    (None)."""
+    if quant != "mxfp8":
+        return _pack_moe_weights_ex(codes, scales, gate_up, quant, stream)
     E, N, K = codes.shape
     cb, sb = ep_moe_packed_bytes(E, N, K)
     pc = torch.empty(cb, dtype=torch.uint8, device=codes.device)
@@ -427,6 +462,175 @@ def ep_moe_gmm2(handle: ep_handle_t, a_buf, inter: int, hidden: int, w2, w2_scal
                             _nbytes(a_buf) if a_buf_bytes is None else a_buf_bytes, inter, hidden, _ptr(w2),
                             _ptr(w2_scales), _ptr(out_buf), _nbytes(out_buf) if out_buf_bytes is None else out_buf_bytes,
                             _stream(stream)))
+
+
+def ep_moe_packed_bytes_ex(num_experts: int, rows: int, k: int, quant) -> tuple[int, int]:
+    c, sc = _sz(0), _sz(0)
+    _check(_lib.ep_moe_packed_bytes_ex(num_experts, rows, k, _quant(quant), ctypes.byref(c), ctypes.byref(sc)))
+    return c.value, sc.value
+
+
+def ep_moe_pack_weights_ex(weights, scales, num_experts: int, rows: int, k: int, quant, gate_up: bool,
+                           packed_weights, packed_scales, *, stream=None) -> None:
+    q = _quant(quant)
+    wb, sb = ep_moe_packed_bytes_ex(num_experts, rows, k, q)
+    dtype, width = (torch.bfloat16, k) if q == QUANT["none"] else (torch.uint8, k if q == QUANT["mxfp8"] else k // 2)
+    specs = [(weights, "weights", dtype, (num_experts, rows, width), None),
+             (packed_weights, "packed_weights", torch.uint8, (wb,), None)]
+    if sb:
+        specs += [(scales, "scales", torch.uint8, (num_experts, rows, k // 32), None),
+                  (packed_scales, "packed_scales", torch.uint8, (sb,), None)]
+    _check_here(*specs)
+    _check(_lib.ep_moe_pack_weights_ex(_ptr(weights), _ptr(scales), num_experts, rows, k, q, int(gate_up),
+                                       _ptr(packed_weights), _ptr(packed_scales), _stream(stream)))
+
+
+def _pack_moe_weights_ex(weights, scales, gate_up, quant, stream):
+    E, N, K = weights.shape
+    if _quant(quant) == QUANT["mxfp4"]:
+        K *= 2
+    wb, sb = ep_moe_packed_bytes_ex(E, N, K, quant)
+    pw = torch.empty(wb, dtype=torch.uint8, device=weights.device)
+    ps = torch.empty(sb, dtype=torch.uint8, device=weights.device) if sb else None
+    ep_moe_pack_weights_ex(weights, scales, E, N, K, quant, gate_up, pw, ps, stream=stream)
+    return pw, ps
+
+
+def _check_here(*specs) -> None:
+    """_check_args, and that the tensors' GPU is the current one (whose
+    stream the launch goes to)."""
+    _check_args(*specs)
+    for t, name, *_ in specs:
+        if isinstance(t, torch.Tensor):
+            if t.get_device() != torch.cuda.current_device():
+                raise EpError(EP_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current device")
+            return
+
+
+def ep_moe_layer_workspace_bytes(num_tokens: int, num_topk: int, num_experts: int, hidden: int, inter: int) -> int:
+    return _lib.ep_moe_layer_workspace_bytes(num_tokens, num_topk, num_experts, hidden, inter)
+
+
+def ep_moe_layer(x, topk_idx, topk_weights, num_experts: int, inter: int, w_quant, w1, w1_scales, w2, w2_scales,
+                 workspace, out, *, stream=None) -> None:
+    """The whole expert layer for a few tokens (num_tokens * num_topk <= 2048)
+    in two launches.  x, out: bf16 [T, H]; the weights as pack_moe_weights
+    returns them for ``w_quant`` ("none", "mxfp8" or "mxfp4")."""
+    num_tokens, num_topk, idx_dtype = _idx_args(topk_idx, None, None, None)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise EpError(EP_ERR_INVALID_ARG, "x must be a [num_tokens, hidden] tensor")
+    hidden, q = x.shape[1], _quant(w_quant)
+    try:
+        (b1, s1), (b2, s2) = _layer_weight_bytes(num_experts, hidden, inter, q)
+    except EpError:                                    # shapes the library rejects with its own message
+        b1 = s1 = b2 = s2 = None
+    specs = [(x, "x", torch.bfloat16, (num_tokens, hidden), None), (topk_idx, "topk_idx", None, None, None),
+             (topk_weights, "topk_weights", torch.float32, (num_tokens, num_topk), None),
+             (w1, "w1", torch.uint8, b1 and (b1,), None), (w2, "w2", torch.uint8, b2 and (b2,), None),
+             (workspace, "workspace", None, None, None), (out, "out", torch.bfloat16, (num_tokens, hidden), None)]
+    if s1:
+        specs += [(w1_scales, "w1_scales", torch.uint8, (s1,), None), (w2_scales, "w2_scales", torch.uint8, (s2,), None)]
+    _check_here(*specs)
+    _check(_lib.ep_moe_layer(_ptr(x), num_tokens, hidden, _ptr(topk_idx), idx_dtype, _ptr(topk_weights), num_topk,
+                             num_experts, inter, q, _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales),
+                             _ptr(workspace), _nbytes(workspace), _ptr(out), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=64)
+def _layer_weight_bytes(num_experts, hidden, inter, q):
+    return (ep_moe_packed_bytes_ex(num_experts, 2 * inter, hidden, q),
+            ep_moe_packed_bytes_ex(num_experts, hidden, inter, q))
+
+
+def _score(score) -> int:
+    if isinstance(score, str):
+        if score not in SCORE:
+            raise EpError(EP_ERR_INVALID_ARG, f"unknown score {score!r}")
+        return SCORE[score]
+    return int(score)
+
+
+def _router_args(logits, topk_idx, topk_weights, name, extra):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in _FLOAT:
+        raise EpError(EP_ERR_INVALID_ARG, "logits must be a float32, bfloat16 or float16 [num_tokens, num_experts] tensor")
+    T, E = logits.shape
+    n, k, idx_dtype = _idx_args(topk_idx, None, None, None)
+    if n != T:
+        raise EpError(EP_ERR_INVALID_ARG, f"topk_idx must have {T} rows (got {n})")
+    _check_here((logits, "logits", None, None, None), (topk_idx, "topk_idx", None, None, None),
+                (topk_weights, name, torch.float32, (T, k), None), extra)
+    return T, E, k, idx_dtype
+
+
+def ep_router(logits, topk_idx, topk_weights, *, score="softmax", bias=None, num_groups: int = 1,
+              topk_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+              stream=None) -> None:
+    """Writes topk_idx [T, k] (int32 / int64) and topk_weights (float32 [T, k])
+    from the logits [T, E] (float32, bf16 or fp16)."""
+    E = logits.shape[-1] if isinstance(logits, torch.Tensor) and logits.dim() else 0
+    T, E, k, idx_dtype = _router_args(logits, topk_idx, topk_weights, "topk_weights",
+                                      (bias, "bias", torch.float32, (E,), None))
+    _check(_lib.ep_router(_ptr(logits), _FLOAT[logits.dtype], T, E, k, _score(score), _ptr(bias), num_groups,
+                          topk_groups, group_top, int(bool(renormalize)), scale, _ptr(topk_idx), idx_dtype,
+                          _ptr(topk_weights), _stream(stream)))
+
+
+def ep_router_backward(logits, topk_idx, grad_weights, grad_logits, *, score="softmax", renormalize: bool = True,
+                       scale: float = 1.0, stream=None) -> None:
+    """Writes grad_logits (the logits' shape and dtype) from the gradient of
+    ep_router's topk_weights; score, renormalize and scale as given there."""
+    like = (logits.dtype, tuple(logits.shape)) if isinstance(logits, torch.Tensor) else (None, None)
+    T, E, k, idx_dtype = _router_args(logits, topk_idx, grad_weights, "grad_weights",
+                                      (grad_logits, "grad_logits", *like, None))
+    _check(_lib.ep_router_backward(_ptr(logits), _FLOAT[logits.dtype], T, E, k, _score(score), int(bool(renormalize)),
+                                   scale, _ptr(topk_idx), idx_dtype, _ptr(grad_weights), _ptr(grad_logits),
+                                   _stream(stream)))
+
+
+def ep_lora_workspace_bytes(num_max_tokens: int, in_features: int, out_features: int, rank: int, num_adapters: int,
+                            backward: bool = False) -> int:
+    return _lib.ep_lora_workspace_bytes(num_max_tokens, in_features, out_features, rank, num_adapters,
+                                        int(bool(backward)))
+
+
+def _lora_shapes(handle, a, b):
+    if not (isinstance(a, torch.Tensor) and isinstance(b, torch.Tensor) and a.dim() == 3 and b.dim() == 3):
+        raise EpError(EP_ERR_INVALID_ARG, "a and b must be [num_adapters, rank, in] and [num_adapters, out, rank] tensors")
+    N, rank, fin = a.shape
+    if N != handle.num_experts:
+        raise EpError(EP_ERR_INVALID_ARG, f"a holds {N} adapters, the layout {handle.num_experts}")
+    return handle.num_tokens, N, rank, fin, b.shape[1]
+
+
+def ep_lora(handle: ep_handle_t, x, a, b, out, down, workspace, *, scale=None, base=None, stream=None) -> None:
+    """out[t] = base[t] + scale[e] * B[e] (A[e] x[t]) for the adapter e of each
+    token in the layout ``handle`` (of [T, 1] adapter ids).  x, base, out:
+    bf16 rows; a [N, rank, in], b [N, out, rank] bf16; scale float32 [N];
+    down float32 [T, rank] (kept for ep_lora_backward).  base may be out."""
+    T, N, rank, fin, fout = _lora_shapes(handle, a, b)
+    bf = torch.bfloat16
+    _check_here((x, "x", bf, (T, fin), None), (a, "a", bf, None, None), (b, "b", bf, (N, fout, rank), None),
+                (out, "out", bf, (T, fout), None), (down, "down", torch.float32, (T, rank), None),
+                (workspace, "workspace", None, None, None), (scale, "scale", torch.float32, (N,), None),
+                (base, "base", bf, (T, fout), None))
+    _check(_lib.ep_lora(ctypes.byref(handle), _ptr(x), fin, fout, rank, _ptr(a), _ptr(b), _ptr(scale), _ptr(base),
+                        _ptr(out), _ptr(down), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def ep_lora_backward(handle: ep_handle_t, grad_out, x, a, b, down, grad_x, grad_a, grad_b, workspace, *, scale=None,
+                     grad_base=None, stream=None) -> None:
+    """Gradients of ep_lora: grad_x (bf16, plus grad_base if given, which may
+    be grad_x), grad_a and grad_b (float32, the shapes of a and b)."""
+    T, N, rank, fin, fout = _lora_shapes(handle, a, b)
+    bf, f32 = torch.bfloat16, torch.float32
+    _check_here((grad_out, "grad_out", bf, (T, fout), None), (x, "x", bf, (T, fin), None), (a, "a", bf, None, None),
+                (b, "b", bf, (N, fout, rank), None), (down, "down", f32, (T, rank), None),
+                (grad_x, "grad_x", bf, (T, fin), None), (grad_a, "grad_a", f32, (N, rank, fin), None),
+                (grad_b, "grad_b", f32, (N, fout, rank), None), (workspace, "workspace", None, None, None),
+                (scale, "scale", f32, (N,), None), (grad_base, "grad_base", bf, (T, fin), None))
+    _check(_lib.ep_lora_backward(ctypes.byref(handle), _ptr(grad_out), _ptr(x), fin, fout, rank, _ptr(a), _ptr(b),
+                                 _ptr(scale), _ptr(down), _ptr(grad_base), _ptr(grad_x), _ptr(grad_a), _ptr(grad_b),
+                                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def ep_read_status(handle: ep_handle_t, stream=None) -> int:

@@ -370,6 +370,133 @@ ep_status_t ep_moe_gmm2(const ep_handle_t *handle, const int64_t *recv_count, co
                         size_t a_buf_bytes, int32_t inter, int32_t hidden, const void *w2,
                         const void *w2_scales, void *out_buf, size_t out_buf_bytes, void *stream);
 
+/* Packed weights of every type the few-token layer takes: bf16
+ * (EP_QUANT_NONE; [E, N, K] bf16, no scales: pass NULL, scales_bytes is 0),
+ * MXFP8 (exactly ep_moe_pack_weights) or MXFP4 ([E, N, K/2] bytes, element
+ * 2i in the low nibble, and scales [E, N, K/32]).  The fragment order is that
+ * of ep_moe_pack_weights; lane l = 32g + r of a fragment holds the same K
+ * elements of row r in 1, 2 or 4 planes of 1 KB (16 bytes a lane).  Buffers are
+ * 16-byte aligned. */
+ep_status_t ep_moe_packed_bytes_ex(int32_t num_experts, int32_t rows, int32_t k, ep_quant_t quant,
+                                   size_t *weight_bytes, size_t *scales_bytes);
+ep_status_t ep_moe_pack_weights_ex(const void *weights, const void *scales, int32_t num_experts, int32_t rows,
+                                   int32_t k, ep_quant_t quant, int32_t gate_up, void *packed_weights,
+                                   void *packed_scales, void *stream);
+
+/* The whole expert layer for a few tokens, in two launches: dispatch, both
+ * expert products, SwiGLU and combine without receive rows (a decoding
+ * step's form of ep_layout_dispatch, ep_moe_gmm1, ep_moe_gmm2, ep_combine).
+ *   x             device bf16 [T, H], 16-byte aligned; not quantised
+ *   num_tokens    T >= 0, T * k <= 2048 (more pairs: EP_ERR_UNSUPPORTED, use
+ *                 the calls above)
+ *   hidden, inter H and I, positive multiples of 64
+ *   topk_idx      device [T, k]; -1 and ids outside [0, E) take no part; an
+ *                 id may repeat within a row
+ *   topk_weights  device float32 [T, k]
+ *   w_quant       EP_QUANT_NONE, EP_QUANT_MXFP8 or EP_QUANT_MXFP4
+ *   w1, w1_scales packed [E, 2I, H] (gate_up = 1); w2, w2_scales packed
+ *                 [E, H, I] (gate_up = 0); the scales NULL for bf16
+ *   workspace     device, 256-byte aligned, >= ep_moe_layer_workspace_bytes;
+ *                 in use until the call's work has ended, so calls that may
+ *                 overlap (other streams, graphs replayed at once) need their
+ *                 own.  Nothing is kept in it between calls.
+ *   out           device bf16 [T, H], 16-byte aligned; may not overlap x
+ * out[t] = bf16( sum over j ascending of w[t, j] * (W2[e] a) ), e =
+ * topk_idx[t, j], a = bf16(silu(g) * u), [g; u] = W1[e] x[t], with float32 sums;
+ * a token without a valid id gets +0.  A weight code times its scale is
+ * rounded to bf16, which is exact unless the product lies below 2^-126. */
+size_t ep_moe_layer_workspace_bytes(int64_t num_tokens, int32_t num_topk, int32_t num_experts, int32_t hidden,
+                                    int32_t inter);
+ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, const void *topk_idx,
+                         ep_idx_dtype_t idx_dtype, const float *topk_weights, int32_t num_topk,
+                         int32_t num_experts, int32_t inter, ep_quant_t w_quant, const void *w1,
+                         const void *w1_scales, const void *w2, const void *w2_scales, void *workspace,
+                         size_t workspace_bytes, void *out, void *stream);
+
+/* Router: the topk_idx and topk_weights of the calls above from the gate's
+ * logits.  For a row z of E logits:
+ *   s_e = softmax(z)_e or sigmoid(z_e); key_e = s_e + bias_e
+ *   num_groups > 1: the experts form groups of E / num_groups consecutive
+ *   ones; a group is ranked by its largest key (group_top = 1) or the sum of
+ *   its two largest (2), and only the topk_groups best groups (ties to the
+ *   lower group) are kept
+ *   topk_idx[t] = the k largest keys kept, descending, ties to the lower id
+ *   topk_weights[t, j] = scale * s_j, divided by the sum of the row's chosen
+ *   s when renormalize is set
+ * Without a bias the keys are the logits themselves (both scores rise with
+ * them).  Keys with a bias are compared as float64.  An expert whose logit
+ * or key is -inf or NaN is never chosen (+inf counts as the largest finite
+ * logit); a row that has fewer than k experts left gets -1 with weight 0 in its last places.
+ *   logits       device [T, E] of dtype, aligned to it
+ *   num_topk     0 < k <= 16, k <= E;  0 < E <= 512
+ *   bias         device float32 [E] or NULL
+ *   num_groups   divides E, <= 64; 0 < topk_groups <= num_groups; E / num_groups >= group_top
+ *   topk_idx     device [T, k] of idx_dtype, written
+ *   topk_weights device float32 [T, k], written */
+typedef enum { EP_FLOAT_F32 = 0, EP_FLOAT_BF16 = 1, EP_FLOAT_F16 = 2 } ep_float_t;
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
+ep_status_t ep_router(const void *logits, ep_float_t dtype, int64_t num_tokens, int32_t num_experts,
+                      int32_t num_topk, ep_score_t score, const float *bias, int32_t num_groups,
+                      int32_t topk_groups, int32_t group_top, int32_t renormalize, float scale, void *topk_idx,
+                      ep_idx_dtype_t idx_dtype, float *topk_weights, void *stream);
+
+/* Gradient of ep_router's weights with respect to the logits (the ids are
+ * constants, the bias has none).
+ *   topk_idx      device [T, k]: ep_router's ids (-1 and ids outside [0, E): no gradient)
+ *   grad_weights  device float32 [T, k]
+ *   grad_logits   device [T, E] of dtype, written in whole; may be logits'
+ *                 own memory only if it is not needed afterwards and not
+ *                 overlapped otherwise */
+ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num_tokens, int32_t num_experts,
+                               int32_t num_topk, ep_score_t score, int32_t renormalize, float scale,
+                               const void *topk_idx, ep_idx_dtype_t idx_dtype, const float *grad_weights,
+                               void *grad_logits, void *stream);
+
+/* Low-rank adapters of many requests beside a shared projection, grouped by
+ * a routing layout of the adapter ids (ep_layout of ids [T, 1]: -1 = no
+ * adapter; one layout serves every projection of a step).  For token t with
+ * adapter e:
+ *   down[t] = A[e] x[t]                        (float32 [rank])
+ *   out[t]  = bf16( base[t] + scale[e] * (B[e] down[t]) )
+ * and out[t] = base[t] for a token without one.
+ *   handle       host; num_topk must be 1, num_experts is the number of
+ *                adapters N; any of the row arrangements
+ *   x            device bf16 [T, in], out_features and in_features positive
+ *                multiples of 32
+ *   rank         a multiple of 8, 8 .. 128 (adapters of lower rank: zero rows)
+ *   a, b         device bf16 [N, rank, in] and [N, out, rank]
+ *   scale        device float32 [N] or NULL (1)
+ *   base         device bf16 [T, out] or NULL (0): the shared projection's
+ *                output; may be `out` itself
+ *   out          device bf16 [T, out]
+ *   down         device float32 [T, rank], written (rows without an adapter
+ *                are left as they were): ep_lora_backward takes it
+ *   workspace    device, 256-byte aligned, >= ep_lora_workspace_bytes; as for
+ *                ep_moe_layer
+ * All row buffers are 16-byte aligned. */
+size_t ep_lora_workspace_bytes(int64_t num_max_tokens, int32_t in_features, int32_t out_features, int32_t rank,
+                               int32_t num_adapters, int32_t backward);
+ep_status_t ep_lora(const ep_handle_t *handle, const void *x, int32_t in_features, int32_t out_features,
+                    int32_t rank, const void *a, const void *b, const float *scale, const void *base, void *out,
+                    float *down, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of ep_lora.  With u[t] = scale[e] * B[e]^T grad_out[t]:
+ *   grad_x[t] = bf16( grad_base[t] + A[e]^T u[t] )
+ *   grad_a[e] = sum over its tokens of u[t] x[t]^T             (float32)
+ *   grad_b[e] = scale[e] * sum of grad_out[t] down[t]^T        (float32)
+ * The gradient of base is grad_out itself.
+ *   grad_out     device bf16 [T, out];  down: ep_lora's
+ *   grad_base    device bf16 [T, in] or NULL (0): the gradient of x through
+ *                the shared projection; may be grad_x itself
+ *   grad_x       device bf16 [T, in];  grad_a float32 [N, rank, in]; grad_b
+ *                float32 [N, out, rank]: all written in whole (zeros for an
+ *                adapter without tokens)
+ *   workspace    >= ep_lora_workspace_bytes(..., backward = 1) */
+ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, const void *x, int32_t in_features,
+                             int32_t out_features, int32_t rank, const void *a, const void *b, const float *scale,
+                             const float *down, const void *grad_base, void *grad_x, float *grad_a, float *grad_b,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
 /* Waits for `stream` and copies the status word of `handle` (EP_STATUS_*
  * bits) to host *flags. */
 ep_status_t ep_read_status(const ep_handle_t *handle, uint32_t *flags, void *stream);
