@@ -514,7 +514,7 @@ size_t ep_moe_layer_workspace_bytes(int64_t num_tokens, int32_t num_topk, int32_
       num_experts > ep::kMaxExperts || num_tokens > ep::kLayerMaxPairs / num_topk || hidden <= 0 || hidden % 64 != 0 ||
       hidden > kMaxHidden || inter <= 0 || inter % 64 != 0 || inter > kMaxHidden)
     return 0;
-  return ep::layer_ws(num_tokens, num_topk, hidden, inter).total;
+  return ep::layer_ws(num_tokens, num_topk, num_experts, hidden, inter).total;
 }
 
 ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, const void *topk_idx,
@@ -556,7 +556,7 @@ ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, cons
     return fail(EP_ERR_INVALID_ARG, "%s: w1_scales / w2_scales NULL or not 16-byte aligned", fn);
   if (!workspace || !aligned(workspace, ep::kWsAlign))
     return fail(EP_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
-  const size_t need = ep::layer_ws(num_tokens, num_topk, hidden, inter).total;
+  const size_t need = ep::layer_ws(num_tokens, num_topk, num_experts, hidden, inter).total;
   if (workspace_bytes < need)
     return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
   const ep::LayerArgs a{x, num_tokens, num_topk, num_experts, hidden, inter, w_quant, topk_idx,

@@ -34,7 +34,13 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 8;
+// Measured (us, both launches): one token of 256 MXFP8 experts (H 7168, I
+// 2048, top 8) 39 + 30 with 4 waves, 2 groups and 2 steps in flight; 42 + 37
+// with 8 waves, 68 + 53 with 1 group, 40 + 31 with 3 steps; 128 tokens 1180 +
+// 770, against 1220 + 1010, 1900 + 1300 and 1215 + 830.
+constexpr int kWaves = 4;
+constexpr int kGroups = 2;                        // 32-row weight groups of a workgroup
+constexpr int kRing = 2;                          // K steps in flight per wave
 constexpr int kThreads = kWaves * kWave;
 constexpr int kTile = 32;                         // tokens per pass over an expert's weights
 
@@ -96,64 +102,86 @@ __global__ void pack_kernel(const uint8_t *__restrict__ w, const uint8_t *__rest
 
 // ------------------------------------------------------ rows of an expert
 
-struct Rows {
-  int used;                                       // experts in use
-  int expert, n;                                  // the unit's expert (-1: none) and its pairs
-};
+// Workgroup barrier for LDS hand-offs: the LDS writes before it are waited
+// for, global loads in flight are not (__syncthreads would drain them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// The `rank`-th expert in use (ascending id) and its pairs in ascending
-// order, into `list`; every thread of the workgroup takes part.
+constexpr int kIter = (int)(kLayerMaxPairs / kThreads);   // ids per thread, at most
+
+// A call's ids in LDS, as the workgroup that looks for its expert sees them.
+struct Ids {
+  uint16_t id[kLayerMaxPairs];                    // kNoExpert: none
+  uint32_t in_use[kMaxExperts / 32];              // bit set of the experts in use
+  int cnt[kIter * kWaves];
+};
+constexpr uint16_t kNoExpert = 0xffff;
+
+// Reads the ids; the rank-th expert in use (-1: there are fewer) and how many
+// are.  Every thread of the workgroup takes part.
 template <typename IdxT>
-__device__ __forceinline__ Rows find_rows(const IdxT *__restrict__ idx, int P, int E, int rank, uint16_t *list) {
-  constexpr int kIter = (int)(kLayerMaxPairs / kThreads);
-  __shared__ uint32_t s_used[kMaxExperts / 32];
-  __shared__ int s_cnt[kIter * kWaves];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
-  int id[kIter];
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int p = i * kThreads + tid;
-    const int64_t v = p < P ? (int64_t)idx[p] : -1;
-    id[i] = v >= 0 && v < E ? (int)v : -1;
+__device__ __forceinline__ int find_expert(const IdxT *__restrict__ idx, int P, int E, int rank, Ids &s, int &used) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  if (tid < kMaxExperts / 32) s.in_use[tid] = 0;
+  lds_barrier();
+  for (int p = tid; p < P; p += kThreads) {
+    const int64_t v = (int64_t)idx[p];
+    const bool on = v >= 0 && v < E;
+    s.id[p] = on ? (uint16_t)v : kNoExpert;
+    if (on) atomicOr(&s.in_use[v >> 5], 1u << (v & 31));
   }
-  if (tid < kMaxExperts / 32) s_used[tid] = 0;
-  __syncthreads();
+  lds_barrier();
+  // the rank-th set bit: every wave counts the 16 words in its first 16 lanes
+  const uint32_t word = lane < kMaxExperts / 32 ? s.in_use[lane] : 0u;
+  int upto = __popc(word);
 #pragma unroll
-  for (int i = 0; i < kIter; ++i)
-    if (id[i] >= 0) atomicOr(&s_used[id[i] >> 5], 1u << (id[i] & 31));
-  __syncthreads();
-  Rows r;
-  r.used = 0;
-  r.expert = -1;
-  r.n = 0;
-#pragma unroll
-  for (int w = 0; w < kMaxExperts / 32; ++w) {
-    uint32_t bits = s_used[w];
-    const int c = __popc(bits);
-    if (rank >= r.used && rank < r.used + c) {
-      for (int d = rank - r.used; d > 0; --d) bits &= bits - 1;
-      r.expert = w * 32 + __ffs(bits) - 1;
-    }
-    r.used += c;
+  for (int d = 1; d < kMaxExperts / 32; d <<= 1) {
+    const int o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
   }
-  if (r.expert < 0) return r;
-  uint64_t bal[kIter];
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    bal[i] = __ballot(id[i] == r.expert);
-    if (lane == 0) s_cnt[i * kWaves + wv] = __popcll(bal[i]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    int before = 0;
-    for (int j = 0; j < kIter * kWaves; ++j) before += j < i * kWaves + wv ? s_cnt[j] : 0;
-    if (id[i] == r.expert) list[before + __popcll(bal[i] & ((1ull << lane) - 1ull))] = (uint16_t)(i * kThreads + tid);
-  }
-  for (int j = 0; j < kIter * kWaves; ++j) r.n += s_cnt[j];
-  __syncthreads();
-  return r;
+  used = __builtin_amdgcn_readlane(upto, kMaxExperts / 32 - 1);
+  if (rank >= used) return -1;                    // uniform
+  const int at = __ffsll(__ballot(lane < kMaxExperts / 32 && upto > rank)) - 1;
+  uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)word, at);
+  for (int d = rank - (__builtin_amdgcn_readlane(upto, at) - __popc(bits)); d > 0; --d) bits &= bits - 1;
+  return at * 32 + __ffs(bits) - 1;
 }
+
+// The pairs of `expert` in ascending order, into `list`; returns their
+// number.  Every thread takes part.
+__device__ __forceinline__ int list_pairs(Ids &s, int P, int expert, uint16_t *list) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+  const int iters = (P + kThreads - 1) / kThreads;
+  // pairs in (iteration, wave, lane) order
+  for (int i = 0; i < iters; ++i) {
+    const int p = i * kThreads + tid;
+    const uint64_t mine = __ballot(p < P && s.id[p] == expert);
+    if (lane == 0) s.cnt[i * kWaves + wv] = __popcll(mine);
+  }
+  lds_barrier();
+  const int cnt = lane < iters * kWaves ? s.cnt[lane] : 0;
+  int sum = cnt;
+#pragma unroll
+  for (int d = 1; d < kIter * kWaves; d <<= 1) {
+    const int o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
+  }
+  for (int i = 0; i < iters; ++i) {
+    const int p = i * kThreads + tid, before = __shfl(sum - cnt, i * kWaves + wv);
+    const bool on = p < P && s.id[p] == expert;
+    const uint64_t mine = __ballot(on);
+    if (on) list[before + __popcll(mine & ((1ull << lane) - 1ull))] = (uint16_t)p;
+  }
+  lds_barrier();
+  return __builtin_amdgcn_readlane(sum, kIter * kWaves - 1);
+}
+static_assert(kIter * kWaves <= kWave, "one count per lane");
+
+// What launch 1 leaves for launch 2 about the rank-th expert in use: its id
+// (-1: there are fewer), its pairs, and the number of experts in use.  The
+// pairs follow at rank * P of the list.
+struct Head {
+  int expert, n, used, pad;
+};
 
 // -------------------------------------------------------------- fragments
 
@@ -199,19 +227,18 @@ __device__ __forceinline__ void operands(const Frag<Q> &f, int u, bf16x8 (&a)[4]
 
 // Partial products of this wave's share [s0, s1) of the K steps: NG weight
 // groups from `wp` (fragments of one step: groups, then lanes) times the
-// lane's activation row `b` (K bf16 values).
-template <int Q, int NG>
-__device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const uint8_t *sp, size_t sspan,
-                                        const uint16_t *b, int s0, int s1, v16f (&acc)[NG]) {
+// lane's activation row (K bf16 values), which `row()` finds while the first
+// weights are on their way (every wave calls it, so it may hold a barrier).
+template <int Q, int NG, typename Row>
+__device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const uint8_t *sp, size_t sspan, int s0,
+                                        int s1, Row row, v16f (&acc)[NG]) {
   constexpr int kPieces = fragment_bytes(Q) / 1024;
-  constexpr int kRing = 2;
-  const int lane = threadIdx.x & (kWave - 1), g = lane >> 5;
+  const uint32_t lane = threadIdx.x & (kWave - 1), g = lane >> 5;
 #pragma unroll
   for (int q = 0; q < NG; ++q) acc[q] = v16f{};
-  if (s0 >= s1) return;                           // uniform
   Frag<Q> w[kRing][NG];
   u32x4 bv[kRing][4];
-  auto load = [&](int slot, int s) {
+  auto load_w = [&](int slot, int s) {
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
 #pragma unroll
@@ -221,12 +248,19 @@ __device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const u
       if constexpr (Q != EP_QUANT_NONE)
         w[slot][q].scale = *(const uint32_t *)(sp + (size_t)(s >> 2) * sspan + q * 256 + lane * 4);
     }
+  };
+  if (s0 < s1) {                                  // uniform
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-      bv[slot][m] = *(const u32x4 *)(b + (size_t)s * 64 + (m >> 1) * 32 + g * 16 + (m & 1) * 8);
+    for (int r = 0; r < kRing; ++r) load_w(r, min(s0 + r, s1 - 1));
+  }
+  const uint16_t *b = row() + g * 16;
+  if (s0 >= s1) return;
+  auto load_b = [&](int slot, int s) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) bv[slot][m] = *(const u32x4 *)(b + s * 64 + (m >> 1) * 32 + (m & 1) * 8);
   };
 #pragma unroll
-  for (int r = 0; r < kRing; ++r) load(r, min(s0 + r, s1 - 1));
+  for (int r = 0; r < kRing; ++r) load_b(r, min(s0 + r, s1 - 1));
   for (int s = s0; s < s1; s += kRing) {
 #pragma unroll
     for (int r = 0; r < kRing; ++r) {
@@ -241,7 +275,8 @@ __device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const u
                                                              0);
         }
       }
-      load(r, min(s + r + kRing, s1 - 1));        // past the end: the last step again, never used
+      load_w(r, min(s + r + kRing, s1 - 1));      // past the end: the last step again, never used
+      load_b(r, min(s + r + kRing, s1 - 1));
     }
   }
 }
@@ -268,105 +303,145 @@ __device__ __forceinline__ f32x4 summed(const float *tile, int q, int b, int lan
 
 __device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
 
+// Two floats for a workgroup that may run on another die.
+__device__ __forceinline__ void put_shared(uint64_t *to, float lo, float hi) {
+  __hip_atomic_store(to, (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Launch 1: act[p] = silu(G x) * (U x) of every pair p; NG groups of 16
 // gate and 16 up rows per workgroup.
 template <int Q, int NG, typename IdxT>
 __global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerArgs a, uint16_t *__restrict__ act,
+                                                            Head *__restrict__ heads, uint16_t *__restrict__ lists,
                                                             uint32_t *__restrict__ done, int blocks) {
+  __shared__ Ids s_ids;
   __shared__ uint16_t s_list[kLayerMaxPairs];
   __shared__ __attribute__((aligned(16))) float s_tile[kWaves * NG * 16 * kWave];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   if (blockIdx.x == 0)
     for (int i = tid; i < a.hidden / 32; i += kThreads) done[i] = 0;
-  const int blk = blockIdx.x % blocks;
-  const Rows rows = find_rows((const IdxT *)a.idx, (int)a.T * a.k, a.E, blockIdx.x / blocks, s_list);
-  if (rows.expert < 0) return;                    // uniform
+  const int blk = blockIdx.x % blocks, rank = blockIdx.x / blocks, P = (int)a.T * a.k;
+  int used;
+  const int expert = find_expert((const IdxT *)a.idx, P, a.E, rank, s_ids, used);
+  if (expert < 0) {                               // uniform
+    if (blk == 0 && tid == 0) heads[rank] = Head{-1, 0, used, 0};
+    return;
+  }
   const int K = a.hidden, ksteps = K / 64, groups = a.inter / 16;
   const int g0 = min(blk * NG, groups - NG);      // a partial last block repeats groups of the one before
-  const size_t gidx = (size_t)rows.expert * groups + g0;
+  const size_t gidx = (size_t)expert * groups + g0;
   const int s0 = ksteps * wv / kWaves, s1 = ksteps * (wv + 1) / kWaves;
-  for (int r0 = 0; r0 < rows.n; r0 += kTile) {
-    const int n = min(kTile, rows.n - r0);
-    const uint16_t *b = (const uint16_t *)a.x + (size_t)(s_list[r0 + min(lane & 31, n - 1)] / a.k) * K;
+  int n = 0;
+  for (int r0 = 0; r0 == 0 || r0 < n; r0 += kTile) {
+    int pair = 0;
     v16f acc[NG];
     product<Q, NG>(a.w1 + gidx * fragment_bytes(Q), (size_t)a.E * groups * fragment_bytes(Q), a.w1_scales + gidx * 256,
-                   (size_t)a.E * groups * 256, b, s0, s1, acc);
-    if (r0 > 0) __syncthreads();
+                   (size_t)a.E * groups * 256, s0, s1,
+                   [&] {
+                     if (r0 == 0) n = list_pairs(s_ids, P, expert, s_list);
+                     pair = s_list[min(r0 + (lane & 31), n - 1)];
+                     return (const uint16_t *)a.x + (size_t)(pair / a.k) * K;
+                   },
+                   acc);
+    if (r0 > 0) lds_barrier();
     leave_partials<NG>(s_tile, acc);
-    __syncthreads();
+    lds_barrier();
     // lane l of quad b holds column l % 32, rows 8b + 4 (l / 32) + 0..3: quads
     // 0 and 1 are gate rows, 2 and 3 the same up rows
-    for (int job = tid; job < NG * 2 * kWave; job += kThreads) {
-      const int l = job & 63, qb = job >> 6, q = qb >> 1, h = qb & 1;
-      const int c = l & 31;
-      if (c >= n) continue;
-      const f32x4 gate = summed<NG>(s_tile, q, h, l), up = summed<NG>(s_tile, q, h + 2, l);
+    for (int qb = wv; qb < NG * 2; qb += kWaves) {
+      const int q = qb >> 1, h = qb & 1;
+      if (r0 + (lane & 31) >= n) break;
+      const f32x4 gate = summed<NG>(s_tile, q, h, lane), up = summed<NG>(s_tile, q, h + 2, lane);
       const u32x2 v = {pack_bf16x2(silu(gate.x) * up.x, silu(gate.y) * up.y),
                        pack_bf16x2(silu(gate.z) * up.z, silu(gate.w) * up.w)};
-      *(u32x2 *)(act + (size_t)s_list[r0 + c] * a.inter + 16 * (g0 + q) + 8 * h + 4 * (l >> 5)) = v;
+      *(u32x2 *)(act + (size_t)pair * a.inter + 16 * (g0 + q) + 8 * h + 4 * (lane >> 5)) = v;
     }
+  }
+  if (blk == 0) {
+    if (tid == 0) heads[rank] = Head{expert, n, used, 0};
+    for (int i = tid; i < n; i += kThreads) lists[(size_t)rank * P + i] = s_list[i];
   }
 }
 
 // Launch 2: y[p] = D act[p], then out[t] = sum_j w y[t k + j] by the last
 // workgroup of each block of 32 NG columns.
 template <int Q, int NG, typename IdxT>
-__global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const uint16_t *__restrict__ act, float *y,
+__global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const uint16_t *__restrict__ act,
+                                                              const Head *__restrict__ heads,
+                                                              const uint16_t *__restrict__ lists, float *y,
                                                               uint32_t *done, int blocks) {
-  __shared__ uint16_t s_list[kLayerMaxPairs];
   __shared__ __attribute__((aligned(16))) float s_tile[kWaves * NG * 16 * kWave];
   __shared__ uint32_t s_last;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
-  const int blk = blockIdx.x % blocks, rank = blockIdx.x / blocks;
-  const int P = (int)a.T * a.k;
-  const Rows rows = find_rows((const IdxT *)a.idx, P, a.E, rank, s_list);
-  if (rows.expert < 0 && !(rank == 0 && rows.used == 0)) return;   // uniform
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int blk = blockIdx.x % blocks, rank = blockIdx.x / blocks, P = (int)a.T * a.k;
+  const int expert = heads[rank].expert, n = heads[rank].n, used = heads[rank].used;
+  if (expert < 0 && !(rank == 0 && used == 0)) return;             // uniform
   const int K = a.inter, ksteps = K / 64, groups = a.hidden / 32;
   const int g0 = min(blk * NG, groups - NG);
-  if (rows.expert >= 0) {
-    const size_t gidx = (size_t)rows.expert * groups + g0;
+  if (expert >= 0) {
+    const size_t gidx = (size_t)expert * groups + g0;
     const int s0 = ksteps * wv / kWaves, s1 = ksteps * (wv + 1) / kWaves;
-    for (int r0 = 0; r0 < rows.n; r0 += kTile) {
-      const int n = min(kTile, rows.n - r0);
-      const uint16_t *b = act + (size_t)s_list[r0 + min(lane & 31, n - 1)] * K;
+    for (int r0 = 0; r0 < n; r0 += kTile) {
+      int pair = 0;
       v16f acc[NG];
       product<Q, NG>(a.w2 + gidx * fragment_bytes(Q), (size_t)a.E * groups * fragment_bytes(Q),
-                     a.w2_scales + gidx * 256, (size_t)a.E * groups * 256, b, s0, s1, acc);
-      if (r0 > 0) __syncthreads();
+                     a.w2_scales + gidx * 256, (size_t)a.E * groups * 256, s0, s1,
+                     [&] {
+                       pair = lists[(size_t)rank * P + min(r0 + (lane & 31), n - 1)];
+                       return act + (size_t)pair * K;
+                     },
+                     acc);
+      if (r0 > 0) lds_barrier();
       leave_partials<NG>(s_tile, acc);
-      __syncthreads();
-      for (int job = tid; job < NG * 4 * kWave; job += kThreads) {
-        const int l = job & 63, qb = job >> 6, q = qb >> 2, h = qb & 3;
-        const int c = l & 31;
-        if (c >= n) continue;
-        const f32x4 v = summed<NG>(s_tile, q, h, l);
-        // agent scope: read by a workgroup that may sit on another die
-        float *to = y + (size_t)s_list[r0 + c] * a.hidden + 32 * (g0 + q) + 8 * h + 4 * (l >> 5);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) __hip_atomic_store(to + i, v[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      lds_barrier();
+      for (int qb = wv; qb < NG * 4; qb += kWaves) {
+        const int q = qb >> 2, h = qb & 3;
+        if (r0 + (lane & 31) >= n) break;
+        const f32x4 v = summed<NG>(s_tile, q, h, lane);
+        uint64_t *to = (uint64_t *)(y + (size_t)pair * a.hidden + 32 * (g0 + q) + 8 * h + 4 * (lane >> 5));
+        put_shared(to, v.x, v.y);
+        put_shared(to + 1, v.z, v.w);
       }
     }
-    __threadfence();
+    // y goes past the die's L2 (agent scope), and the wait below holds until
+    // it has arrived: the count can then rise without a fence, which would
+    // write back the whole L2 (at 128 tokens launch 2 took 12 times as long
+    // with one)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid == 0)
-      s_last = __hip_atomic_fetch_add(done + blk, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-               (uint32_t)rows.used - 1;
+      s_last = __hip_atomic_fetch_add(done + blk, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (uint32_t)used - 1;
     __syncthreads();
     if (!s_last) return;
   }
-  // out[t] over the block's columns, two per thread
+  // out[t] over the block's columns, two per thread; the rows of up to 8
+  // pairs are loaded at once
   constexpr int kPairs = 16 * NG;
   const IdxT *idx = (const IdxT *)a.idx;
   for (int job = tid; job < (int)a.T * kPairs; job += kThreads) {
     const int t = job / kPairs, c = 32 * g0 + 2 * (job - t * kPairs);
     float o0 = 0.0f, o1 = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      const int64_t e = (int64_t)idx[t * a.k + j];
-      if (e < 0 || e >= a.E) continue;
-      float *from = y + (size_t)(t * a.k + j) * a.hidden + c;
-      const float w = a.weights[t * a.k + j];
-      o0 += w * __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      o1 += w * __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      uint64_t v[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = t * a.k + min(j0 + j, a.k - 1);
+        const int64_t e = (int64_t)idx[p];
+        const bool on = j0 + j < a.k && e >= 0 && e < a.E;
+        w[j] = a.weights[p];
+        v[j] = 0;
+        if (on) v[j] = __hip_atomic_load((uint64_t *)(y + (size_t)p * a.hidden + c), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+        if (!on) w[j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o0 += w[j] * __uint_as_float((uint32_t)v[j]);
+        o1 += w[j] * __uint_as_float((uint32_t)(v[j] >> 32));
+      }
     }
     *(uint32_t *)((uint16_t *)a.out + (size_t)t * a.hidden + c) = pack_bf16x2(o0, o1);
   }
@@ -374,23 +449,25 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
 
 template <int Q, int NG, typename IdxT>
 hipError_t layer_launch(const LayerArgs &a, hipStream_t s) {
-  const LayerWs ws = layer_ws(a.T, a.k, a.hidden, a.inter);
+  const LayerWs ws = layer_ws(a.T, a.k, a.E, a.hidden, a.inter);
   uint16_t *act = (uint16_t *)(a.ws + ws.act);
   float *y = (float *)(a.ws + ws.y);
   uint32_t *done = (uint32_t *)(a.ws + ws.done);
+  Head *heads = (Head *)(a.ws + ws.heads);
+  uint16_t *lists = (uint16_t *)(a.ws + ws.lists);
   const int64_t P = a.T * a.k, used = P < a.E ? P : a.E;
   const int up_blocks = (a.inter / 16 + NG - 1) / NG, down_blocks = (a.hidden / 32 + NG - 1) / NG;
   hipLaunchKernelGGL((layer_up_kernel<Q, NG, IdxT>), dim3((unsigned)(used * up_blocks)), dim3(kThreads), 0, s, a, act,
-                     done, up_blocks);
+                     heads, lists, done, up_blocks);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((layer_down_kernel<Q, NG, IdxT>), dim3((unsigned)(used * down_blocks)), dim3(kThreads), 0, s, a,
-                     act, y, done, down_blocks);
+                     act, heads, lists, y, done, down_blocks);
   return hipGetLastError();
 }
 template <int Q>
 hipError_t layer_q(const LayerArgs &a, hipStream_t s) {
-  return a.idx64 ? layer_launch<Q, 2, int64_t>(a, s) : layer_launch<Q, 2, int32_t>(a, s);
+  return a.idx64 ? layer_launch<Q, kGroups, int64_t>(a, s) : layer_launch<Q, kGroups, int32_t>(a, s);
 }
 
 }  // namespace

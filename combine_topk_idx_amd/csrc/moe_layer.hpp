@@ -13,14 +13,17 @@ __host__ __device__ constexpr int fragment_bytes(int quant) {
 }
 
 struct LayerWs {                                  // byte offsets of the workspace sub-arrays
-  size_t act, y, done, total;
+  size_t act, y, done, heads, lists, total;
 };
-__host__ inline LayerWs layer_ws(int64_t T, int32_t k, int32_t hidden, int32_t inter) {
+__host__ inline LayerWs layer_ws(int64_t T, int32_t k, int32_t E, int32_t hidden, int32_t inter) {
+  const size_t P = (size_t)T * k, used = P < (size_t)E ? P : (size_t)E;
   LayerWs w;
   w.act = 0;
-  w.y = w.act + align_up((size_t)T * k * inter * 2, kWsAlign);
-  w.done = w.y + align_up((size_t)T * k * hidden * 4, kWsAlign);
-  w.total = w.done + align_up((size_t)(hidden / 32) * 4, kWsAlign);
+  w.y = w.act + align_up(P * inter * 2, kWsAlign);
+  w.done = w.y + align_up(P * hidden * 4, kWsAlign);
+  w.heads = w.done + align_up((size_t)(hidden / 32) * 4, kWsAlign);
+  w.lists = w.heads + align_up(used * 16, kWsAlign);
+  w.total = w.lists + align_up(used * P * 2, kWsAlign);
   return w;
 }
 
