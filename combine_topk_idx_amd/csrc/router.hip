@@ -13,8 +13,17 @@
 // An expert whose logit or key is -inf or NaN is never chosen.
 //
 // Two keys s_e + bias_e may lie closer than float32 rounding, and then the
-// order would depend on how exp was evaluated; keys with a bias and sums of
-// two scores are therefore held in float64.
+// order would depend on how exp was evaluated.  The order is therefore that
+// of float64 keys: the fast path ranks float32 keys and checks that every
+// gap that matters is wider than their error; a wave that finds a closer one
+// ranks its tokens again with float64 keys.
+//
+// Fast path: 16 lanes take a token (four tokens a wave), each a run of
+// ceil(E / 16) experts.  A key and its expert are one double (the expert in
+// the low mantissa bits, so that all are different and ties go to the lower
+// id), which v_max_f64 / v_min_f64 compare at full rate: every lane sorts its
+// run in registers, then four exchange steps inside the 16 lanes merge the
+// lanes' best lists.  No LDS, no loop over the k choices.
 #include <math.h>
 
 #include "common.hpp"
@@ -25,8 +34,11 @@ namespace ep {
 
 namespace {
 
-constexpr int kTokens = 4;                        // tokens (waves) per workgroup
-constexpr int kItems = kMaxExperts / kWave;       // experts per lane: lane, lane + 64, ...
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kRow = 16;                          // lanes of a token
+constexpr int kTokens = kThreads / kRow;          // tokens per workgroup
+constexpr float kLargest = 3.402823466e38f;
 
 template <int DT>
 __device__ __forceinline__ float logit(const void *p, int64_t i) {
@@ -39,6 +51,169 @@ __device__ __forceinline__ void put(void *p, int64_t i, float v) {
   if constexpr (DT == EP_FLOAT_F32) ((float *)p)[i] = v;
   else if constexpr (DT == EP_FLOAT_BF16) ((__bf16 *)p)[i] = (__bf16)v;
   else ((_Float16 *)p)[i] = (_Float16)v;
+}
+// NaN and -inf: no expert (-inf); +inf: the largest finite logit
+__device__ __forceinline__ float usable(float z) { return z > -INFINITY ? fminf(z, kLargest) : -INFINITY; }
+
+// This lane's run of `run` logits, [first, first + run) of a row of E (which
+// starts at element `row`); -inf past them.  16-byte loads where every run
+// starts on 16 bytes.
+template <int DT, int I>
+__device__ __forceinline__ void load_run(const void *p, int64_t row, int E, int first, int run, bool live, bool wide,
+                                         float (&z)[I]) {
+  constexpr int kVec = DT == EP_FLOAT_F32 ? 4 : 8;
+  if constexpr (I >= kVec) {
+    if (wide) {                                   // uniform; run is a multiple of kVec
+#pragma unroll
+      for (int v = 0; v < I / kVec; ++v) {
+        u32x4 w = {};
+        const bool on = live && v * kVec < run && first + v * kVec < E;
+        if (on) w = *(const u32x4 *)((const char *)p + (row + first + v * kVec) * (16 / kVec));
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          float f;
+          if constexpr (DT == EP_FLOAT_F32) f = __uint_as_float(w[i]);
+          else if constexpr (DT == EP_FLOAT_BF16) f = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+          else f = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+          z[v * kVec + i] = on ? usable(f) : -INFINITY;
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+    z[i] = live && i < run && first + i < E ? usable(logit<DT>(p, row + first + i)) : -INFINITY;
+}
+
+// ------------------------------------------------ exchanges in 16 lanes
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128;   // quad swaps, rotations by 4 and 8
+constexpr int kHalf = 0x141;                      // mirror of 8 lanes: the other quad of the half
+constexpr int kBcast = 0x150;                                             // + lane of the row
+
+// max / min of doubles that are never NaN (the operator forms compile to a
+// compare and two selects, fmax to extra canonicalisations)
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double max_of(double a, double b) { return max64(a, b); }
+
+template <typename T>
+__device__ __forceinline__ T row_max(T v) {
+  v = max_of(v, dpp<kXor1>(v));
+  v = max_of(v, dpp<kXor2>(v));
+  v = max_of(v, dpp<kRor4>(v));
+  return max_of(v, dpp<kRor8>(v));
+}
+template <typename T>
+__device__ __forceinline__ T row_sum(T v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kRor4>(v);
+  return v + dpp<kRor8>(v);
+}
+
+// -------------------------------------------------------- packed keys
+// A key of at most 44 significant bits with its expert in the 9 low mantissa
+// bits: among equal keys the lower expert is the larger double.  No key: -inf.
+__device__ __forceinline__ double pack_key(double key, int e) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, key + 0.0);   // -0 becomes +0
+  const uint64_t low = (u >> 63) ? (uint64_t)e : (uint64_t)(kMaxExperts - 1 - e);
+  const double r = __builtin_bit_cast(double, (u & ~(uint64_t)(kMaxExperts - 1)) | low);
+  return key > -INFINITY ? r : -INFINITY;
+}
+__device__ __forceinline__ int expert_in(double packed) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, packed);
+  const int low = (int)(u & (kMaxExperts - 1));
+  return (u >> 63) ? low : kMaxExperts - 1 - low;
+}
+__device__ __forceinline__ double key_in(double packed) {
+  return packed > -INFINITY
+             ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, packed) & ~(uint64_t)(kMaxExperts - 1))
+             : packed;
+}
+static_assert((kMaxExperts & (kMaxExperts - 1)) == 0, "the expert is a bit field");
+
+// Batcher's odd-even merge sort, descending; n a power of two.
+template <int N>
+__device__ __forceinline__ void sort_run(double (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const double a = v[i + j], b = v[i + j + q];
+            v[i + j] = max64(a, b);
+            v[i + j + q] = min64(a, b);
+          }
+}
+// The L largest of two descending lists, one here and one in the lane CTRL
+// names: the element-wise maximum against the other's reverse holds them as a
+// bitonic sequence, which log L exchange steps sort.
+template <int CTRL, int L>
+__device__ __forceinline__ void merge_step(double (&v)[L]) {
+  double o[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) o[i] = dpp<CTRL>(v[L - 1 - i]);
+#pragma unroll
+  for (int i = 0; i < L; ++i) v[i] = max64(v[i], o[i]);
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if ((i & d) == 0) {
+        const double a = v[i], b = v[i + d];
+        v[i] = max64(a, b);
+        v[i + d] = min64(a, b);
+      }
+}
+
+// log of the score, up to a constant of the row: z for a softmax,
+// log sigmoid(z) = min(z, 0) - log(1 + e^-|z|)
+__device__ __forceinline__ float log_score(int score, float z) {
+  return score == EP_SCORE_SOFTMAX ? z : fminf(z, 0.0f) - log1pf(expf(-fabsf(z)));
+}
+__device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// ------------------------------------------------------------ wave path
+// One token per wave with float64 keys in LDS: group shapes that do not fall
+// on whole lanes, and the tokens whose float32 keys lie too close.
+struct WaveLds {
+  double key[kMaxExperts], rank[kMaxGroups];
+};
+
+// LDS written by some lanes of a wave is read by others: its accesses
+// complete in order, the compiler must not move them across.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 template <typename T>
@@ -54,99 +229,75 @@ __device__ __forceinline__ T wave_sum(T v) {
   return v;
 }
 
-// log of the score, up to a constant of the row: z for a softmax,
-// log sigmoid(z) = min(z, 0) - log(1 + e^-|z|)
-__device__ __forceinline__ float log_score(int score, float z) {
-  return score == EP_SCORE_SOFTMAX ? z : fminf(z, 0.0f) - log1pf(expf(-fabsf(z)));
-}
-__device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(-z)); }
-
-template <int DT, typename IdxT>
-__global__ __launch_bounds__(kTokens *kWave) void router_kernel(RouterArgs a, IdxT *__restrict__ idx,
-                                                                float *__restrict__ weights) {
-  __shared__ double s_key[kTokens][kMaxExperts];
-  __shared__ double s_rank[kTokens][kMaxGroups];
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + wv;
-  const bool live = t < a.T;
-  const int E = a.E, k = a.k;
+// The ids of token t: lane j gets the j-th (-1: none).
+template <int DT>
+__device__ __forceinline__ int wave_route(const RouterArgs &a, int64_t t, WaveLds &s) {
+  const int lane = threadIdx.x & (kWave - 1), E = a.E;
   const double kNone = -INFINITY;
-
-  float z[kItems];
-  double key[kItems];
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const int e = lane + i * kWave;
-    z[i] = live && e < E ? logit<DT>(a.logits, t * E + e) : -INFINITY;
-    z[i] = z[i] > -INFINITY ? fminf(z[i], 3.402823466e38f) : -INFINITY;   // NaN and -inf: not there; +inf: the largest
-    top = fmaxf(top, z[i]);
-  }
-  top = wave_max(top);
   const bool softmax = a.score == EP_SCORE_SOFTMAX;
-  double sum = 0.0;
-  double s64[kItems];
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const bool there = z[i] > -INFINITY;
-    s64[i] = !there ? 0.0 : softmax ? exp((double)z[i] - (double)top) : 1.0 / (1.0 + exp(-(double)z[i]));
-    sum += s64[i];
-  }
+  float top = -INFINITY;
+  double sum = 1.0;
   if (softmax) {
+    for (int e = lane; e < E; e += kWave) top = fmaxf(top, usable(logit<DT>(a.logits, t * E + e)));
+    top = wave_max(top);
+    sum = 0.0;
+    for (int e = lane; e < E; e += kWave) {
+      const float z = usable(logit<DT>(a.logits, t * E + e));
+      sum += z > -INFINITY ? exp((double)z - (double)top) : 0.0;
+    }
     sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) s64[i] = sum > 0.0 ? s64[i] / sum : 0.0;
   }
   const bool by_sum = a.groups > 1 && a.top == 2;
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const int e = lane + i * kWave;
-    const bool there = z[i] > -INFINITY;
-    double c = kNone;
-    if (there) c = s64[i] + (a.bias ? (double)a.bias[e] : 0.0);
-    if (!(c > kNone)) c = kNone;                  // a NaN bias
-    key[i] = a.bias ? c : (there ? (double)z[i] : kNone);
-    if (a.groups > 1 && e < E) s_key[wv][e] = by_sum ? c : key[i];
+  // the keys; without a bias the group sums need the scores first
+  for (int pass = by_sum && !a.bias ? 0 : 1; pass < 2; ++pass) {
+    for (int e = lane; e < E; e += kWave) {
+      const float z = usable(logit<DT>(a.logits, t * E + e));
+      double c = kNone;
+      if (z > -INFINITY) {
+        if (pass == 1 && !a.bias) {
+          c = (double)z;
+        } else {
+          c = softmax ? exp((double)z - (double)top) / sum : 1.0 / (1.0 + exp(-(double)z));
+          if (a.bias) c += (double)a.bias[e];
+        }
+        if (!(c > kNone)) c = kNone;              // a NaN bias
+      }
+      s.key[e] = c;
+    }
+    if (a.groups > 1 && (pass == 0 || a.bias || !by_sum)) {
+      const int size = E / a.groups;
+      wave_lds_fence();
+      if (lane < a.groups) {
+        double b0 = kNone, b1 = kNone;
+        for (int j = 0; j < size; ++j) {
+          const double v = s.key[lane * size + j];
+          if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) b1 = v;
+        }
+        s.rank[lane] = a.top == 2 ? b0 + b1 : b0;
+      }
+      wave_lds_fence();
+    }
   }
   if (a.groups > 1) {
-    __syncthreads();
-    const int size = E / a.groups;
-    if (lane < a.groups) {
-      double b0 = kNone, b1 = kNone;
-      for (int j = 0; j < size; ++j) {
-        const double v = s_key[wv][lane * size + j];
-        if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) b1 = v;
-      }
-      s_rank[wv][lane] = a.top == 2 ? b0 + b1 : b0;
-    }
-    __syncthreads();
     // a group stays when fewer than `keep` groups come before it
+    const int size = E / a.groups;
     bool stays = false;
     if (lane < a.groups) {
-      const double mine = s_rank[wv][lane];
+      const double mine = s.rank[lane];
       int before = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const double o = s_rank[wv][g];
-        before += o > mine || (o == mine && g < lane);
-      }
+      for (int g = 0; g < a.groups; ++g) before += s.rank[g] > mine || (s.rank[g] == mine && g < lane);
       stays = before < a.keep;
     }
     const uint64_t kept = __ballot(stays);
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int e = lane + i * kWave;
-      if (e < E && !((kept >> (e / size)) & 1)) key[i] = kNone;
-    }
+    for (int e = lane; e < E; e += kWave)
+      if (!((kept >> (e / size)) & 1)) s.key[e] = kNone;
   }
-
-  // k rounds of the wave's largest key; lane j keeps the j-th
   int my_id = -1;
-  for (int j = 0; j < k; ++j) {
+  for (int j = 0; j < a.k; ++j) {
     double best = kNone;
     int at = INT32_MAX;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-      if (key[i] > best) { best = key[i]; at = lane + i * kWave; }
+    for (int e = lane; e < E; e += kWave)
+      if (s.key[e] > best) { best = s.key[e]; at = e; }
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const double ob = __shfl_xor(best, d);
@@ -155,29 +306,229 @@ __global__ __launch_bounds__(kTokens *kWave) void router_kernel(RouterArgs a, Id
     }
     if (!(best > kNone)) break;                   // uniform: nothing left
     if (lane == j) my_id = at;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i)
-      if (lane + i * kWave == at) key[i] = kNone;
+    if ((at & (kWave - 1)) == lane) s.key[at] = kNone;
   }
-  float zj = -INFINITY;
-  if (my_id >= 0) {
-    zj = fminf(logit<DT>(a.logits, t * E + my_id), 3.402823466e38f);
-  }
-  float w = 0.0f;
+  return my_id;
+}
+
+// The weight of choice `lane` (of 16 lanes, id -1: none) and its store;
+// top and sum: the row's largest logit and sum of exp(z - top).
+template <int DT>
+__device__ __forceinline__ void store_choice(const RouterArgs &a, int64_t t, int j, bool live, int id, float top,
+                                             float sum, void *idx, int idx64, float *weights) {
+  const bool softmax = a.score == EP_SCORE_SOFTMAX;
+  const bool on = live && id >= 0;
+  const float z = on ? fminf(logit<DT>(a.logits, t * a.E + id), kLargest) : -INFINITY;
+  float w;
   if (a.renorm) {
     // s_j / sum s = softmax of the logs: no score underflows
-    const float ls = my_id >= 0 ? log_score(a.score, zj) : -INFINITY;
-    const float m = wave_max(ls);
-    const float p = my_id >= 0 ? expf(ls - m) : 0.0f;
-    const float total = wave_sum(p);
-    w = my_id >= 0 ? p / total : 0.0f;
-  } else if (my_id >= 0) {
-    w = softmax ? (float)(exp((double)zj - (double)top) / sum) : sigmoidf(zj);
+    const float ls = on ? log_score(a.score, z) : -INFINITY;
+    const float m = row_max(ls);
+    const float p = on ? expf(ls - m) : 0.0f;
+    const float total = row_sum(p);
+    w = on ? p / total : 0.0f;
+  } else {
+    w = !on ? 0.0f : softmax ? expf(z - top) / sum : sigmoidf(z);
   }
-  if (live && lane < k) {
-    idx[t * k + lane] = (IdxT)my_id;
-    weights[t * k + lane] = w * a.scale;
+  if (live && j < a.k) {
+    if (idx64) ((int64_t *)idx)[t * a.k + j] = id;
+    else ((int32_t *)idx)[t * a.k + j] = id;
+    weights[t * a.k + j] = w * a.scale;
   }
+}
+
+// Row maximum and sum of exp(z - max), float32, over a wave's token.
+template <int DT>
+__device__ __forceinline__ void wave_softmax(const RouterArgs &a, int64_t t, float &top, float &sum) {
+  const int lane = threadIdx.x & (kWave - 1);
+  top = -INFINITY;
+  for (int e = lane; e < a.E; e += kWave) top = fmaxf(top, usable(logit<DT>(a.logits, t * a.E + e)));
+  top = wave_max(top);
+  sum = 0.0f;
+  for (int e = lane; e < a.E; e += kWave) {
+    const float z = usable(logit<DT>(a.logits, t * a.E + e));
+    sum += z > -INFINITY ? expf(z - top) : 0.0f;
+  }
+  sum = wave_sum(sum);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void wave_router_kernel(RouterArgs a, void *idx, int idx64, float *weights) {
+  __shared__ WaveLds s_wave[kWaves];
+  const int wv = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+  const int64_t t = (int64_t)blockIdx.x * kWaves + wv;
+  if (t >= a.T) return;                           // a whole wave; no barriers below
+  const int id = wave_route<DT>(a, t, s_wave[wv]);
+  float top = 0.0f, sum = 1.0f;
+  if (!a.renorm && a.score == EP_SCORE_SOFTMAX) wave_softmax<DT>(a, t, top, sum);
+  if (lane < kRow) store_choice<DT>(a, t, lane, true, id, top, sum, idx, idx64, weights);
+}
+
+// ------------------------------------------------------------- row path
+// I: experts of a lane (its run padded to a power of two), L: length of the
+// merged lists (k rounded up to 8 or 16).
+template <int DT, int I, int L>
+__global__ __launch_bounds__(kThreads) void row_router_kernel(RouterArgs a, void *idx, int idx64, float *weights,
+                                                              int run, int wide) {
+  __shared__ WaveLds s_wave[kWaves];
+  const int j = threadIdx.x & (kRow - 1), wv = threadIdx.x / kWave;
+  const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kRow;
+  const bool live = t < a.T;
+  const bool softmax = a.score == EP_SCORE_SOFTMAX, biased = a.bias != nullptr;
+  const int first = j * run;
+  float z[I];
+  load_run<DT, I>(a.logits, t * a.E, a.E, first, run, live, wide & 1, z);
+
+  float top = -INFINITY, sum = 1.0f;
+  if (softmax) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) top = fmaxf(top, z[i]);
+    top = row_max(top);
+    if (biased || !a.renorm) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < I; ++i) sum += z[i] > -INFINITY ? expf(z[i] - top) : 0.0f;
+      sum = row_sum(sum);
+    }
+  }
+  // Keys.  What float32 may do to a score s (v_exp_f32 and v_rcp_f32 within
+  // 1 ulp, the product with log2 e in the exponent): a sigmoid is off by at
+  // most s ((1 - s) (|z| 2^-23.4 + 2^-23) + 2^-24 + 2^-23) < 2^-22, two of
+  // them by 2^-21; a softmax's terms by less than that, its sum (at most 36
+  // additions one after another) by 2^-18.8 of itself, which is common to
+  // the row: 2^-18 of the largest score for a difference.  The sum with the
+  // bias adds 2^-24 |key| each.  Keys further apart than
+  // off + 2^-22 |key| are in float64's order.
+  double v[I];
+  float off = 0x1p-21f;
+  if (biased) {
+    const float inv = softmax ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+    if (softmax) off = 0x1p-18f * inv;
+    constexpr float kLog2e = 1.44269504f;
+    float bias[I];
+    if (wide & 2) {                               // uniform
+#pragma unroll
+      for (int i = 0; i < I; i += 4) {
+        const u32x4 w = *(const u32x4 *)(a.bias + min(first + i, a.E - 4));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bias[i + q] = __uint_as_float(w[q]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < I; ++i) bias[i] = a.bias[min(first + i, a.E - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const float s = softmax ? __builtin_amdgcn_exp2f((z[i] - top) * kLog2e) * inv
+                              : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[i] * -kLog2e));
+      const float c = z[i] > -INFINITY ? s + bias[i] : -INFINITY;
+      v[i] = pack_key((double)c, min(first + i, kMaxExperts - 1));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < I; ++i) v[i] = pack_key((double)z[i], min(first + i, kMaxExperts - 1));
+  }
+  sort_run(v);
+
+  bool close = false;                             // of this token, seen by some lane
+  bool stays = true;
+  if (a.groups > 1) {
+    // a group is kRow / groups whole lanes: its two best keys from theirs
+    const int lanes = kRow / a.groups;
+    double b0 = v[0], b1 = I > 1 ? v[I > 1 ? 1 : 0] : (double)-INFINITY;
+    auto join = [&](double o0, double o1) {
+      const double lo = min64(b0, o0);
+      b0 = max64(b0, o0);
+      b1 = max64(lo, max64(b1, o1));
+    };
+    if (lanes > 1) join(dpp<kXor1>(b0), dpp<kXor1>(b1));
+    if (lanes > 2) join(dpp<kXor2>(b0), dpp<kXor2>(b1));
+    if (lanes > 4) join(dpp<kHalf>(b0), dpp<kHalf>(b1));
+    double rank = key_in(b0);
+    if (a.top == 2) {
+      if (biased) {
+        rank += key_in(b1);
+      } else {
+        // sums of two scores, in float64 (a softmax's up to the row's factor)
+        const double k0 = key_in(b0), k1 = key_in(b1);
+        const bool both = k1 > -INFINITY;
+        rank = !both ? (double)-INFINITY
+               : softmax ? exp(k0 - (double)top) + exp(k1 - (double)top)
+                         : 1.0 / (1.0 + exp(-k0)) + 1.0 / (1.0 + exp(-k1));
+      }
+    }
+    // a group stays when fewer than `keep` groups come before it
+    const int mine = j / lanes;
+    int before = 0;
+    double below = -INFINITY;                     // the best rank after this one
+    auto against = [&](double o, int og) {
+      const bool first_is = o > rank || (o == rank && og < mine);
+      before += first_is;
+      if (!first_is) below = max64(below, o);
+    };
+#define EP_ROT(R) \
+  if ((R) % lanes == 0) against(dpp<0x120 + (R)>(rank), ((j - (R)) & (kRow - 1)) / lanes)
+    EP_ROT(1); EP_ROT(2); EP_ROT(3); EP_ROT(4); EP_ROT(5); EP_ROT(6); EP_ROT(7); EP_ROT(8);
+    EP_ROT(9); EP_ROT(10); EP_ROT(11); EP_ROT(12); EP_ROT(13); EP_ROT(14); EP_ROT(15);
+#undef EP_ROT
+    stays = before < a.keep;
+    // the last kept group against the first one dropped
+    if (biased) {
+      const float k0 = (float)key_in(b0), k1 = (float)key_in(b1);
+      const float size = row_max(fmaxf(k0 > -INFINITY ? fabsf(k0) : 0.0f, k1 > -INFINITY ? fabsf(k1) : 0.0f));
+      if (before == a.keep - 1 && a.keep < a.groups)
+        close = !(rank - below > 2.0 * (double)(off + 0x1p-22f * size));
+    }
+  }
+
+  double best[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) best[i] = i < I && stays ? v[i < I ? i : 0] : (double)-INFINITY;
+  merge_step<kXor1>(best);
+  merge_step<kXor2>(best);
+  merge_step<kRor4>(best);
+  merge_step<kRor8>(best);
+
+  double mine = best[0], kth = best[0];
+#pragma unroll
+  for (int i = 1; i < L; ++i) {
+    if (j == i) mine = best[i];
+    if (i < a.k) kth = best[i];                   // uniform
+  }
+  int id = j < a.k && mine > -INFINITY ? expert_in(mine) : -1;
+  if (biased) {
+    // gaps inside the list, and from its end to the best key left out
+    float gap = INFINITY, size = 0.0f;
+#pragma unroll
+    for (int i = 0; i + 1 < L; ++i)
+      if (i + 1 < a.k && best[i + 1] > -INFINITY) {
+        gap = fminf(gap, (float)(key_in(best[i]) - key_in(best[i + 1])));
+        size = fmaxf(size, fabsf((float)best[i + 1]));
+      }
+    double next = -INFINITY;
+    if (stays) {
+#pragma unroll
+      for (int i = 0; i < I; ++i) next = max64(next, v[i] < kth ? v[i] : (double)-INFINITY);
+    }
+    next = row_max(next);
+    if (kth > -INFINITY && next > -INFINITY) {
+      gap = fminf(gap, (float)(key_in(kth) - key_in(next)));
+      size = fmaxf(size, fabsf((float)kth));
+    }
+    size = fmaxf(size, fabsf((float)(best[0] > -INFINITY ? best[0] : 0.0)));
+    close |= !(gap > off + 0x1p-22f * size);
+    uint64_t again = __ballot(close && live);
+    while (again) {                               // uniform: a token with close keys, by the whole wave
+      const int lane = threadIdx.x & (kWave - 1);
+      const int r = (__builtin_ffsll((long long)again) - 1) / kRow;
+      again &= ~(0xffffull << (r * kRow));
+      const int64_t tr = (int64_t)blockIdx.x * kTokens + (threadIdx.x / kWave) * (kWave / kRow) + r;
+      const int got = wave_route<DT>(a, tr, s_wave[wv]);
+      const int mine_of = __shfl(got, j);
+      if (lane / kRow == r) id = mine_of;
+    }
+  }
+  store_choice<DT>(a, t, j, live, id, top, sum, idx, idx64, weights);
 }
 
 // Gradient of the weights with respect to the logits.  With p_j the
@@ -186,87 +537,149 @@ __global__ __launch_bounds__(kTokens *kWave) void router_kernel(RouterArgs a, Id
 //   otherwise:    d log-score_j = s_j q_j
 //   softmax: dz_e = [e chosen] d_j - s_e sum_j d_j (the sum is 0 when
 //   renormalised); sigmoid: dz_j = d_j (1 - s_j)
-template <int DT, typename IdxT>
-__global__ __launch_bounds__(kTokens *kWave) void router_backward_kernel(RouterArgs a, const IdxT *__restrict__ idx,
-                                                                         const float *__restrict__ grad,
-                                                                         void *__restrict__ dz) {
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
-  const int64_t t = (int64_t)blockIdx.x * kTokens + wv;
-  if (t >= a.T) return;
-  const int E = a.E, k = a.k;
-  const bool softmax = a.score == EP_SCORE_SOFTMAX;
+// 16 lanes a token: lane j has choice j and the j-th run of experts.
+template <int DT, int I>
+__global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterArgs a, const void *idx, int idx64,
+                                                                   const float *__restrict__ grad, void *dz, int run,
+                                                                   int wide) {
+  const int j = threadIdx.x & (kRow - 1);
+  const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kRow;
+  const bool live = t < a.T;
+  const int E = a.E, k = a.k, first = j * run;
+  const bool softmax = a.score == EP_SCORE_SOFTMAX, dense = softmax && !a.renorm;
   int id = -1;
   float zj = -INFINITY, q = 0.0f;
-  if (lane < k) {
-    const int64_t v = (int64_t)idx[t * k + lane];
-    if (v >= 0 && v < E) {
-      zj = fminf(logit<DT>(a.logits, t * E + v), 3.402823466e38f);
-      if (zj > -INFINITY) { id = (int)v; q = grad[t * k + lane] * a.scale; }
+  if (live && j < k) {
+    const int64_t e = idx64 ? ((const int64_t *)idx)[t * k + j] : (int64_t)((const int32_t *)idx)[t * k + j];
+    if (e >= 0 && e < E) {
+      zj = usable(logit<DT>(a.logits, t * E + e));
+      if (zj > -INFINITY) { id = (int)e; q = grad[t * k + j] * a.scale; }
     }
   }
-  float d = 0.0f, top = 0.0f, sum = 1.0f;
-  float z[kItems];
-  const bool dense = softmax && !a.renorm;
-  if (dense) {
+  float v[I];
+  float top = 0.0f, inv = 0.0f;
+  if (dense) {                                    // v: the scores
+    load_run<DT, I>(a.logits, t * E, E, first, run, live, wide, v);
     top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int e = lane + i * kWave;
-      z[i] = e < E ? logit<DT>(a.logits, t * E + e) : -INFINITY;
-      z[i] = z[i] > -INFINITY ? fminf(z[i], 3.402823466e38f) : -INFINITY;
-      top = fmaxf(top, z[i]);
-    }
-    top = wave_max(top);
-    sum = 0.0f;
+    for (int i = 0; i < I; ++i) top = fmaxf(top, v[i]);
+    top = row_max(top);
+    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) sum += z[i] > -INFINITY ? expf(z[i] - top) : 0.0f;
-    sum = wave_sum(sum);
+    for (int i = 0; i < I; ++i) {
+      v[i] = v[i] > -INFINITY ? expf(v[i] - top) : 0.0f;
+      sum += v[i];
+    }
+    sum = row_sum(sum);
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   }
+  float d = 0.0f;
   if (a.renorm) {
     const float ls = id >= 0 ? log_score(a.score, zj) : -INFINITY;
-    const float m = wave_max(ls);
+    const float m = row_max(ls);
     float p = id >= 0 ? expf(ls - m) : 0.0f;
-    const float total = wave_sum(p);
+    const float total = row_sum(p);
     p = id >= 0 ? p / total : 0.0f;
-    const float mean = wave_sum(p * q);
+    const float mean = row_sum(p * q);
     d = p * (q - mean);
   } else if (id >= 0) {
-    d = q * (softmax ? expf(zj - top) / sum : sigmoidf(zj));
+    d = q * (softmax ? expf(zj - top) * inv : sigmoidf(zj));
   }
   if (!softmax && id >= 0) d *= sigmoidf(-zj);
-  const float pull = dense ? wave_sum(d) : 0.0f;
+  const float pull = dense ? row_sum(d) * inv : 0.0f;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const int e = lane + i * kWave;
-    if (i * kWave >= E) break;                    // uniform
-    float v = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int oj = __shfl(id, j);
-      const float dj = __shfl(d, j);
-      if (oj == e) v += dj;
-    }
-    if (dense && z[i] > -INFINITY) v -= expf(z[i] - top) / sum * pull;
-    if (e < E) put<DT>(dz, t * E + e, v);
+  for (int i = 0; i < I; ++i) v[i] = dense ? -v[i] * pull : 0.0f;
+  // the choices in ascending j
+#define EP_CHOICE(J)                                   \
+  if ((J) < k) {                                       \
+    const int e = dpp<kBcast + (J)>(id) - first;       \
+    const float dj = dpp<kBcast + (J)>(d);             \
+    _Pragma("unroll") for (int i = 0; i < I; ++i) v[i] += e == i ? dj : 0.0f; \
   }
+  EP_CHOICE(0) EP_CHOICE(1) EP_CHOICE(2) EP_CHOICE(3) EP_CHOICE(4) EP_CHOICE(5) EP_CHOICE(6) EP_CHOICE(7)
+  EP_CHOICE(8) EP_CHOICE(9) EP_CHOICE(10) EP_CHOICE(11) EP_CHOICE(12) EP_CHOICE(13) EP_CHOICE(14) EP_CHOICE(15)
+#undef EP_CHOICE
+  if (!live) return;
+  constexpr int kVec = DT == EP_FLOAT_F32 ? 4 : 8;
+  if constexpr (I >= kVec) {
+    if (wide) {
+#pragma unroll
+      for (int q0 = 0; q0 < I / kVec; ++q0) {
+        if (q0 * kVec >= run || first + q0 * kVec >= E) break;
+        u32x4 w;
+        if constexpr (DT == EP_FLOAT_F32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[q0 * 4 + i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = v[q0 * kVec + (2 * i) % kVec], hi = v[q0 * kVec + (2 * i + 1) % kVec];
+            if constexpr (DT == EP_FLOAT_BF16) {
+              w[i] = pack_bf16x2(lo, hi);
+            } else {
+              w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
+                     (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+            }
+          }
+        }
+        *(u32x4 *)((char *)dz + (t * E + first + q0 * kVec) * (16 / kVec)) = w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+    if (i < run && first + i < E) put<DT>(dz, t * E + first + i, v[i]);
 }
 
+// A lane's run of experts, and whether every run of every row starts on 16 bytes.
+int run_of(int E) { return (E + kRow - 1) / kRow; }
+bool wide_rows(const void *p, int dtype, int E, int run) {
+  const int vec = dtype == EP_FLOAT_F32 ? 4 : 8;
+  return (uintptr_t)p % 16 == 0 && E % vec == 0 && run % vec == 0;
+}
+
+template <int DT, int I>
+hipError_t router_i(const RouterArgs &a, void *idx, int idx64, float *weights, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kThreads);
+  const int run = run_of(a.E);
+  const int wide = (wide_rows(a.logits, DT, a.E, run) ? 1 : 0) |
+                   ((uintptr_t)a.bias % 16 == 0 && a.E % 4 == 0 && run % 4 == 0 ? 2 : 0);
+  if (a.k <= 8)
+    hipLaunchKernelGGL((row_router_kernel<DT, I, 8>), grid, block, 0, s, a, idx, idx64, weights, run, wide);
+  else
+    hipLaunchKernelGGL((row_router_kernel<DT, I, 16>), grid, block, 0, s, a, idx, idx64, weights, run, wide);
+  return hipGetLastError();
+}
 template <int DT>
 hipError_t router_dt(const RouterArgs &a, void *idx, int idx64, float *weights, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kTokens * kWave);
-  if (idx64)
-    hipLaunchKernelGGL((router_kernel<DT, int64_t>), grid, block, 0, s, a, (int64_t *)idx, weights);
-  else
-    hipLaunchKernelGGL((router_kernel<DT, int32_t>), grid, block, 0, s, a, (int32_t *)idx, weights);
+  // groups of whole lanes: E / 16 experts a lane, 16 / groups lanes a group
+  if (a.groups > 1 && (a.E % kRow != 0 || kRow % a.groups != 0)) {
+    const dim3 grid((unsigned)((a.T + kWaves - 1) / kWaves)), block(kThreads);
+    hipLaunchKernelGGL(wave_router_kernel<DT>, grid, block, 0, s, a, idx, idx64, weights);
+    return hipGetLastError();
+  }
+  const int run = run_of(a.E);
+  if (run <= 4) return router_i<DT, 4>(a, idx, idx64, weights, s);
+  if (run <= 8) return router_i<DT, 8>(a, idx, idx64, weights, s);
+  if (run <= 16) return router_i<DT, 16>(a, idx, idx64, weights, s);
+  return router_i<DT, 32>(a, idx, idx64, weights, s);
+}
+template <int DT, int I>
+hipError_t backward_i(const RouterArgs &a, const void *idx, int idx64, const float *grad, void *dz, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kThreads);
+  const int run = run_of(a.E);
+  const int wide = wide_rows(a.logits, DT, a.E, run) && wide_rows(dz, DT, a.E, run);
+  hipLaunchKernelGGL((router_backward_kernel<DT, I>), grid, block, 0, s, a, idx, idx64, grad, dz, run, wide);
   return hipGetLastError();
 }
 template <int DT>
 hipError_t backward_dt(const RouterArgs &a, const void *idx, int idx64, const float *grad, void *dz, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + kTokens - 1) / kTokens)), block(kTokens * kWave);
-  if (idx64)
-    hipLaunchKernelGGL((router_backward_kernel<DT, int64_t>), grid, block, 0, s, a, (const int64_t *)idx, grad, dz);
-  else
-    hipLaunchKernelGGL((router_backward_kernel<DT, int32_t>), grid, block, 0, s, a, (const int32_t *)idx, grad, dz);
-  return hipGetLastError();
+  const int run = run_of(a.E);
+  if (run <= 4) return backward_i<DT, 4>(a, idx, idx64, grad, dz, s);
+  if (run <= 8) return backward_i<DT, 8>(a, idx, idx64, grad, dz, s);
+  if (run <= 16) return backward_i<DT, 16>(a, idx, idx64, grad, dz, s);
+  return backward_i<DT, 32>(a, idx, idx64, grad, dz, s);
 }
 
 }  // namespace

@@ -160,3 +160,35 @@ def test_no_tokens(ep):
     idx, w = torch.zeros(0, 2, dtype=torch.int64, device=DEV), torch.zeros(0, 2, device=DEV)
     ep.ep_router(z, idx, w)
     ep.ep_router_backward(z, idx, w, torch.zeros_like(z))
+
+
+@pytest.mark.parametrize("E,groups", [(256, 8), (256, 2), (64, 4), (128, 16), (60, 5), (512, 64)])
+@pytest.mark.parametrize("top", [1, 2])
+def test_equal_groups(ep, E, groups, top):
+    """Groups of equal rank: the lower ones stay; a better one anywhere comes first."""
+    keep = max(1, groups // 2)
+    for bias in (None, torch.zeros(E)):
+        for score in ("softmax", "sigmoid"):
+            z = torch.zeros(groups + 1, E)
+            for g in range(groups):
+                z[g, g * (E // groups):(g + 1) * (E // groups)] = 1.0
+            _check(ep, z, min(16, E // groups * keep), score=score, bias=bias, num_groups=groups, topk_groups=keep,
+                   group_top=top)
+
+
+@pytest.mark.parametrize("T", [1, 15, 16, 17, 1000])
+def test_many_tokens_grouped(ep, T):
+    g = np.random.default_rng(T)
+    z = torch.from_numpy(g.normal(size=(T, 256)) * 1.5).float()
+    bias = torch.from_numpy(g.normal(size=256) * 0.1).float()
+    _check(ep, z, 8, torch.int32, score="sigmoid", bias=bias, num_groups=8, topk_groups=4, group_top=2, scale=2.5)
+    _check(ep, z.bfloat16(), 9, torch.int64, score="softmax", bias=bias, renormalize=False)
+    # strided storage is refused, an unaligned start is not
+    big = torch.zeros(T * 256 + 1)
+    big[1:] = z.reshape(-1)
+    zu = big.to(DEV)[1:].view(T, 256)
+    idx, w = torch.empty(T, 8, dtype=torch.int64, device=DEV), torch.empty(T, 8, device=DEV)
+    ep.ep_router(zu, idx, w)
+    assert np.array_equal(idx.cpu().numpy(), OR.route(z.double().numpy(), 8)[0])
+    with pytest.raises(ep.EpError):
+        ep.ep_router(torch.zeros(256, max(T, 2), device=DEV).t(), idx, w)
