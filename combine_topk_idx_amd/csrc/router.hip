@@ -13,17 +13,17 @@
 // An expert whose logit or key is -inf or NaN is never chosen.
 //
 // Two keys s_e + bias_e may lie closer than float32 rounding, and then the
-// order would depend on how exp was evaluated.  The order is therefore that
-// of float64 keys: the fast path ranks float32 keys and checks that every
-// gap that matters is wider than their error; a wave that finds a closer one
-// ranks its tokens again with float64 keys.
+// order would depend on how exp was evaluated; keys with a bias and sums of
+// two scores are therefore float64, to 43 significant bits.
 //
-// Fast path: 16 lanes take a token (four tokens a wave), each a run of
-// ceil(E / 16) experts.  A key and its expert are one double (the expert in
-// the low mantissa bits, so that all are different and ties go to the lower
-// id), which v_max_f64 / v_min_f64 compare at full rate: every lane sorts its
-// run in registers, then four exchange steps inside the 16 lanes merge the
+// 16 lanes take a token (four tokens a wave), each a run of ceil(E / 16)
+// experts.  A key and its expert are one double (the expert in the low
+// mantissa bits, so that all are different and ties go to the lower id),
+// which v_max_f64 / v_min_f64 compare at full rate: every lane sorts its run
+// in registers, then four exchange steps inside the 16 lanes merge the
 // lanes' best lists.  No LDS, no loop over the k choices.
+//
+// Bound by its instructions, not by the logits' bytes.
 #include <math.h>
 
 #include "common.hpp"
@@ -53,7 +53,7 @@ __device__ __forceinline__ void put(void *p, int64_t i, float v) {
   else ((_Float16 *)p)[i] = (_Float16)v;
 }
 // NaN and -inf: no expert (-inf); +inf: the largest finite logit
-__device__ __forceinline__ float usable(float z) { return z > -INFINITY ? fminf(z, kLargest) : -INFINITY; }
+__device__ __forceinline__ float usable(float z) { return fminf(fmaxf(z, -INFINITY), kLargest); }
 
 // This lane's run of `run` logits, [first, first + run) of a row of E (which
 // starts at element `row`); -inf past them.  16-byte loads where every run
@@ -89,17 +89,17 @@ __device__ __forceinline__ void load_run(const void *p, int64_t row, int E, int 
 // ------------------------------------------------ exchanges in 16 lanes
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
 }
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
 }
 template <int CTRL>
 __device__ __forceinline__ double dpp(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, true);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kRor4 = 0x124, kRor8 = 0x128;   // quad swaps, rotations by 4 and 8
@@ -137,25 +137,62 @@ __device__ __forceinline__ T row_sum(T v) {
 }
 
 // -------------------------------------------------------- packed keys
-// A key of at most 44 significant bits with its expert in the 9 low mantissa
-// bits: among equal keys the lower expert is the larger double.  No key: -inf.
+// A key (its first 44 significant bits) with its expert in the 9 low
+// mantissa bits: among equal keys the lower expert is the larger double.  An
+// expert that is not there has the key kNoKey (a finite one, so that the low
+// bits make no NaN of it).
+constexpr double kNoKey = -1e300;
 __device__ __forceinline__ double pack_key(double key, int e) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, key + 0.0);   // -0 becomes +0
-  const uint64_t low = (u >> 63) ? (uint64_t)e : (uint64_t)(kMaxExperts - 1 - e);
-  const double r = __builtin_bit_cast(double, (u & ~(uint64_t)(kMaxExperts - 1)) | low);
-  return key > -INFINITY ? r : -INFINITY;
+  const uint64_t u = __builtin_bit_cast(uint64_t, key);
+  const uint32_t hi = (uint32_t)(u >> 32), sign = (uint32_t)((int32_t)hi >> 31);
+  const uint32_t low = ((uint32_t)(kMaxExperts - 1 - e) ^ sign) & (kMaxExperts - 1);
+  const uint32_t lo = ((uint32_t)u & ~(uint32_t)(kMaxExperts - 1)) | low;
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ int expert_in(double packed) {
   const uint64_t u = __builtin_bit_cast(uint64_t, packed);
-  const int low = (int)(u & (kMaxExperts - 1));
-  return (u >> 63) ? low : kMaxExperts - 1 - low;
+  const uint32_t sign = (uint32_t)((int32_t)(u >> 32) >> 31);
+  return kMaxExperts - 1 - (int)(((uint32_t)u ^ sign) & (kMaxExperts - 1));
 }
+__device__ __forceinline__ bool is_key(double packed) { return packed > kNoKey * 0.5; }
 __device__ __forceinline__ double key_in(double packed) {
-  return packed > -INFINITY
-             ? __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, packed) & ~(uint64_t)(kMaxExperts - 1))
-             : packed;
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, packed) & ~(uint64_t)(kMaxExperts - 1));
 }
 static_assert((kMaxExperts & (kMaxExperts - 1)) == 0, "the expert is a bit field");
+
+// e^x for x <= 700 or so, to 2^-46 of it: 2^n times the Taylor series of e^r,
+// |r| <= ln 2 / 2, whose 12th term is below 2^-47; 0 below e^-745.  The
+// coefficients are held in scalar registers (as literals each costs two
+// moves a use, a quarter of the kernel's instructions).
+__device__ __forceinline__ double scalar(double c) {
+  asm("" : "+s"(c));
+  return c;
+}
+__device__ __forceinline__ double exp64(double x) {
+  const double n = rint(x * scalar(1.4426950408889634));
+  const double r = fma(n, scalar(-0.6931471805599453), x);
+  double p = 1.0 / 39916800;
+  p = fma(p, r, scalar(1.0 / 3628800));
+  p = fma(p, r, scalar(1.0 / 362880));
+  p = fma(p, r, scalar(1.0 / 40320));
+  p = fma(p, r, scalar(1.0 / 5040));
+  p = fma(p, r, scalar(1.0 / 720));
+  p = fma(p, r, scalar(1.0 / 120));
+  p = fma(p, r, scalar(1.0 / 24));
+  p = fma(p, r, scalar(1.0 / 6));
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)n);
+}
+// 1 / x of a normal x: the hardware's approximation and two Newton steps
+__device__ __forceinline__ double rcp64(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+  y = fma(y, fma(-x, y, 1.0), y);
+  return fma(y, fma(-x, y, 1.0), y);
+}
+// sigmoid; e^-z is kept in double's range (beyond it the score is 0 to 2^-999)
+__device__ __forceinline__ double sigmoid64(float z) { return rcp64(1.0 + exp64(fmin(-(double)z, 690.0))); }
 
 // Batcher's odd-even merge sort, descending; n a power of two.
 template <int N>
@@ -203,8 +240,8 @@ __device__ __forceinline__ float log_score(int score, float z) {
 __device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(-z)); }
 
 // ------------------------------------------------------------ wave path
-// One token per wave with float64 keys in LDS: group shapes that do not fall
-// on whole lanes, and the tokens whose float32 keys lie too close.
+// One token per wave with its keys in LDS: group shapes that do not fall on
+// whole lanes.
 struct WaveLds {
   double key[kMaxExperts], rank[kMaxGroups];
 };
@@ -370,8 +407,7 @@ __global__ __launch_bounds__(kThreads) void wave_router_kernel(RouterArgs a, voi
 template <int DT, int I, int L>
 __global__ __launch_bounds__(kThreads) void row_router_kernel(RouterArgs a, void *idx, int idx64, float *weights,
                                                               int run, int wide) {
-  __shared__ WaveLds s_wave[kWaves];
-  const int j = threadIdx.x & (kRow - 1), wv = threadIdx.x / kWave;
+  const int j = threadIdx.x & (kRow - 1);
   const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / kRow;
   const bool live = t < a.T;
   const bool softmax = a.score == EP_SCORE_SOFTMAX, biased = a.bias != nullptr;
@@ -384,27 +420,15 @@ __global__ __launch_bounds__(kThreads) void row_router_kernel(RouterArgs a, void
 #pragma unroll
     for (int i = 0; i < I; ++i) top = fmaxf(top, z[i]);
     top = row_max(top);
-    if (biased || !a.renorm) {
+    if (!a.renorm) {
       sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < I; ++i) sum += z[i] > -INFINITY ? expf(z[i] - top) : 0.0f;
       sum = row_sum(sum);
     }
   }
-  // Keys.  What float32 may do to a score s (v_exp_f32 and v_rcp_f32 within
-  // 1 ulp, the product with log2 e in the exponent): a sigmoid is off by at
-  // most s ((1 - s) (|z| 2^-23.4 + 2^-23) + 2^-24 + 2^-23) < 2^-22, two of
-  // them by 2^-21; a softmax's terms by less than that, its sum (at most 36
-  // additions one after another) by 2^-18.8 of itself, which is common to
-  // the row: 2^-18 of the largest score for a difference.  The sum with the
-  // bias adds 2^-24 |key| each.  Keys further apart than
-  // off + 2^-22 |key| are in float64's order.
   double v[I];
-  float off = 0x1p-21f;
   if (biased) {
-    const float inv = softmax ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-    if (softmax) off = 0x1p-18f * inv;
-    constexpr float kLog2e = 1.44269504f;
     float bias[I];
     if (wide & 2) {                               // uniform
 #pragma unroll
@@ -417,25 +441,33 @@ __global__ __launch_bounds__(kThreads) void row_router_kernel(RouterArgs a, void
 #pragma unroll
       for (int i = 0; i < I; ++i) bias[i] = a.bias[min(first + i, a.E - 1)];
     }
+    double by = 1.0;
+    if (softmax) {
+      double sum64 = 0.0;
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        v[i] = z[i] > -INFINITY ? exp64(fmax((double)z[i] - (double)top, -700.0)) : 0.0;
+        sum64 += v[i];
+      }
+      by = rcp64(row_sum(sum64));
+    }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const float s = softmax ? __builtin_amdgcn_exp2f((z[i] - top) * kLog2e) * inv
-                              : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z[i] * -kLog2e));
-      const float c = z[i] > -INFINITY ? s + bias[i] : -INFINITY;
-      v[i] = pack_key((double)c, min(first + i, kMaxExperts - 1));
+      const double c = (softmax ? v[i] * by : sigmoid64(z[i])) + (double)bias[i];
+      // NaN fails the comparison; +inf is held below infinity, so that it stays a number
+      v[i] = pack_key(z[i] > -INFINITY && c > -1e299 ? fmin(c, 1e300) : kNoKey, first + i);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < I; ++i) v[i] = pack_key((double)z[i], min(first + i, kMaxExperts - 1));
+    for (int i = 0; i < I; ++i) v[i] = pack_key(z[i] > -INFINITY ? (double)z[i] + 0.0 : kNoKey, first + i);
   }
   sort_run(v);
 
-  bool close = false;                             // of this token, seen by some lane
   bool stays = true;
   if (a.groups > 1) {
     // a group is kRow / groups whole lanes: its two best keys from theirs
     const int lanes = kRow / a.groups;
-    double b0 = v[0], b1 = I > 1 ? v[I > 1 ? 1 : 0] : (double)-INFINITY;
+    double b0 = v[0], b1 = v[1];
     auto join = [&](double o0, double o1) {
       const double lo = min64(b0, o0);
       b0 = max64(b0, o0);
@@ -447,87 +479,41 @@ __global__ __launch_bounds__(kThreads) void row_router_kernel(RouterArgs a, void
     double rank = key_in(b0);
     if (a.top == 2) {
       if (biased) {
-        rank += key_in(b1);
+        rank = is_key(b1) ? rank + key_in(b1) : kNoKey;
       } else {
-        // sums of two scores, in float64 (a softmax's up to the row's factor)
-        const double k0 = key_in(b0), k1 = key_in(b1);
-        const bool both = k1 > -INFINITY;
-        rank = !both ? (double)-INFINITY
-               : softmax ? exp(k0 - (double)top) + exp(k1 - (double)top)
-                         : 1.0 / (1.0 + exp(-k0)) + 1.0 / (1.0 + exp(-k1));
+        // sums of two scores (a softmax's up to the row's factor)
+        const float k0 = (float)key_in(b0), k1 = (float)key_in(b1);
+        const double s = softmax ? exp64(fmax((double)k0 - (double)top, -700.0)) +
+                                       exp64(fmax((double)k1 - (double)top, -700.0))
+                                 : sigmoid64(k0) + sigmoid64(k1);
+        rank = is_key(b1) ? s : kNoKey;
       }
     }
     // a group stays when fewer than `keep` groups come before it
     const int mine = j / lanes;
     int before = 0;
-    double below = -INFINITY;                     // the best rank after this one
-    auto against = [&](double o, int og) {
-      const bool first_is = o > rank || (o == rank && og < mine);
-      before += first_is;
-      if (!first_is) below = max64(below, o);
-    };
-#define EP_ROT(R) \
-  if ((R) % lanes == 0) against(dpp<0x120 + (R)>(rank), ((j - (R)) & (kRow - 1)) / lanes)
-    EP_ROT(1); EP_ROT(2); EP_ROT(3); EP_ROT(4); EP_ROT(5); EP_ROT(6); EP_ROT(7); EP_ROT(8);
-    EP_ROT(9); EP_ROT(10); EP_ROT(11); EP_ROT(12); EP_ROT(13); EP_ROT(14); EP_ROT(15);
+#define EP_ROT(R)                                                    \
+  if ((R) % lanes == 0) {                                            \
+    const double o = dpp<0x120 + (R)>(rank);                         \
+    before += o > rank || (o == rank && ((j - (R)) & (kRow - 1)) / lanes < mine); \
+  }
+    EP_ROT(1) EP_ROT(2) EP_ROT(3) EP_ROT(4) EP_ROT(5) EP_ROT(6) EP_ROT(7) EP_ROT(8)
+    EP_ROT(9) EP_ROT(10) EP_ROT(11) EP_ROT(12) EP_ROT(13) EP_ROT(14) EP_ROT(15)
 #undef EP_ROT
     stays = before < a.keep;
-    // the last kept group against the first one dropped
-    if (biased) {
-      const float k0 = (float)key_in(b0), k1 = (float)key_in(b1);
-      const float size = row_max(fmaxf(k0 > -INFINITY ? fabsf(k0) : 0.0f, k1 > -INFINITY ? fabsf(k1) : 0.0f));
-      if (before == a.keep - 1 && a.keep < a.groups)
-        close = !(rank - below > 2.0 * (double)(off + 0x1p-22f * size));
-    }
   }
 
   double best[L];
 #pragma unroll
-  for (int i = 0; i < L; ++i) best[i] = i < I && stays ? v[i < I ? i : 0] : (double)-INFINITY;
+  for (int i = 0; i < L; ++i) best[i] = i < I && stays ? v[i < I ? i : 0] : kNoKey;
   merge_step<kXor1>(best);
   merge_step<kXor2>(best);
   merge_step<kRor4>(best);
   merge_step<kRor8>(best);
-
-  double mine = best[0], kth = best[0];
+  double mine = best[0];
 #pragma unroll
-  for (int i = 1; i < L; ++i) {
-    if (j == i) mine = best[i];
-    if (i < a.k) kth = best[i];                   // uniform
-  }
-  int id = j < a.k && mine > -INFINITY ? expert_in(mine) : -1;
-  if (biased) {
-    // gaps inside the list, and from its end to the best key left out
-    float gap = INFINITY, size = 0.0f;
-#pragma unroll
-    for (int i = 0; i + 1 < L; ++i)
-      if (i + 1 < a.k && best[i + 1] > -INFINITY) {
-        gap = fminf(gap, (float)(key_in(best[i]) - key_in(best[i + 1])));
-        size = fmaxf(size, fabsf((float)best[i + 1]));
-      }
-    double next = -INFINITY;
-    if (stays) {
-#pragma unroll
-      for (int i = 0; i < I; ++i) next = max64(next, v[i] < kth ? v[i] : (double)-INFINITY);
-    }
-    next = row_max(next);
-    if (kth > -INFINITY && next > -INFINITY) {
-      gap = fminf(gap, (float)(key_in(kth) - key_in(next)));
-      size = fmaxf(size, fabsf((float)kth));
-    }
-    size = fmaxf(size, fabsf((float)(best[0] > -INFINITY ? best[0] : 0.0)));
-    close |= !(gap > off + 0x1p-22f * size);
-    uint64_t again = __ballot(close && live);
-    while (again) {                               // uniform: a token with close keys, by the whole wave
-      const int lane = threadIdx.x & (kWave - 1);
-      const int r = (__builtin_ffsll((long long)again) - 1) / kRow;
-      again &= ~(0xffffull << (r * kRow));
-      const int64_t tr = (int64_t)blockIdx.x * kTokens + (threadIdx.x / kWave) * (kWave / kRow) + r;
-      const int got = wave_route<DT>(a, tr, s_wave[wv]);
-      const int mine_of = __shfl(got, j);
-      if (lane / kRow == r) id = mine_of;
-    }
-  }
+  for (int i = 1; i < L; ++i) mine = j == i ? best[i] : mine;
+  const int id = j < a.k && is_key(mine) ? expert_in(mine) : -1;
   store_choice<DT>(a, t, j, live, id, top, sum, idx, idx64, weights);
 }
 
