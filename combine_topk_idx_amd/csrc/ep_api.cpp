@@ -608,7 +608,7 @@ ep_status_t check_lora(const char *fn, const ep_handle_t *h, int32_t in, int32_t
   if (scale && !aligned(scale, 4)) return fail(EP_ERR_INVALID_ARG, "%s: scale is misaligned", fn);
   if (!workspace || !aligned(workspace, ep::kWsAlign))
     return fail(EP_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
-  const size_t need = ep::lora_ws(h->num_tokens, in, out, rank, h->num_experts, backward).total;
+  const size_t need = ep::lora_ws(ep::lora_rows(*h), in, out, rank, h->num_experts, backward).total;
   if (workspace_bytes < need)
     return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
   return EP_OK;
@@ -664,14 +664,14 @@ ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num
   return EP_OK;
 }
 
-size_t ep_lora_workspace_bytes(int64_t num_max_tokens, int32_t in_features, int32_t out_features, int32_t rank,
+size_t ep_lora_workspace_bytes(int64_t rows, int32_t in_features, int32_t out_features, int32_t rank,
                                int32_t num_adapters, int32_t backward) {
-  if (num_max_tokens < 0 || num_max_tokens > INT32_MAX || in_features <= 0 || in_features % 32 != 0 ||
+  if (rows < 0 || rows > INT32_MAX || in_features <= 0 || in_features % 32 != 0 ||
       in_features > kMaxHidden || out_features <= 0 || out_features % 32 != 0 || out_features > kMaxHidden || rank < 8 ||
       rank > ep::kMaxRank || rank % 8 != 0 || num_adapters <= 0 || num_adapters > ep::kMaxExperts ||
       (backward != 0 && backward != 1))
     return 0;
-  return ep::lora_ws(num_max_tokens, in_features, out_features, rank, num_adapters, backward).total;
+  return ep::lora_ws(rows, in_features, out_features, rank, num_adapters, backward).total;
 }
 
 ep_status_t ep_lora(const ep_handle_t *handle, const void *x, int32_t in_features, int32_t out_features,

@@ -12,12 +12,12 @@
 // once and the bytes of x, base, out and their gradients bound the time.  The
 // layout gives each adapter's tokens as one run of rows; a work item is up
 // to 32 of them.
-//   down   (v, u): a workgroup takes an item and a share of the reduction
-//          axis, split again over its waves; the shares' partial sums go to the
-//          workspace in float32 and are added in a fixed order by the reader.
-//   up     (out, dx): a workgroup takes an item and a block of columns.  The
-//          float32 v is cut into bf16 high and low parts (16 significant bits)
-//          for the matrix cores.
+//   down   (v, u): a workgroup takes an item, its waves share the reduction
+//          axis and their sums are added through LDS.  It leaves v in float32
+//          for the caller and, times the scale, cut into bf16 high and low
+//          parts (16 significant bits) in the operand order of
+//   up     (out, dx): a workgroup takes 64 (32) rows and a block of columns, whose
+//          part of B (A) it holds in registers.
 //   outer  (dA, dB): a workgroup takes an adapter and a block of columns and
 //          walks the adapter's rows, its waves sharing them out; the float32
 //          factor is cut into three bf16 parts (24 bits), so the products are
@@ -35,114 +35,216 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
-constexpr int kTile = 32;                         // rows of a work item
+constexpr int kTile = 32;                         // rows of a down product's work item
+constexpr int kPer = kMaxExperts / kWave;         // adapters per lane of a search, at most
 
 struct Item {
-  int expert, row0, n;                            // expert -1: none; n rows, 1 .. kTile
+  int expert, row0, n;                            // expert -1: none; rows [row0, row0 + n)
+  int pieces, slot;                               // the adapter's items; partial slot of its first one
 };
 
-// The `item`-th work item: every adapter's block cut into tiles of kTile
-// rows, in adapter order.  Rows past an adapter's tokens (padded blocks) have
-// row_src -1; a tile that starts on one is empty (n = 0).
-__device__ __forceinline__ Item find_item(const int *__restrict__ offsets, int N, int item) {
-  __shared__ int s_wave[kWaves];
-  __shared__ Item s_found;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
-  const int rows = tid < N ? offsets[tid + 1] - offsets[tid] : 0;   // kMaxExperts == kThreads
-  const int mine = (rows + kTile - 1) / kTile;
-  int upto = mine;
+// The `item`-th work item: every adapter's block of rows cut into pieces of
+// `tile`, in adapter order; with `empty` an adapter without rows has one item
+// of none.  Slots count the pieces of the adapters that have several.  Every
+// wave searches by itself (no LDS, no barrier): a lane takes one adapter, or
+// kPer of them where there are more than 64.
+template <int PER>
+__device__ __forceinline__ Item find_item_per(const int *__restrict__ offsets, int N, int tile, bool empty, int item) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int start[PER + 1], mine = 0, split = 0;
+#pragma unroll
+  for (int i = 0; i <= PER; ++i) start[i] = offsets[min(lane * PER + i, N)];
+  int pieces[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int rows = start[i + 1] - start[i];
+    pieces[i] = (rows + tile - 1) / tile;
+    if (empty && lane * PER + i < N) pieces[i] = max(pieces[i], 1);
+    mine += pieces[i];
+    split += pieces[i] > 1 ? pieces[i] : 0;
+  }
+  int upto = mine, slots = split;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
-    const int o = __shfl_up(upto, d);
-    if (lane >= d) upto += o;
+    const int o = __shfl_up(upto, d), q = __shfl_up(slots, d);
+    if (lane >= d) { upto += o; slots += q; }
   }
-  if (lane == kWave - 1) s_wave[wv] = upto;
-  if (tid == 0) s_found.expert = -1;
-  __syncthreads();
-  for (int w = 0; w < wv; ++w) upto += s_wave[w];
-  const int at = item - (upto - mine);
-  if (at >= 0 && at < mine) {
-    s_found.expert = tid;
-    s_found.row0 = offsets[tid] + at * kTile;
-    s_found.n = min(kTile, rows - at * kTile);
-  }
-  __syncthreads();
   Item it;
-  it.expert = __builtin_amdgcn_readfirstlane(s_found.expert);
-  it.row0 = __builtin_amdgcn_readfirstlane(s_found.row0);
-  it.n = __builtin_amdgcn_readfirstlane(s_found.n);
+  it.expert = -1;
+  const uint64_t past = __ballot(upto > item);
+  if (past == 0) return it;                       // uniform
+  const int owner = __builtin_ffsll((long long)past) - 1;
+  int at = item - (upto - mine), slot = slots - split, e = -1, row0 = 0, n = 0, pc = 0, sl = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (e < 0 && at < pieces[i]) {
+      e = lane * PER + i;
+      row0 = start[i] + at * tile;
+      n = min(tile, start[i + 1] - row0);
+      pc = pieces[i];
+      sl = slot + at;
+    }
+    at -= pieces[i];
+    slot += pieces[i] > 1 ? pieces[i] : 0;
+  }
+  it.expert = __builtin_amdgcn_readlane(e, owner);
+  it.row0 = __builtin_amdgcn_readlane(row0, owner);
+  it.n = __builtin_amdgcn_readlane(n, owner);
+  it.pieces = __builtin_amdgcn_readlane(pc, owner);
+  it.slot = __builtin_amdgcn_readlane(sl, owner);
   return it;
 }
-static_assert(kMaxExperts == kThreads, "one adapter per thread");
+__device__ __forceinline__ Item find_item(const int *__restrict__ offsets, int N, int tile, bool empty, int item) {
+  return N <= kWave ? find_item_per<1>(offsets, N, tile, empty, item)
+                    : find_item_per<kPer>(offsets, N, tile, empty, item);
+}
 
+// Operands of the 16 x 16 x 32 step: lane (c = l % 16, g = l / 16) holds K
+// [8 g, 8 g + 8) of row / column c; its sums are column c, rows 4 g + i.
+__device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 __device__ __forceinline__ v16f mfma(const bf16x8 &a, const bf16x8 &b, const v16f &c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Down product: part[split][t][r] = sum over this split's share of
-// w[e][r][i] rows[t][i].  MF: 32-row blocks of the rank.
-template <int MF>
-__global__ __launch_bounds__(kThreads) void down_kernel(const int *__restrict__ offsets,
+// Down product: v[r] = sum over i of w[e][r][i] rows[t][i], t the token of the
+// layout's row.  MF: 16-row blocks of the rank; W: waves.
+//
+// A wave takes every W-th 64-wide step.  In the matrix cores' operand order 16
+// consecutive lanes hold 16 rows, and a load in that order makes one cache
+// access a lane (16 bytes a clock and CU, which bounded the kernel); so eight
+// lanes read a row's 128-byte line, and the order is changed through LDS the
+// wave has to itself (no barrier).  Chunk q of row r lies at place q ^ (r & 7)
+// of its line there: reads of 8 rows fall in distinct banks.
+template <int MF, int W>
+__global__ __launch_bounds__(W *kWave) void down_kernel(const int *__restrict__ offsets,
                                                         const int *__restrict__ row_src, int N,
                                                         const uint16_t *__restrict__ rows, int K,
-                                                        const uint16_t *__restrict__ w, int R, int splits, int64_t T,
-                                                        float *__restrict__ part) {
-  __shared__ __attribute__((aligned(16))) float s_tile[kWaves * 16 * kWave];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave, c = lane & 31, g = lane >> 5;
+                                                        const uint16_t *__restrict__ w, int R,
+                                                        const float *__restrict__ scale, int scaled,
+                                                        float *__restrict__ sum, uint16_t *__restrict__ operand,
+                                                        int splits, int64_t max_rows, float *__restrict__ part) {
+  constexpr int kLines = 32 + 16 * MF;            // rows of a step: the tokens', then w's
+  constexpr int kLoads = kLines / 8;
+  constexpr int kRing = MF <= 4 ? 2 : 1;          // steps in flight
+  constexpr int kStage = W * kLines * 8, kSums = 4 * W * kWave;
+  __shared__ __attribute__((aligned(16))) u32x4 s_mem[kStage > kSums ? kStage : kSums];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % splits;
-  const Item it = find_item(offsets, N, blockIdx.x / splits);
+  const Item it = find_item(offsets, N, kTile, false, blockIdx.x / splits);
   if (it.expert < 0) return;                      // uniform
-  const int first = row_src[it.row0];
+  // token of row `lane` of the tile; rows past the tile and of padding: -1
+  const int src = (lane & 31) < it.n ? row_src[it.row0 + (lane & 31)] : -1;
+  const int first = __builtin_amdgcn_readfirstlane(src);
   if (first < 0) return;                          // uniform: a tile of padding
-  const int own = c < it.n ? row_src[it.row0 + c] : -1;
-  const uint16_t *x = rows + (size_t)(own < 0 ? first : own) * K + g * 16;
-  const uint16_t *a[MF];
+  // load i: line 8 i + lane / 8, chunk lane % 8
+  const uint16_t *line[kLoads];
+  int chunk = lane & 7;
 #pragma unroll
-  for (int f = 0; f < MF; ++f) a[f] = w + ((size_t)it.expert * R + min(f * 32 + c, R - 1)) * K + g * 16;
-  const int steps = K / 32, parts = splits * kWaves, me = split * kWaves + wv;
-  const int s0 = (int)((int64_t)steps * me / parts), s1 = (int)((int64_t)steps * (me + 1) / parts);
-  v16f acc[MF];
-#pragma unroll
-  for (int f = 0; f < MF; ++f) acc[f] = v16f{};
-#pragma unroll 4
-  for (int s = s0; s < s1; ++s) {
-    const bf16x8 b0 = *(const bf16x8 *)(x + s * 32), b1 = *(const bf16x8 *)(x + s * 32 + 8);
-#pragma unroll
-    for (int f = 0; f < MF; ++f) {
-      acc[f] = mfma(*(const bf16x8 *)(a[f] + s * 32), b0, acc[f]);
-      acc[f] = mfma(*(const bf16x8 *)(a[f] + s * 32 + 8), b1, acc[f]);
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    if (i < 4) {
+      const int t = __shfl(src, r & 31);
+      line[i] = rows + (size_t)(t < 0 ? first : t) * K + chunk * 8;
+    } else {
+      line[i] = w + ((size_t)it.expert * R + min(r - 32, R - 1)) * K + chunk * 8;
     }
   }
-  // lane (c, g) holds token c, ranks 8 b + 4 g + i of each 32-row block
+  u32x4 *mine = s_mem + wv * kLines * 8;
+  const int all = K / 64, s_lo = (int)((int64_t)all * split / splits);   // this split's steps
+  const int steps = (int)((int64_t)all * (split + 1) / splits) - s_lo;
+  f32x4 acc[MF][2];
 #pragma unroll
-  for (int f = 0; f < MF; ++f) {
-    if (f > 0) __syncthreads();
+  for (int f = 0; f < MF; ++f)
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      *(f32x4 *)(s_tile + ((wv * 4 + b) * kWave + lane) * 4) =
-          f32x4{acc[f][4 * b], acc[f][4 * b + 1], acc[f][4 * b + 2], acc[f][4 * b + 3]};
+    for (int h = 0; h < 2; ++h) acc[f][h] = f32x4{};
+  u32x4 in[kRing][kLoads];
+  auto load = [&](int q, int s) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) in[q][i] = *(const u32x4 *)(line[i] + (s_lo + s) * 64);
+    keep_loads();
+  };
+  // the line's chunks [0, 4 M) are multiplied
+  auto multiply = [&](int q, int M) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) mine[(8 * i + (lane >> 3)) * 8 + (chunk ^ (lane >> 3))] = in[q][i];
+    auto operand_at = [&](int row, int m) {
+      return __builtin_bit_cast(bf16x8, mine[row * 8 + ((m * 4 + g) ^ (row & 7))]);
+    };
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (m >= M) break;                          // uniform
+      const bf16x8 x0 = operand_at(c, m), x1 = operand_at(16 + c, m);
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const bf16x8 a = operand_at(32 + 16 * f + c, m);
+        acc[f][0] = mfma(a, x0, acc[f][0]);
+        acc[f][1] = mfma(a, x1, acc[f][1]);
+      }
+    }
+  };
+  if (wv < steps) {                               // uniform
+#pragma unroll
+    for (int q = 0; q < kRing; ++q) load(q, min(wv + q * W, steps - 1));
+    // whole rings without a condition in them (a load whose value only a
+    // branch uses is moved into that branch), then the rest
+    int s = wv;
+    for (; s + (kRing - 1) * W < steps; s += kRing * W) {
+#pragma unroll
+      for (int q = 0; q < kRing; ++q) {
+        multiply(q, 2);
+        load(q, min(s + (q + kRing) * W, steps - 1));   // past the end: never used
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kRing - 1; ++q)
+      if (s + q * W < steps) multiply(q, 2);      // uniform
+  }
+  if (K % 64 != 0 && split == splits - 1 && wv == W - 1) {   // uniform: the last 32, twice in the line
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) in[0][i] = *(const u32x4 *)(line[i] + all * 64 - (chunk & 4) * 8);
+    multiply(0, 1);
+  }
+  __syncthreads();                                // the stages become the sums
+  f32x4 *s_tile = (f32x4 *)s_mem;                 // [tile of a round][wave][lane]
+  // a lane holds token c of half h, ranks 16 f + 4 g + i; waves 0..3 add up
+  // one of four (f, h) tiles each
+  const float sc = scale ? scale[it.expert] : 1.0f;
+  const int r16 = operand_ranks(R);
+#pragma unroll
+  for (int f0 = 0; f0 < MF; f0 += 2) {
+    if (f0 > 0) __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (f0 + (q >> 1) < MF) s_tile[(q * W + wv) * kWave + lane] = acc[f0 + (q >> 1) < MF ? f0 + (q >> 1) : 0][q & 1];
     __syncthreads();
-    if (tid < 4 * kWave) {
-      const int b = tid / kWave;
-      f32x4 v = *(const f32x4 *)(s_tile + (b * kWave + lane) * 4);
+    const int f = f0 + (wv >> 1), h = wv & 1;
+    if (wv < 4 && f * 16 < r16) {                 // uniform
+      f32x4 v = s_tile[wv * W * kWave + lane];
 #pragma unroll
-      for (int q = 1; q < kWaves; ++q) v += *(const f32x4 *)(s_tile + ((q * 4 + b) * kWave + lane) * 4);
-      const int r = f * 32 + 8 * b + 4 * g;
-      if (own >= 0 && r < R) *(f32x4 *)(part + ((size_t)split * T + own) * R + r) = v;
+      for (int q = 1; q < W; ++q) v += s_tile[(wv * W + q) * kWave + lane];
+      const int r = f * 16 + 4 * g, row = h * 16 + c, t = __shfl(src, row);
+      if (t >= 0 && splits > 1) {
+        if (r < R) *(f32x4 *)(part + ((size_t)split * max_rows + it.row0 + row) * R + r) = v;
+      } else if (t >= 0) {
+        if (r >= R) v = f32x4{};                  // ranks that fill up the operand
+        const f32x4 by = v * sc;
+        if (r < R) *(f32x4 *)(sum + (size_t)t * R + r) = scaled ? by : v;
+        uint16_t *to = operand + (size_t)(it.row0 + row) * 2 * r16 + f * 32 + 4 * g;
+        const u32x2 hi = {pack_bf16x2(by.x, by.y), pack_bf16x2(by.z, by.w)};
+        *(u32x2 *)to = hi;
+        *(u32x2 *)(to + 16) = u32x2{pack_bf16x2(by.x - bf16_lo(hi.x), by.y - bf16_hi(hi.x)),
+                                    pack_bf16x2(by.z - bf16_lo(hi.y), by.w - bf16_hi(hi.y))};
+      }
     }
   }
 }
 
-// x as bf16 parts x0 + x1 + x2 (each the rounding of what is left)
-__device__ __forceinline__ void split2(const float (&v)[8], bf16x8 &hi, bf16x8 &lo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = (__bf16)v[i];
-    lo[i] = (__bf16)(v[i] - (float)hi[i]);
-  }
-}
+// x as bf16 parts: each the rounding of what the ones before it leave
 __device__ __forceinline__ void split3(const float (&v)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -153,96 +255,170 @@ __device__ __forceinline__ void split3(const float (&v)[8], bf16x8 &hi, bf16x8 &
   }
 }
 
-// Up product: out[t] = base[t] + w[e] (s v[t]) over a block of kUpCols
-// columns; v[t] is the sum of the splits' partials, and the first column block
-// leaves it (times s if `scaled`) in `sum`.  RS: 16-rank steps.
-constexpr int kUpCols = 512;                      // columns of a workgroup: two 32-column tiles per wave
-template <int RS>
-__global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ offsets, const int *__restrict__ row_src,
-                                                      int N, const float *__restrict__ part, int splits, int64_t T,
-                                                      const uint16_t *__restrict__ w, int R,
-                                                      const float *__restrict__ scale, const uint16_t *base,
-                                                      uint16_t *out, int C, float *__restrict__ sum, int scaled,
-                                                      int blocks) {
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave, c = lane & 31, g = lane >> 5;
-  const int blk = blockIdx.x % blocks;
-  const Item it = find_item(offsets, N, blockIdx.x / blocks);
-  if (it.expert < 0) return;                      // uniform
-  const int own = c < it.n ? row_src[it.row0 + c] : -1;
-  const float sc = scale ? scale[it.expert] : 1.0f;
-  bf16x8 hi[RS], lo[RS];
+// Up product: out[t] = base[t] + w[e] (s v[t]) of up to 16 STEPS rows over a
+// block of columns.  The 32-wide K of a matrix-core step holds 16 ranks' high parts,
+// then their low parts, against the same w twice (RS steps).  A wave takes
+// 16 NT columns in NT tiles, lane c the columns NT c + o of tile o, so that
+// base and out move as runs of 16 lanes; it holds their w in registers and
+// walks the rows 16 at a time, the base of all of them loaded beforehand.  The
+// first `rest` workgroups copy the rows of the tokens without an adapter, a
+// token a wave.
+template <int NT>
+struct Run;
+template <>
+struct Run<4> { typedef u32x2 type; };
+template <>
+struct Run<8> { typedef u32x4 type; };
+
+// What the up product reads of the down product: its operand, or where the
+// reduction axis was split over workgroups the shares' sums, which it adds
+// up and cuts itself (the first column block leaves the sum for the caller).
+struct Down {
+  const uint16_t *operand;
+  const float *part;
+  int splits, scaled;
+  int64_t max_rows;
+  const float *scale;
+  float *sum;
+};
+
+template <int RS, int NT, int STEPS, bool PART>
+__device__ __forceinline__ void up_rows(int src, const Item &it, int from_row, int n, const Down &down, int R, bool leave,
+                                        const bf16x8 (&wv16)[NT][RS], const uint16_t *base, uint16_t *out, int C, int col,
+                                        bool on) {
+  typedef typename Run<NT>::type Cols;
+  const int lane = threadIdx.x & (kWave - 1), c = lane & 15, g = lane >> 4;
+  int tok[STEPS][4];
+  Cols bv[STEPS][4];
+  bf16x8 v[STEPS][RS];
+  // unconditional loads (rows and columns out of range: ones in range, never
+  // used), so that they stay in flight together
 #pragma unroll
-  for (int k = 0; k < RS; ++k) {
-    const int r = k * 16 + g * 8;
-    float v[8] = {};
-    if (own >= 0 && r < R) {
-      for (int q = 0; q < splits; ++q) {
-        const f32x4 *from = (const f32x4 *)(part + ((size_t)q * T + own) * R + r);
-        const f32x4 p0 = from[0], p1 = from[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { v[i] += p0[i]; v[4 + i] += p1[i]; }
-      }
-      if (blk == 0 && wv == 0) {
-        const float by = scaled ? sc : 1.0f;
-        f32x4 *to = (f32x4 *)(sum + (size_t)own * R + r);
-        to[0] = f32x4{v[0] * by, v[1] * by, v[2] * by, v[3] * by};
-        to[1] = f32x4{v[4] * by, v[5] * by, v[6] * by, v[7] * by};
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= sc;
-    split2(v, hi[k], lo[k]);
-  }
-  // a tile's A row m = 8 b + 4 g' + i is column 16 g' + 4 b + i, so that a
-  // lane's 16 sums are 16 consecutive columns of its token
-  const int col_of = 16 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
-  for (int c0 = blk * kUpCols + wv * 32; c0 < min(C, (blk + 1) * kUpCols); c0 += kWaves * 32) {
-    v16f acc = {};
-    const uint16_t *row = w + ((size_t)it.expert * C + c0 + col_of) * R;
-#pragma unroll
-    for (int k = 0; k < RS; ++k) {
-      const int r = min(k * 16 + g * 8, R - 8);   // ranks past R meet zeros in hi and lo
-      const bf16x8 a = *(const bf16x8 *)(row + r);
-      acc = mfma(a, lo[k], acc);
-      acc = mfma(a, hi[k], acc);
-    }
-    if (own < 0) continue;
-    const size_t at = (size_t)own * C + c0 + 16 * g;
-    u32x4 b0 = {}, b1 = {};
-    if (base) {
-      b0 = *(const u32x4 *)(base + at);
-      b1 = *(const u32x4 *)(base + at + 8);
-    }
-    u32x4 o0, o1;
+  for (int s = 0; s < STEPS; ++s)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o0[i] = pack_bf16x2(bf16_lo(b0[i]) + acc[2 * i], bf16_hi(b0[i]) + acc[2 * i + 1]);
-      o1[i] = pack_bf16x2(bf16_lo(b1[i]) + acc[8 + 2 * i], bf16_hi(b1[i]) + acc[8 + 2 * i + 1]);
+      tok[s][i] = __shfl(src, from_row + 16 * s + 4 * g + i);
+      bv[s][i] = Cols{};
     }
-    *(u32x4 *)(out + at) = o0;
-    *(u32x4 *)(out + at + 8) = o1;
+  if (base) {                                     // uniform
+    const uint16_t *from = base + min(col, C - NT);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bv[s][i] = *(const Cols *)(from + (size_t)max(tok[s][i], 0) * C);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+    for (int k = 0; k < RS; ++k) {
+      const int row = from_row + 16 * s + c;
+      const size_t at = it.row0 + min(row, n - 1);
+      if constexpr (!PART) {
+        v[s][k] = *(const bf16x8 *)(down.operand + at * 2 * operand_ranks(R) + k * 32 + g * 8);
+      } else {
+        // lanes g and g + 2 hold the high and the low parts of the same ranks
+        const int r = k * 16 + (g & 1) * 8, t = __shfl(src, row);
+        const float sc = down.scale ? down.scale[it.expert] : 1.0f;
+        const float *from = down.part + at * R + min(r, R - 8);
+        f32x4 p0 = {}, p1 = {};
+        for (int q = 0; q < down.splits; ++q) {
+          p0 += *(const f32x4 *)(from + (size_t)q * down.max_rows * R);
+          p1 += *(const f32x4 *)(from + (size_t)q * down.max_rows * R + 4);
+        }
+        if (leave && g < 2 && t >= 0 && r < R) {
+          const float by = down.scaled ? sc : 1.0f;
+          *(f32x4 *)(down.sum + (size_t)t * R + r) = p0 * by;
+          *(f32x4 *)(down.sum + (size_t)t * R + r + 4) = p1 * by;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = r < R ? (i < 4 ? p0[i & 3] : p1[i & 3]) * sc : 0.0f;
+          const __bf16 hi = (__bf16)x;
+          v[s][k][i] = g < 2 ? hi : (__bf16)(x - (float)hi);
+        }
+      }
+    }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    f32x4 acc[NT];
+#pragma unroll
+    for (int o = 0; o < NT; ++o) {
+      acc[o] = f32x4{};
+#pragma unroll
+      for (int k = 0; k < RS; ++k) acc[o] = mfma(v[s][k], wv16[o][k], acc[o]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      Cols o;
+#pragma unroll
+      for (int q = 0; q < NT / 2; ++q)
+        o[q] = pack_bf16x2(bf16_lo(bv[s][i][q]) + acc[2 * q][i], bf16_hi(bv[s][i][q]) + acc[2 * q + 1][i]);
+      if (on && tok[s][i] >= 0) *(Cols *)(out + (size_t)tok[s][i] * C + col) = o;
+    }
   }
 }
 
-// out[t] = base[t] (or zeros) for the tokens without an adapter
-__global__ __launch_bounds__(256) void rest_kernel(const int *__restrict__ slot, int64_t T, const u32x4 *base,
-                                                   u32x4 *out, int vecs) {
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    if (slot[t] >= 0) continue;                   // uniform
-    for (int i = threadIdx.x; i < vecs; i += blockDim.x) out[t * vecs + i] = base ? base[t * vecs + i] : u32x4{};
+template <int RS, int NT, int STEPS, bool PART>
+__global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ offsets, const int *__restrict__ row_src,
+                                                      const int *__restrict__ slot, int N,
+                                                      Down down, int64_t T, const uint16_t *__restrict__ w, int R,
+                                                      const uint16_t *base, uint16_t *out, int C, int blocks,
+                                                      int rest) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane & 15, g = lane >> 4;
+  if ((int)blockIdx.x < rest) {                   // uniform
+    const int vecs = C / 8;
+    for (int64_t t = (int64_t)blockIdx.x * kWaves + wv; t < T; t += (int64_t)rest * kWaves) {
+      if (slot[t] >= 0) continue;                 // uniform
+      const u32x4 *from = (const u32x4 *)base + t * vecs;
+      u32x4 *to = (u32x4 *)out + t * vecs;
+#pragma unroll 4
+      for (int i = lane; i < vecs; i += kWave) to[i] = base ? from[i] : u32x4{};
+    }
+    return;
+  }
+  const int unit = blockIdx.x - rest;
+  const int first = (unit % blocks * kWaves + wv) * 16 * NT;
+  const Item it = find_item(offsets, N, 16 * STEPS, false, unit / blocks);
+  if (it.expert < 0 || first >= C) return;        // uniform
+  const int src = lane < it.n ? row_src[it.row0 + lane] : -1;
+  const int col = first + NT * c;
+  bf16x8 wv16[NT][RS];
+#pragma unroll
+  for (int o = 0; o < NT; ++o) {
+    const uint16_t *wr = w + ((size_t)it.expert * C + min(col + o, C - 1)) * R;
+#pragma unroll
+    for (int k = 0; k < RS; ++k)                  // ranks past R meet zeros in the operand
+      wv16[o][k] = *(const bf16x8 *)(wr + min(k * 16 + (g & 1) * 8, R - 8));
+  }
+  // rows of padding come last in a block: none from the first on
+  const int n = __popcll(__ballot(src >= 0));
+  if (n == 0) return;                             // uniform
+  if (PART || n <= 16) {
+    for (int r = 0; r < n; r += 16)
+      up_rows<RS, NT, 1, PART>(src, it, r, n, down, R, first == 0, wv16, base, out, C, col, col < C);
+  } else {
+    up_rows<RS, NT, STEPS, PART>(src, it, 0, n, down, R, first == 0, wv16, base, out, C, col, col < C);
   }
 }
 
-// dst[n][j][i] = src[n][i][j], in 32 x 32 tiles
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t *__restrict__ src, int rows, int cols,
-                                                        uint16_t *__restrict__ dst) {
+// dst[n][j][i] = src[n][i][j] of two stacks of matrices, in 32 x 32 tiles
+struct Transpose {
+  const uint16_t *src;
+  int rows, cols;
+  uint16_t *dst;
+};
+__global__ __launch_bounds__(256) void transpose_kernel(Transpose a, Transpose b, int tiles_a) {
   __shared__ uint16_t tile[32][33];
+  const Transpose &m = (int)blockIdx.x < tiles_a ? a : b;
+  const int at = (int)blockIdx.x < tiles_a ? blockIdx.x : blockIdx.x - tiles_a;
+  const int rows = m.rows, cols = m.cols;
   const int tr = (rows + 31) / 32, tc = (cols + 31) / 32;
-  const int n = blockIdx.x / (tr * tc), in = blockIdx.x % (tr * tc);
+  const int n = at / (tr * tc), in = at % (tr * tc);
   const int i0 = in / tc * 32, j0 = in % tc * 32;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const uint16_t *s = src + (size_t)n * rows * cols;
-  uint16_t *d = dst + (size_t)n * rows * cols;
+  const uint16_t *s = m.src + (size_t)n * rows * cols;
+  uint16_t *d = m.dst + (size_t)n * rows * cols;
   for (int i = y; i < 32; i += 8)
     if (i0 + i < rows && j0 + x < cols) tile[i][x] = s[(size_t)(i0 + i) * cols + j0 + x];
   __syncthreads();
@@ -251,152 +427,241 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t *__restri
 }
 
 // Outer products: grad[e][r][c] (or [c][r] if T_OUT) = by * sum over the
-// adapter's tokens of p[t][r] q[t][c], for a block of 64 columns.  The
-// columns are taken in pairs: lane c of the even tile holds column 2 c, of
-// the odd one 2 c + 1, so that a lane's four bytes of a row feed both.
-template <int MF, bool T_OUT>
+// adapter's tokens of p[t][r] q[t][c], for a piece of `chunk` tokens and 32 NT
+// columns.  A lane takes NT consecutive columns of 8 tokens' rows at a time
+// (column NT c + o of tile o), so a wave reads whole lines and turns them to
+// the matrix cores' token-major operands in registers.  An adapter of one
+// piece is done; the pieces of the others go to `part` (a slot of R x C
+// each), which outer_sum_kernel adds up.
+template <int NT>
+struct Cols;
+template <>
+struct Cols<2> { typedef uint32_t type __attribute__((ext_vector_type(1))); };
+template <>
+struct Cols<4> { typedef u32x2 type; };
+
+template <int MF, int NT, bool T_OUT>
 __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__ offsets,
-                                                         const int *__restrict__ row_src,
+                                                         const int *__restrict__ row_src, int N, int chunk,
                                                          const float *__restrict__ p, int R,
                                                          const uint16_t *__restrict__ q, int C,
                                                          const float *__restrict__ scale, float *__restrict__ grad,
-                                                         int blocks) {
-  __shared__ __attribute__((aligned(16))) float s_tile[kWaves * 2 * 16 * kWave];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave, c = lane & 31, g = lane >> 5;
-  const int e = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * 64;
-  const int lo = offsets[e], hi = offsets[e + 1];
-  const int col = min(c0 + 2 * c, C - 2);
-  v16f acc[MF][2];
+                                                         float *__restrict__ part, int blocks) {
+  typedef typename Cols<NT>::type Row;
+  constexpr int kRing = 2;                        // steps of 16 tokens in flight
+  __shared__ __attribute__((aligned(16))) float s_tile[kWaves * 2 * 16 * kWave];   // [wave][tile][quad][lane][4]
+  extern __shared__ __attribute__((aligned(16))) int s_src[];   // the piece's tokens, padded with -1
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane & 31, g = lane >> 5;
+  const int c0 = (blockIdx.x % blocks) * 32 * NT;
+  const Item it = find_item(offsets, N, chunk, true, blockIdx.x / blocks);
+  if (it.expert < 0) return;                      // uniform
+  const int padded = (it.n + 15) / 16 * 16;
+  for (int i = tid; i < padded; i += kThreads) s_src[i] = i < it.n ? row_src[it.row0 + i] : -1;
+  __syncthreads();
+  const int col = min(c0 + NT * c, C - NT);
+  v16f acc[MF][NT];
 #pragma unroll
   for (int f = 0; f < MF; ++f)
 #pragma unroll
-    for (int o = 0; o < 2; ++o) acc[f][o] = v16f{};
-  for (int row = lo + wv * 16; row < hi; row += kWaves * 16) {
-    bf16x8 even, odd;
-    int own[8];
+    for (int o = 0; o < NT; ++o) acc[f][o] = v16f{};
+  Row qv[kRing][8];
+  float pv[kRing][MF][8];
+  auto load = [&](int k, int t0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = row + g * 8 + i;
-      own[i] = at < hi ? row_src[at] : -1;
-      const uint32_t v = own[i] >= 0 ? *(const uint32_t *)(q + (size_t)own[i] * C + col) : 0u;
-      even[i] = __builtin_bit_cast(__bf16, (uint16_t)(v & 0xffffu));
-      odd[i] = __builtin_bit_cast(__bf16, (uint16_t)(v >> 16));
+      // rows of padding: token 0's, taken out below (the loads stay
+      // unconditional, so that they are in flight together)
+      const size_t t = (size_t)max(s_src[t0 + g * 8 + i], 0);
+      qv[k][i] = *(const Row *)(q + t * C + col);
+#pragma unroll
+      for (int f = 0; f < MF; ++f) pv[k][f][i] = p[t * R + min(f * 32 + c, R - 1)];
+    }
+    keep_loads();
+  };
+  constexpr int kStep = kWaves * 16;
+  if (wv * 16 < padded) {                         // uniform
+    const int last = padded - 16;
+#pragma unroll
+    for (int k = 0; k < kRing; ++k) load(k, min(wv * 16 + k * kStep, last));
+    auto multiply = [&](int k, int t0) {
+      bf16x8 b[NT];
+      const int *src = s_src + t0 + g * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool on = src[i] >= 0;
+#pragma unroll
+        for (int o = 0; o < NT; ++o)
+          b[o][i] = __builtin_bit_cast(__bf16, (uint16_t)(on ? qv[k][i][o >> 1] >> (16 * (o & 1)) : 0u));
+#pragma unroll
+        for (int f = 0; f < MF; ++f) pv[k][f][i] = on ? pv[k][f][i] : 0.0f;
+      }
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        bf16x8 a0, a1, a2;
+        split3(pv[k][f], a0, a1, a2);
+#pragma unroll
+        for (int o = 0; o < NT; ++o) acc[f][o] = mfma(a0, b[o], mfma(a1, b[o], mfma(a2, b[o], acc[f][o])));
+      }
+    };
+    int t0 = wv * 16;
+    for (; t0 + (kRing - 1) * kStep < padded; t0 += kRing * kStep) {
+#pragma unroll
+      for (int k = 0; k < kRing; ++k) {
+        multiply(k, t0 + k * kStep);
+        load(k, min(t0 + (k + kRing) * kStep, last));   // past the end: never used
+      }
     }
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-      const int r = min(f * 32 + c, R - 1);
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = own[i] >= 0 ? p[(size_t)own[i] * R + r] : 0.0f;
-      bf16x8 a0, a1, a2;
-      split3(v, a0, a1, a2);
-      acc[f][0] = mfma(a0, even, mfma(a1, even, mfma(a2, even, acc[f][0])));
-      acc[f][1] = mfma(a0, odd, mfma(a1, odd, mfma(a2, odd, acc[f][1])));
-    }
+    for (int k = 0; k < kRing - 1; ++k)
+      if (t0 + k * kStep < padded) multiply(k, t0 + k * kStep);   // uniform
   }
-  const float by = scale ? scale[e] : 1.0f;
+  const float by = scale ? scale[it.expert] : 1.0f;
+  float *to = it.pieces > 1 ? part + (size_t)it.slot * R * C : grad + (size_t)it.expert * R * C;
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
-    if (f > 0) __syncthreads();
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
+    for (int o = 0; o < NT; o += 2) {             // two tiles at a time
+      if (f + o > 0) __syncthreads();
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *(f32x4 *)(s_tile + (((wv * 2 + o) * 4 + b) * kWave + lane) * 4) =
-            f32x4{acc[f][o][4 * b], acc[f][o][4 * b + 1], acc[f][o][4 * b + 2], acc[f][o][4 * b + 3]};
-    __syncthreads();
-    // thread: quad (o, b) of a lane; ranks f * 32 + 8 b + 4 g + 0..3 of column c0 + 2 c + o
-    const int o = tid / (4 * kWave), b = tid / kWave % 4;
-    f32x4 v = *(const f32x4 *)(s_tile + ((o * 4 + b) * kWave + lane) * 4);
+      for (int d = 0; d < 2; ++d)
 #pragma unroll
-    for (int k = 1; k < kWaves; ++k) v += *(const f32x4 *)(s_tile + (((k * 2 + o) * 4 + b) * kWave + lane) * 4);
-    v *= by;
-    const int r = f * 32 + 8 * b + 4 * g, cc = c0 + 2 * c + o;
-    if (r < R && cc < C) {
-      if constexpr (T_OUT) {
-        *(f32x4 *)(grad + ((size_t)e * C + cc) * R + r) = v;
-      } else {
+        for (int b = 0; b < 4; ++b) {
+          const v16f &x = acc[f][o + d];
+          *(f32x4 *)(s_tile + (((wv * 2 + d) * 4 + b) * kWave + lane) * 4) =
+              f32x4{x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]};
+        }
+      __syncthreads();
+      // wave b adds up quad b of the lanes: ranks f * 32 + 8 b + 4 g + 0..3 of
+      // columns c0 + NT c + o, + 1
+      const int r = f * 32 + 8 * wv + 4 * g, cc = c0 + NT * c + o;
+      f32x4 v[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) grad[((size_t)e * R + r + i) * C + cc] = v[i];
+      for (int d = 0; d < 2; ++d) {
+        v[d] = *(const f32x4 *)(s_tile + ((d * 4 + wv) * kWave + lane) * 4);
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) v[d] += *(const f32x4 *)(s_tile + (((k * 2 + d) * 4 + wv) * kWave + lane) * 4);
+        v[d] *= by;
+      }
+      if (r < R && cc < C) {
+        if constexpr (T_OUT) {
+          *(f32x4 *)(to + (size_t)cc * R + r) = v[0];
+          *(f32x4 *)(to + (size_t)(cc + 1) * R + r) = v[1];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *(f32x2 *)(to + (size_t)(r + i) * C + cc) = f32x2{v[0][i], v[1][i]};
+        }
       }
     }
   }
 }
-static_assert(kThreads == 2 * 4 * kWave, "one quad per thread");
+
+// grad[e] = the sum of the adapter's pieces in order, where it has several.
+__global__ __launch_bounds__(256) void outer_sum_kernel(const int *__restrict__ offsets, int N, int chunk, int64_t quads,
+                                                        const f32x4 *__restrict__ part, f32x4 *__restrict__ grad,
+                                                        int blocks) {
+  const int e = blockIdx.x / blocks;
+  const int pieces = (offsets[e + 1] - offsets[e] + chunk - 1) / chunk;
+  if (pieces <= 1) return;                        // uniform
+  int slot = 0;
+  for (int i = 0; i < e; ++i) {
+    const int other = (offsets[i + 1] - offsets[i] + chunk - 1) / chunk;
+    slot += other > 1 ? other : 0;
+  }
+  for (int64_t i = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x; i < quads; i += (int64_t)blocks * 256) {
+    f32x4 v = part[slot * quads + i];
+    for (int k = 1; k < pieces; ++k) v += part[(slot + k) * quads + i];
+    grad[e * quads + i] = v;
+  }
+}
 
 // Work items of a layout, at most: its rows in whole tiles and one partial
 // tile per adapter (and no more than one per row).
-int64_t items_upper(const ep_handle_t &h) {
-  const int64_t rows = h.max_rows, whole = rows / kTile + h.num_experts;
+int64_t items_upper(const ep_handle_t &h, int tile) {
+  const int64_t rows = h.max_rows, whole = rows / tile + h.num_experts;
   return rows < whole ? rows : whole;
 }
 
-// Shares of a down product's axis: enough workgroups for two per CU, each
-// wave with at least four 32-wide steps.
-int down_splits(int64_t items, int K) {
+// Shares of a down product's axis.  Split where the tiles leave CUs idle, to
+// about two workgroups a CU with eight steps each; the up product then adds up
+// the shares in every column block, which costs more than it gains from about
+// half a tile a CU on.  Measured (us, down + up; in 7168): 128 tokens of 64
+// adapters of rank 16 (68 tiles) 10.8 + 7.2 whole, 7.3 + 9.0 in two shares,
+// 5.9 + 9.6 in four; 4099 tokens at rank 64 (136 tiles) 24 + 19 whole, 19 + 38
+// in two.
+int down_splits(const ep_handle_t &h, int K) {
+  const int64_t items = items_upper(h, kTile);
   int s = 1;
-  while (s < kLoraSplits && items * s < 512 && K / 32 >= 2 * s * kWaves * 4) s *= 2;
+  if (lora_rows(h) > kLoraSplitRows || items > 128) return s;
+  while (s < kLoraSplits && items * s * 2 <= 512 && K / 64 >= 2 * s * 8) s *= 2;
   return s;
 }
 
-hipError_t run_down(const ep_handle_t &h, const void *rows, int K, const void *w, int R, int splits, float *part,
-                    hipStream_t s) {
-  const dim3 grid((unsigned)(items_upper(h) * splits)), block(kThreads);
-  const int mf = (R + 31) / 32;
-#define EP_DOWN(MF)                                                                                            \
-  hipLaunchKernelGGL(down_kernel<MF>, grid, block, 0, s, h.offsets, h.row_src, h.num_experts,                  \
-                     (const uint16_t *)rows, K, (const uint16_t *)w, R, splits, h.num_tokens, part)
-  if (mf == 1) EP_DOWN(1);
-  else if (mf == 2) EP_DOWN(2);
-  else if (mf == 3) EP_DOWN(3);
-  else EP_DOWN(4);
+hipError_t run_down(const ep_handle_t &h, const void *rows, int K, const void *w, int R, const Down &down, void *operand,
+                    void *part, hipStream_t s) {
+  const dim3 grid((unsigned)(items_upper(h, kTile) * down.splits));
+  const int mf = (R + 15) / 16;
+#define EP_DOWN(MF, W)                                                                                         \
+  hipLaunchKernelGGL((down_kernel<MF, W>), grid, dim3(W * kWave), 0, s, h.offsets, h.row_src, h.num_experts,   \
+                     (const uint16_t *)rows, K, (const uint16_t *)w, R, down.scale, down.scaled, down.sum,     \
+                     (uint16_t *)operand, down.splits, h.max_rows, (float *)part)
+  if (mf == 1) EP_DOWN(1, 8);
+  else if (mf == 2) EP_DOWN(2, 8);
+  else if (mf <= 4) EP_DOWN(4, 8);
+  else EP_DOWN(8, 4);                             // 16 lines of LDS a wave and block
 #undef EP_DOWN
   return hipGetLastError();
 }
 
-hipError_t run_up(const ep_handle_t &h, const float *part, int splits, const void *w, int R, const float *scale,
-                  const void *base, void *out, int C, float *sum, int scaled, hipStream_t s) {
-  const int blocks = (C + kUpCols - 1) / kUpCols;
-  const dim3 grid((unsigned)(items_upper(h) * blocks)), block(kThreads);
-  const int rs = (R + 15) / 16;
-#define EP_UP(RS)                                                                                              \
-  hipLaunchKernelGGL(up_kernel<RS>, grid, block, 0, s, h.offsets, h.row_src, h.num_experts, part, splits,      \
-                     h.num_tokens, (const uint16_t *)w, R, scale, (const uint16_t *)base, (uint16_t *)out, C, sum, \
-                     scaled, blocks)
-  if (rs == 1) EP_UP(1);
-  else if (rs == 2) EP_UP(2);
-  else if (rs <= 4) EP_UP(4);
-  else EP_UP(8);
+hipError_t run_up(const ep_handle_t &h, const Down &down, const void *w, int R, const void *base, void *out, int C,
+                  hipStream_t s) {
+  const int rs = operand_ranks(R) / 16, nt = rs <= 2 ? 8 : 4;
+  const int blocks = (C + kWaves * 16 * nt - 1) / (kWaves * 16 * nt);
+  const int64_t waves = (h.num_tokens + kWaves - 1) / kWaves, rest = out == base ? 0 : waves < 256 ? waves : 256;
+  const int64_t items = items_upper(h, rs <= 2 ? 64 : 32);
+  const dim3 grid((unsigned)(items * blocks + rest)), block(kThreads);
+#define EP_UP_PART(RS, NT, STEPS, PART)                                                                        \
+  hipLaunchKernelGGL((up_kernel<RS, NT, STEPS, PART>), grid, block, 0, s, h.offsets, h.row_src, h.slot,        \
+                     h.num_experts, down, h.num_tokens, (const uint16_t *)w, R, (const uint16_t *)base,        \
+                     (uint16_t *)out, C, blocks, (int)rest)
+#define EP_UP(RS, NT, STEPS)                     \
+  if (down.splits > 1) EP_UP_PART(RS, NT, STEPS, true); \
+  else EP_UP_PART(RS, NT, STEPS, false)
+  switch (rs) {
+    case 1: EP_UP(1, 8, 4); break;
+    case 2: EP_UP(2, 8, 4); break;
+    case 3: EP_UP(3, 4, 2); break;
+    case 4: EP_UP(4, 4, 2); break;
+    case 6: EP_UP(6, 4, 2); break;
+    default: EP_UP(8, 4, 2); break;
+  }
 #undef EP_UP
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || out == base) return e;
-  const int64_t b = h.num_tokens < 1024 ? h.num_tokens : 1024;
-  hipLaunchKernelGGL(rest_kernel, dim3((unsigned)b), dim3(256), 0, s, h.slot, h.num_tokens, (const u32x4 *)base,
-                     (u32x4 *)out, C / 8);
+#undef EP_UP_PART
   return hipGetLastError();
 }
 
 template <bool T_OUT>
 hipError_t run_outer(const ep_handle_t &h, const float *p, int R, const void *q, int C, const float *scale, float *grad,
-                     hipStream_t s) {
-  const int blocks = (C + 63) / 64;
-  const dim3 grid((unsigned)((int64_t)h.num_experts * blocks)), block(kThreads);
-  const int mf = (R + 31) / 32;
-#define EP_OUTER(MF)                                                                                          \
-  hipLaunchKernelGGL((outer_kernel<MF, T_OUT>), grid, block, 0, s, h.offsets, h.row_src, p, R,                \
-                     (const uint16_t *)q, C, scale, grad, blocks)
-  if (mf == 1) EP_OUTER(1);
-  else if (mf == 2) EP_OUTER(2);
-  else if (mf == 3) EP_OUTER(3);
-  else EP_OUTER(4);
+                     float *part, hipStream_t s) {
+  const int chunk = outer_chunk(R), mf = (R + 31) / 32, nt = mf <= 2 ? 4 : 2;
+  const int blocks = (C + 32 * nt - 1) / (32 * nt);
+  const int64_t items = h.max_rows / chunk + h.num_experts;
+  const dim3 grid((unsigned)(items * blocks)), block(kThreads);
+  const size_t lds = (size_t)chunk * 4;
+#define EP_OUTER(MF, NT)                                                                                      \
+  hipLaunchKernelGGL((outer_kernel<MF, NT, T_OUT>), grid, block, lds, s, h.offsets, h.row_src, h.num_experts, chunk, p, \
+                     R, (const uint16_t *)q, C, scale, grad, part, blocks)
+  if (mf == 1) EP_OUTER(1, 4);
+  else if (mf == 2) EP_OUTER(2, 4);
+  else if (mf == 3) EP_OUTER(3, 2);
+  else EP_OUTER(4, 2);
 #undef EP_OUTER
-  return hipGetLastError();
-}
-
-hipError_t run_transpose(const void *src, int N, int rows, int cols, void *dst, hipStream_t s) {
-  const int64_t tiles = (int64_t)N * ((rows + 31) / 32) * ((cols + 31) / 32);
-  hipLaunchKernelGGL(transpose_kernel, dim3((unsigned)tiles), dim3(256), 0, s, (const uint16_t *)src, rows, cols,
-                     (uint16_t *)dst);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || h.max_rows <= chunk) return e;
+  const int64_t quads = (int64_t)R * C / 4;
+  const int sum_blocks = (int)((quads + 255) / 256);
+  hipLaunchKernelGGL(outer_sum_kernel, dim3((unsigned)((int64_t)h.num_experts * sum_blocks)), dim3(256), 0, s, h.offsets,
+                     h.num_experts, chunk, quads, (const f32x4 *)part, (f32x4 *)grad, sum_blocks);
   return hipGetLastError();
 }
 
@@ -404,29 +669,37 @@ hipError_t run_transpose(const void *src, int N, int rows, int cols, void *dst, 
 
 hipError_t launch_lora(const LoraArgs &p, hipStream_t s) {
   if (p.h.num_tokens == 0) return hipSuccess;
-  const LoraWs ws = lora_ws(p.h.num_tokens, p.in, p.out_features, p.rank, p.h.num_experts, 0);
-  float *part = (float *)(p.ws + ws.part);
-  const int splits = down_splits(items_upper(p.h), p.in);
-  hipError_t e = run_down(p.h, p.x, p.in, p.a, p.rank, splits, part, s);
-  if (e == hipSuccess)
-    e = run_up(p.h, part, splits, p.b, p.rank, p.scale, p.base, p.out, p.out_features, p.down, 0, s);
+  const LoraWs ws = lora_ws(lora_rows(p.h), p.in, p.out_features, p.rank, p.h.num_experts, 0);
+  char *operand = p.ws + ws.operand, *part = p.ws + ws.part;
+  const Down down{(const uint16_t *)operand, (const float *)part, down_splits(p.h, p.in), 0, p.h.max_rows, p.scale, p.down};
+  hipError_t e = run_down(p.h, p.x, p.in, p.a, p.rank, down, operand, part, s);
+  if (e == hipSuccess) e = run_up(p.h, down, p.b, p.rank, p.base, p.out, p.out_features, s);
   return e;
 }
 
 hipError_t launch_lora_backward(const LoraGradArgs &p, hipStream_t s) {
-  const LoraWs ws = lora_ws(p.h.num_tokens, p.in, p.out_features, p.rank, p.h.num_experts, 1);
-  float *part = (float *)(p.ws + ws.part), *u = (float *)(p.ws + ws.u);
-  char *bt = p.ws + ws.bt, *at = p.ws + ws.at;
+  const int N = p.h.num_experts, R = p.rank;
+  const LoraWs ws = lora_ws(lora_rows(p.h), p.in, p.out_features, R, N, 1);
+  char *operand = p.ws + ws.operand, *part = p.ws + ws.part;
+  float *u = (float *)(p.ws + ws.u), *outer = (float *)(p.ws + ws.outer);
+  uint16_t *bt = (uint16_t *)(p.ws + ws.bt), *at = (uint16_t *)(p.ws + ws.at);
   hipError_t e = hipSuccess;
-  if (p.h.num_tokens > 0) {
-    const int splits = down_splits(items_upper(p.h), p.out_features);
-    e = run_transpose(p.b, p.h.num_experts, p.out_features, p.rank, bt, s);
-    if (e == hipSuccess) e = run_transpose(p.a, p.h.num_experts, p.rank, p.in, at, s);
-    if (e == hipSuccess) e = run_down(p.h, p.grad_out, p.out_features, bt, p.rank, splits, part, s);
-    if (e == hipSuccess) e = run_up(p.h, part, splits, at, p.rank, p.scale, p.grad_base, p.grad_x, p.in, u, 1, s);
+  if (p.h.num_tokens == 0) {                      // no row is read: the gradients are zeros
+    e = run_outer<false>(p.h, u, R, p.x, p.in, nullptr, p.grad_a, outer, s);
+    if (e == hipSuccess) e = run_outer<true>(p.h, p.down, R, p.grad_out, p.out_features, p.scale, p.grad_b, outer, s);
+    return e;
   }
-  if (e == hipSuccess) e = run_outer<false>(p.h, u, p.rank, p.x, p.in, nullptr, p.grad_a, s);
-  if (e == hipSuccess) e = run_outer<true>(p.h, p.down, p.rank, p.grad_out, p.out_features, p.scale, p.grad_b, s);
+  const Transpose tb{(const uint16_t *)p.b, p.out_features, R, bt}, ta{(const uint16_t *)p.a, R, p.in, at};
+  const int64_t rt = (R + 31) / 32, tiles_b = N * rt * ((p.out_features + 31) / 32), tiles_a = N * rt * ((p.in + 31) / 32);
+  hipLaunchKernelGGL(transpose_kernel, dim3((unsigned)(tiles_a + tiles_b)), dim3(256), 0, s, tb, ta, (int)tiles_b);
+  e = hipGetLastError();
+  const Down down{(const uint16_t *)operand, (const float *)part, down_splits(p.h, p.out_features), 1, p.h.max_rows, p.scale,
+                  u};
+  if (e == hipSuccess) e = run_down(p.h, p.grad_out, p.out_features, bt, R, down, operand, part, s);
+  // grad_out once more while the last-level cache may still hold it
+  if (e == hipSuccess) e = run_outer<true>(p.h, p.down, R, p.grad_out, p.out_features, p.scale, p.grad_b, outer, s);
+  if (e == hipSuccess) e = run_up(p.h, down, at, R, p.grad_base, p.grad_x, p.in, s);
+  if (e == hipSuccess) e = run_outer<false>(p.h, u, R, p.x, p.in, nullptr, p.grad_a, outer, s);
   return e;
 }
 

@@ -7,19 +7,44 @@ namespace ep {
 
 constexpr int32_t kMaxRank = 128;
 constexpr int kLoraSplits = 8;                    // most shares of a down product's reduction axis
+constexpr int64_t kLoraSplitRows = 16384;         // and the most rows it is split for
+
+// Tokens of a piece of an adapter's gradient: its R x C partial sums then
+// have at most a sixteenth of the bytes of the token rows read for them.
+constexpr int outer_chunk(int R) { return R <= 8 ? 256 : 32 * R; }
+
+// The rows a workspace is sized for: the layout's, or its tokens if they are
+// more (blocks with a small capacity).
+__host__ inline int64_t lora_rows(const ep_handle_t &h) {
+  return h.max_rows > h.num_tokens ? h.max_rows : h.num_tokens;
+}
+
+// The up product's operand holds, for each row and step of 16 ranks, 16 high
+// then 16 low bf16 parts; ranks are filled up with zeros to the steps its
+// kernel is built for (1, 2, 3, 4, 6 or 8).
+__host__ __device__ constexpr int operand_ranks(int R) {
+  const int steps = (R + 15) / 16;
+  return 16 * (steps <= 4 ? steps : steps <= 6 ? 6 : 8);
+}
 
 struct LoraWs {                                   // byte offsets of the workspace sub-arrays
-  size_t part, u, bt, at, total;
+  size_t operand, part, u, bt, at, outer, total;
 };
-// part: partial down products [splits][T][R]; backward also keeps u [T][R]
-// and the transposes of B ([N][R][out]) and A ([N][in][R]).
-__host__ inline LoraWs lora_ws(int64_t T, int64_t in, int64_t out, int64_t R, int64_t N, int backward) {
+// For `rows` rows (lora_rows): the up product's operand, 4 bytes a rank and
+// row, and the down product's partial sums; backward also keeps u [T][R],
+// the transposes of B ([N][R][out]) and A ([N][in][R]), and the partial
+// gradients of the adapters with several pieces (an adapter of n rows has at
+// most 2 n / chunk of them).
+__host__ inline LoraWs lora_ws(int64_t rows, int64_t in, int64_t out, int64_t R, int64_t N, int backward) {
   LoraWs w;
-  w.part = 0;
-  w.u = align_up((size_t)(kLoraSplits * T * R) * 4, kWsAlign);
-  w.bt = w.u + (backward ? align_up((size_t)(T * R) * 4, kWsAlign) : 0);
+  const int64_t chunk = outer_chunk((int)R), slots = rows <= chunk ? 0 : 2 * rows / chunk + 1;
+  w.operand = 0;
+  w.part = align_up((size_t)(rows * operand_ranks((int)R)) * 4, kWsAlign);
+  w.u = w.part + align_up((size_t)(rows <= kLoraSplitRows ? kLoraSplits * rows * R : 0) * 4, kWsAlign);
+  w.bt = w.u + (backward ? align_up((size_t)(rows * R) * 4, kWsAlign) : 0);
   w.at = w.bt + (backward ? align_up((size_t)(N * R * out) * 2, kWsAlign) : 0);
-  w.total = w.at + (backward ? align_up((size_t)(N * R * in) * 2, kWsAlign) : 0);
+  w.outer = w.at + (backward ? align_up((size_t)(N * R * in) * 2, kWsAlign) : 0);
+  w.total = w.outer + (backward ? align_up((size_t)(slots * R * (in > out ? in : out)) * 4, kWsAlign) : 0);
   return w;
 }
 

@@ -35,9 +35,11 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Measured (us, both launches): one token of 256 MXFP8 experts (H 7168, I
-// 2048, top 8) 39 + 30 with 4 waves, 2 groups and 2 steps in flight; 42 + 37
-// with 8 waves, 68 + 53 with 1 group, 40 + 31 with 3 steps; 128 tokens 1180 +
-// 770, against 1220 + 1010, 1900 + 1300 and 1215 + 830.
+// 2048, top 8) 39 + 27 with 4 waves, 2 groups and 2 steps in flight, 39 + 29
+// with 3 steps; 128 tokens 1150 + 750, against 1130 + 720; 33 tokens of MXFP4
+// experts 93 + 69, against 102 + 79; 13 tokens of bf16 experts 52 + 34, against
+// 57 + 42.  With 8 waves launch 2 took a third longer, with 1 group everything
+// at least half as long again.
 constexpr int kWaves = 4;
 constexpr int kGroups = 2;                        // 32-row weight groups of a workgroup
 constexpr int kRing = 2;                          // K steps in flight per wave
@@ -248,6 +250,7 @@ __device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const u
       if constexpr (Q != EP_QUANT_NONE)
         w[slot][q].scale = *(const uint32_t *)(sp + (size_t)(s >> 2) * sspan + q * 256 + lane * 4);
     }
+    keep_loads();
   };
   if (s0 < s1) {                                  // uniform
 #pragma unroll
@@ -258,27 +261,34 @@ __device__ __forceinline__ void product(const uint8_t *wp, size_t wstep, const u
   auto load_b = [&](int slot, int s) {
 #pragma unroll
     for (int m = 0; m < 4; ++m) bv[slot][m] = *(const u32x4 *)(b + s * 64 + (m >> 1) * 32 + (m & 1) * 8);
+    keep_loads();
   };
 #pragma unroll
   for (int r = 0; r < kRing; ++r) load_b(r, min(s0 + r, s1 - 1));
-  for (int s = s0; s < s1; s += kRing) {
+  auto multiply = [&](int r, int s) {
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      bf16x8 a[4];
+      operands<Q>(w[r][q], s & 3, a);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m], __builtin_bit_cast(bf16x8, bv[r][m]), acc[q], 0, 0, 0);
+    }
+  };
+  // whole rings without a condition in them (a load whose value only a branch
+  // uses is moved into that branch), then the rest
+  int s = s0;
+  for (; s + kRing <= s1; s += kRing) {
 #pragma unroll
     for (int r = 0; r < kRing; ++r) {
-      if (s + r < s1) {                           // uniform
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          bf16x8 a[4];
-          operands<Q>(w[r][q], (s + r) & 3, a);
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m], __builtin_bit_cast(bf16x8, bv[r][m]), acc[q], 0, 0,
-                                                             0);
-        }
-      }
+      multiply(r, s + r);
       load_w(r, min(s + r + kRing, s1 - 1));      // past the end: the last step again, never used
       load_b(r, min(s + r + kRing, s1 - 1));
     }
   }
+#pragma unroll
+  for (int r = 0; r < kRing - 1; ++r)
+    if (s + r < s1) multiply(r, s + r);           // uniform
 }
 
 // The waves' partial tiles through LDS: [wave][group][quad of registers][lane][4].

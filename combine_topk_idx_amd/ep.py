@@ -587,9 +587,9 @@ def ep_router_backward(logits, topk_idx, grad_weights, grad_logits, *, score="so
                                    _stream(stream)))
 
 
-def ep_lora_workspace_bytes(num_max_tokens: int, in_features: int, out_features: int, rank: int, num_adapters: int,
+def ep_lora_workspace_bytes(rows: int, in_features: int, out_features: int, rank: int, num_adapters: int,
                             backward: bool = False) -> int:
-    return _lib.ep_lora_workspace_bytes(num_max_tokens, in_features, out_features, rank, num_adapters,
+    return _lib.ep_lora_workspace_bytes(rows, in_features, out_features, rank, num_adapters,
                                         int(bool(backward)))
 
 

@@ -471,10 +471,12 @@ ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num
  *   out          device bf16 [T, out]
  *   down         device float32 [T, rank], written (rows without an adapter
  *                are left as they were): ep_lora_backward takes it
- *   workspace    device, 256-byte aligned, >= ep_lora_workspace_bytes; as for
- *                ep_moe_layer
+ *   workspace    device, 256-byte aligned, >= ep_lora_workspace_bytes(rows,
+ *                ...) with rows the larger of the handle's max_rows and
+ *                num_tokens (a compact layout's num_max_tokens); in use as
+ *                for ep_moe_layer
  * All row buffers are 16-byte aligned. */
-size_t ep_lora_workspace_bytes(int64_t num_max_tokens, int32_t in_features, int32_t out_features, int32_t rank,
+size_t ep_lora_workspace_bytes(int64_t rows, int32_t in_features, int32_t out_features, int32_t rank,
                                int32_t num_adapters, int32_t backward);
 ep_status_t ep_lora(const ep_handle_t *handle, const void *x, int32_t in_features, int32_t out_features,
                     int32_t rank, const void *a, const void *b, const float *scale, const void *base, void *out,

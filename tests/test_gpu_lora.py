@@ -47,11 +47,13 @@ class Lora:
 
     def buffers(self):
         T, fin, fout, r, N = self.shape
+        rows = max(T, self.ep.ep_layout_rows(self.tmax, 1, N, self.layout.get("row_align", 1),
+                                             self.layout.get("expert_capacity", 0)))
         nan = float("nan")
         d = dict(out=torch.full((T, fout), nan, dtype=BF, device=DEV), down=torch.full((T, r), nan, device=DEV),
                  grad_x=torch.full((T, fin), nan, dtype=BF, device=DEV),
                  grad_a=torch.full((N, r, fin), nan, device=DEV), grad_b=torch.full((N, fout, r), nan, device=DEV),
-                 ws=torch.full((self.ep.ep_lora_workspace_bytes(T, fin, fout, r, N, True),), 0xFF, dtype=torch.uint8,
+                 ws=torch.full((self.ep.ep_lora_workspace_bytes(rows, fin, fout, r, N, True),), 0xFF, dtype=torch.uint8,
                                device=DEV))
         d.update({n: to_dev(getattr(self, n)) for n in ("x", "base", "dy", "gb", "a", "b", "scale")})
         return d
@@ -84,6 +86,10 @@ CASES = [
     # T, in, out, rank, N
     (1, 32, 32, 8, 1), (1, 2080, 96, 16, 5), (3, 64, 544, 24, 2), (37, 96, 64, 40, 3), (200, 160, 96, 64, 4),
     (65, 64, 64, 128, 2), (129, 1056, 32, 8, 64), (70, 32, 1056, 104, 512), (500, 64, 96, 32, 3),
+    # every number of 16-rank steps
+    (40, 64, 160, 72, 2), (40, 96, 64, 96, 3), (33, 64, 64, 112, 2), (64, 64, 64, 48, 1),
+    # adapters of several pieces (256 tokens at rank 8), beside some of one and of none
+    (1100, 64, 32, 8, 2), (900, 32, 96, 8, 9), (700, 160, 64, 16, 65), (2300, 32, 32, 40, 3),
 ]
 
 
@@ -102,6 +108,20 @@ def test_lora_padded_layouts(ep, layout):
     d = l.buffers()
     l.run(d, l.handle())
     l.check(d)
+
+
+def test_lora_small_capacity(ep):
+    """Fewer rows than tokens, and blocks of several pieces that are mostly padding."""
+    for seed, T, cap in ((67, 90, 3), (68, 300, 600)):
+        l = Lora(ep, seed, T, 64, 96, 8, 4, none=0.0, expert_capacity=cap)
+        d = l.buffers()
+        l.run(d, l.handle())
+        seen = [0] * 4
+        for t, e in enumerate(l.ids):
+            seen[e] += 1
+            if seen[e] > cap:
+                l.ids[t] = -1
+        l.check(d)
 
 
 def test_lora_capacity_drops(ep):
