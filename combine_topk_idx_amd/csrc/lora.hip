@@ -31,7 +31,6 @@ namespace ep {
 
 namespace {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -106,9 +105,6 @@ __device__ __forceinline__ Item find_item(const int *__restrict__ offsets, int N
 __device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ v16f mfma(const bf16x8 &a, const bf16x8 &b, const v16f &c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
 
 // Down product: v[r] = sum over i of w[e][r][i] rows[t][i], t the token of the
 // layout's row.  MF: 16-row blocks of the rank; W: waves.
@@ -134,8 +130,8 @@ __global__ __launch_bounds__(W *kWave) void down_kernel(const int *__restrict__ 
   __shared__ __attribute__((aligned(16))) u32x4 s_mem[kStage > kSums ? kStage : kSums];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % splits;
-  const Item it = find_item(offsets, N, kTile, false, blockIdx.x / splits);
+  const int unit = blockIdx.x, split = unit % splits;
+  const Item it = find_item(offsets, N, kTile, false, unit / splits);
   if (it.expert < 0) return;                      // uniform
   // token of row `lane` of the tile; rows past the tile and of padding: -1
   const int src = (lane & 31) < it.n ? row_src[it.row0 + (lane & 31)] : -1;
@@ -261,8 +257,8 @@ __device__ __forceinline__ void split3(const float (&v)[8], bf16x8 &hi, bf16x8 &
 // 16 NT columns in NT tiles, lane c the columns NT c + o of tile o, so that
 // base and out move as runs of 16 lanes; it holds their w in registers and
 // walks the rows 16 at a time, the base of all of them loaded beforehand.  The
-// first `rest` workgroups copy the rows of the tokens without an adapter, a
-// token a wave.
+// first `rest` workgroups copy the rows of the tokens without an adapter,
+// each wave those of rest_tokens tokens.
 template <int NT>
 struct Run;
 template <>
@@ -362,14 +358,16 @@ template <int RS, int NT, int STEPS, bool PART>
 __global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ offsets, const int *__restrict__ row_src,
                                                       const int *__restrict__ slot, int N,
                                                       Down down, int64_t T, const uint16_t *__restrict__ w, int R,
-                                                      const uint16_t *base, uint16_t *out, int C, int blocks,
-                                                      int rest) {
+                                                      const uint16_t *base, uint16_t *out, int C, int blocks, int rest,
+                                                      int rest_tokens) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane & 15, g = lane >> 4;
   if ((int)blockIdx.x < rest) {                   // uniform
     const int vecs = C / 8;
-    for (int64_t t = (int64_t)blockIdx.x * kWaves + wv; t < T; t += (int64_t)rest * kWaves) {
-      if (slot[t] >= 0) continue;                 // uniform
+    const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wv) * rest_tokens;
+    uint64_t without = __ballot(lane < rest_tokens && t0 + lane < T && slot[min(t0 + lane, T - 1)] < 0);
+    for (; without; without &= without - 1) {     // uniform
+      const int64_t t = t0 + __builtin_ffsll((long long)without) - 1;
       const u32x4 *from = (const u32x4 *)base + t * vecs;
       u32x4 *to = (u32x4 *)out + t * vecs;
 #pragma unroll 4
@@ -427,19 +425,13 @@ __global__ __launch_bounds__(256) void transpose_kernel(Transpose a, Transpose b
 }
 
 // Outer products: grad[e][r][c] (or [c][r] if T_OUT) = by * sum over the
-// adapter's tokens of p[t][r] q[t][c], for a piece of `chunk` tokens and 32 NT
-// columns.  A lane takes NT consecutive columns of 8 tokens' rows at a time
-// (column NT c + o of tile o), so a wave reads whole lines and turns them to
-// the matrix cores' token-major operands in registers.  An adapter of one
-// piece is done; the pieces of the others go to `part` (a slot of R x C
-// each), which outer_sum_kernel adds up.
-template <int NT>
-struct Cols;
-template <>
-struct Cols<2> { typedef uint32_t type __attribute__((ext_vector_type(1))); };
-template <>
-struct Cols<4> { typedef u32x2 type; };
-
+// adapter's tokens of p[t][r] q[t][c], for a piece of `chunk` tokens and 16 NT
+// columns.  MF: 16-row blocks of the rank.  A step takes 32 tokens, lane (c, g)
+// the tokens 8 g .. 8 g + 7: their columns NT c + o for tile o (16 lanes read
+// 16 NT consecutive columns) and their ranks 16 f + c, turned to the matrix
+// cores' token-major operands in registers.  An adapter of one piece is done;
+// the pieces of the others go to `part` (a slot of R x C each), which
+// outer_sum_kernel adds up.
 template <int MF, int NT, bool T_OUT>
 __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__ offsets,
                                                          const int *__restrict__ row_src, int N, int chunk,
@@ -447,25 +439,26 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
                                                          const uint16_t *__restrict__ q, int C,
                                                          const float *__restrict__ scale, float *__restrict__ grad,
                                                          float *__restrict__ part, int blocks) {
-  typedef typename Cols<NT>::type Row;
-  constexpr int kRing = 2;                        // steps of 16 tokens in flight
-  __shared__ __attribute__((aligned(16))) float s_tile[kWaves * 2 * 16 * kWave];   // [wave][tile][quad][lane][4]
+  typedef typename Run<NT>::type Cols;
+  constexpr int kRing = MF <= 4 ? 2 : 1;          // steps of 32 tokens in flight
+  constexpr int kMine = NT / kWaves;              // tiles a wave adds up
+  __shared__ __attribute__((aligned(16))) f32x4 s_tile[NT * kWaves * kWave];   // [tile][wave][lane]
   extern __shared__ __attribute__((aligned(16))) int s_src[];   // the piece's tokens, padded with -1
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int c = lane & 31, g = lane >> 5;
-  const int c0 = (blockIdx.x % blocks) * 32 * NT;
+  const int c = lane & 15, g = lane >> 4;
+  const int c0 = (blockIdx.x % blocks) * 16 * NT;
   const Item it = find_item(offsets, N, chunk, true, blockIdx.x / blocks);
   if (it.expert < 0) return;                      // uniform
-  const int padded = (it.n + 15) / 16 * 16;
+  const int padded = (it.n + 31) / 32 * 32;
   for (int i = tid; i < padded; i += kThreads) s_src[i] = i < it.n ? row_src[it.row0 + i] : -1;
   __syncthreads();
   const int col = min(c0 + NT * c, C - NT);
-  v16f acc[MF][NT];
+  f32x4 acc[MF][NT];
 #pragma unroll
   for (int f = 0; f < MF; ++f)
 #pragma unroll
-    for (int o = 0; o < NT; ++o) acc[f][o] = v16f{};
-  Row qv[kRing][8];
+    for (int o = 0; o < NT; ++o) acc[f][o] = f32x4{};
+  Cols qv[kRing][8];
   float pv[kRing][MF][8];
   auto load = [&](int k, int t0) {
 #pragma unroll
@@ -473,38 +466,38 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
       // rows of padding: token 0's, taken out below (the loads stay
       // unconditional, so that they are in flight together)
       const size_t t = (size_t)max(s_src[t0 + g * 8 + i], 0);
-      qv[k][i] = *(const Row *)(q + t * C + col);
+      qv[k][i] = *(const Cols *)(q + t * C + col);
 #pragma unroll
-      for (int f = 0; f < MF; ++f) pv[k][f][i] = p[t * R + min(f * 32 + c, R - 1)];
+      for (int f = 0; f < MF; ++f) pv[k][f][i] = p[t * R + min(f * 16 + c, R - 1)];
     }
     keep_loads();
   };
-  constexpr int kStep = kWaves * 16;
-  if (wv * 16 < padded) {                         // uniform
-    const int last = padded - 16;
+  auto multiply = [&](int k, int t0) {
+    bf16x8 b[NT];
+    const int *src = s_src + t0 + g * 8;
 #pragma unroll
-    for (int k = 0; k < kRing; ++k) load(k, min(wv * 16 + k * kStep, last));
-    auto multiply = [&](int k, int t0) {
-      bf16x8 b[NT];
-      const int *src = s_src + t0 + g * 8;
+    for (int i = 0; i < 8; ++i) {
+      const bool on = src[i] >= 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool on = src[i] >= 0;
+      for (int o = 0; o < NT; ++o)
+        b[o][i] = __builtin_bit_cast(__bf16, (uint16_t)(on ? qv[k][i][o >> 1] >> (16 * (o & 1)) : 0u));
 #pragma unroll
-        for (int o = 0; o < NT; ++o)
-          b[o][i] = __builtin_bit_cast(__bf16, (uint16_t)(on ? qv[k][i][o >> 1] >> (16 * (o & 1)) : 0u));
+      for (int f = 0; f < MF; ++f) pv[k][f][i] = on ? pv[k][f][i] : 0.0f;
+    }
 #pragma unroll
-        for (int f = 0; f < MF; ++f) pv[k][f][i] = on ? pv[k][f][i] : 0.0f;
-      }
+    for (int f = 0; f < MF; ++f) {
+      bf16x8 a0, a1, a2;
+      split3(pv[k][f], a0, a1, a2);
 #pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        bf16x8 a0, a1, a2;
-        split3(pv[k][f], a0, a1, a2);
+      for (int o = 0; o < NT; ++o) acc[f][o] = mfma(a0, b[o], mfma(a1, b[o], mfma(a2, b[o], acc[f][o])));
+    }
+  };
+  constexpr int kStep = kWaves * 32;
+  if (wv * 32 < padded) {                         // uniform
+    const int last = padded - 32;
 #pragma unroll
-        for (int o = 0; o < NT; ++o) acc[f][o] = mfma(a0, b[o], mfma(a1, b[o], mfma(a2, b[o], acc[f][o])));
-      }
-    };
-    int t0 = wv * 16;
+    for (int k = 0; k < kRing; ++k) load(k, min(wv * 32 + k * kStep, last));
+    int t0 = wv * 32;
     for (; t0 + (kRing - 1) * kStep < padded; t0 += kRing * kStep) {
 #pragma unroll
       for (int k = 0; k < kRing; ++k) {
@@ -520,36 +513,30 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
   float *to = it.pieces > 1 ? part + (size_t)it.slot * R * C : grad + (size_t)it.expert * R * C;
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
+    if (f > 0) __syncthreads();
 #pragma unroll
-    for (int o = 0; o < NT; o += 2) {             // two tiles at a time
-      if (f + o > 0) __syncthreads();
+    for (int o = 0; o < NT; ++o) s_tile[(o * kWaves + wv) * kWave + lane] = acc[f][o];
+    __syncthreads();
+    // ranks 16 f + 4 g + 0..3 of columns c0 + NT c + o for this wave's tiles
+    const int r = f * 16 + 4 * g, o0 = wv * kMine, cc = c0 + NT * c + o0;
+    f32x4 v[kMine];
 #pragma unroll
-      for (int d = 0; d < 2; ++d)
+    for (int d = 0; d < kMine; ++d) {
+      v[d] = s_tile[(o0 + d) * kWaves * kWave + lane];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const v16f &x = acc[f][o + d];
-          *(f32x4 *)(s_tile + (((wv * 2 + d) * 4 + b) * kWave + lane) * 4) =
-              f32x4{x[4 * b], x[4 * b + 1], x[4 * b + 2], x[4 * b + 3]};
-        }
-      __syncthreads();
-      // wave b adds up quad b of the lanes: ranks f * 32 + 8 b + 4 g + 0..3 of
-      // columns c0 + NT c + o, + 1
-      const int r = f * 32 + 8 * wv + 4 * g, cc = c0 + NT * c + o;
-      f32x4 v[2];
+      for (int k = 1; k < kWaves; ++k) v[d] += s_tile[((o0 + d) * kWaves + k) * kWave + lane];
+      v[d] *= by;
+    }
+    if (r < R && cc < C) {
+      if constexpr (T_OUT) {
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        v[d] = *(const f32x4 *)(s_tile + ((d * 4 + wv) * kWave + lane) * 4);
+        for (int d = 0; d < kMine; ++d) *(f32x4 *)(to + (size_t)(cc + d) * R + r) = v[d];
+      } else {
 #pragma unroll
-        for (int k = 1; k < kWaves; ++k) v[d] += *(const f32x4 *)(s_tile + (((k * 2 + d) * 4 + wv) * kWave + lane) * 4);
-        v[d] *= by;
-      }
-      if (r < R && cc < C) {
-        if constexpr (T_OUT) {
-          *(f32x4 *)(to + (size_t)cc * R + r) = v[0];
-          *(f32x4 *)(to + (size_t)(cc + 1) * R + r) = v[1];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) *(f32x2 *)(to + (size_t)(r + i) * C + cc) = f32x2{v[0][i], v[1][i]};
+        for (int i = 0; i < 4; ++i) {
+          float *line = to + (size_t)(r + i) * C + cc;
+          if constexpr (kMine == 2) *(f32x2 *)line = f32x2{v[0][i], v[kMine - 1][i]};
+          else *line = v[0][i];
         }
       }
     }
@@ -608,7 +595,7 @@ hipError_t run_down(const ep_handle_t &h, const void *rows, int K, const void *w
   if (mf == 1) EP_DOWN(1, 8);
   else if (mf == 2) EP_DOWN(2, 8);
   else if (mf <= 4) EP_DOWN(4, 8);
-  else EP_DOWN(8, 4);                             // 16 lines of LDS a wave and block
+  else EP_DOWN(8, 4);                             // LDS: 20 KB a wave
 #undef EP_DOWN
   return hipGetLastError();
 }
@@ -617,13 +604,15 @@ hipError_t run_up(const ep_handle_t &h, const Down &down, const void *w, int R, 
                   hipStream_t s) {
   const int rs = operand_ranks(R) / 16, nt = rs <= 2 ? 8 : 4;
   const int blocks = (C + kWaves * 16 * nt - 1) / (kWaves * 16 * nt);
-  const int64_t waves = (h.num_tokens + kWaves - 1) / kWaves, rest = out == base ? 0 : waves < 256 ? waves : 256;
+  // tokens a wave looks at for the rows without an adapter: 256 workgroups, then more tokens
+  const int64_t per = h.num_tokens / (256 * kWaves) + 1, rest_tokens = per < kWave ? per : kWave;
+  const int64_t rest = out == base ? 0 : (h.num_tokens + kWaves * rest_tokens - 1) / (kWaves * rest_tokens);
   const int64_t items = items_upper(h, rs <= 2 ? 64 : 32);
   const dim3 grid((unsigned)(items * blocks + rest)), block(kThreads);
 #define EP_UP_PART(RS, NT, STEPS, PART)                                                                        \
   hipLaunchKernelGGL((up_kernel<RS, NT, STEPS, PART>), grid, block, 0, s, h.offsets, h.row_src, h.slot,        \
                      h.num_experts, down, h.num_tokens, (const uint16_t *)w, R, (const uint16_t *)base,        \
-                     (uint16_t *)out, C, blocks, (int)rest)
+                     (uint16_t *)out, C, blocks, (int)rest, (int)rest_tokens)
 #define EP_UP(RS, NT, STEPS)                     \
   if (down.splits > 1) EP_UP_PART(RS, NT, STEPS, true); \
   else EP_UP_PART(RS, NT, STEPS, false)
@@ -643,18 +632,18 @@ hipError_t run_up(const ep_handle_t &h, const Down &down, const void *w, int R, 
 template <bool T_OUT>
 hipError_t run_outer(const ep_handle_t &h, const float *p, int R, const void *q, int C, const float *scale, float *grad,
                      float *part, hipStream_t s) {
-  const int chunk = outer_chunk(R), mf = (R + 31) / 32, nt = mf <= 2 ? 4 : 2;
-  const int blocks = (C + 32 * nt - 1) / (32 * nt);
+  const int chunk = outer_chunk(R), mf = (R + 15) / 16, nt = mf <= 2 ? 8 : 4;
+  const int blocks = (C + 16 * nt - 1) / (16 * nt);
   const int64_t items = h.max_rows / chunk + h.num_experts;
   const dim3 grid((unsigned)(items * blocks)), block(kThreads);
   const size_t lds = (size_t)chunk * 4;
 #define EP_OUTER(MF, NT)                                                                                      \
   hipLaunchKernelGGL((outer_kernel<MF, NT, T_OUT>), grid, block, lds, s, h.offsets, h.row_src, h.num_experts, chunk, p, \
                      R, (const uint16_t *)q, C, scale, grad, part, blocks)
-  if (mf == 1) EP_OUTER(1, 4);
-  else if (mf == 2) EP_OUTER(2, 4);
-  else if (mf == 3) EP_OUTER(3, 2);
-  else EP_OUTER(4, 2);
+  if (mf == 1) EP_OUTER(1, 8);
+  else if (mf == 2) EP_OUTER(2, 8);
+  else if (mf <= 4) EP_OUTER(4, 4);
+  else EP_OUTER(8, 4);
 #undef EP_OUTER
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || h.max_rows <= chunk) return e;

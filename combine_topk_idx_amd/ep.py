@@ -185,14 +185,14 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-def _check_args(*specs) -> None:
+def _check_args(*specs) -> int:
     """Host checks of tensor arguments before their pointers reach the
     library, which can only check pointers and byte counts.  Each spec is
     (tensor, name, dtype, shape, min_numel) with None for "any"; raw integer
     pointers and None tensors pass unchecked.  Every tensor's dtype, shape,
     density and size, then that all of them are on one GPU.  The common case
     (everything valid) reads each attribute once; the messages are built
-    only on failure."""
+    only on failure.  Returns the GPU's index (-2 if there was no tensor)."""
     dev, dev_name = -2, None
     for t, name, dtype, shape, min_numel in specs:
         if t is None or type(t) is int:
@@ -209,6 +209,7 @@ def _check_args(*specs) -> None:
             raise EpError(EP_ERR_INVALID_ARG, f"{name} is on {t.device}, {dev_name} on another device")
     if dev == -1:
         raise EpError(EP_ERR_INVALID_ARG, f"{dev_name} must be a GPU tensor (got cpu)")
+    return dev
 
 
 def _explain(t, name, dtype, shape, min_numel) -> None:
@@ -480,9 +481,9 @@ def ep_moe_pack_weights_ex(weights, scales, num_experts: int, rows: int, k: int,
     if sb:
         specs += [(scales, "scales", torch.uint8, (num_experts, rows, k // 32), None),
                   (packed_scales, "packed_scales", torch.uint8, (sb,), None)]
-    _check_here(*specs)
+    stream = _check_here(stream, *specs)
     _check(_lib.ep_moe_pack_weights_ex(_ptr(weights), _ptr(scales), num_experts, rows, k, q, int(gate_up),
-                                       _ptr(packed_weights), _ptr(packed_scales), _stream(stream)))
+                                       _ptr(packed_weights), _ptr(packed_scales), stream))
 
 
 def _pack_moe_weights_ex(weights, scales, gate_up, quant, stream):
@@ -496,15 +497,18 @@ def _pack_moe_weights_ex(weights, scales, gate_up, quant, stream):
     return pw, ps
 
 
-def _check_here(*specs) -> None:
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _check_here(stream, *specs) -> Optional[int]:
     """_check_args, and that the tensors' GPU is the current one (whose
-    stream the launch goes to)."""
-    _check_args(*specs)
-    for t, name, *_ in specs:
-        if isinstance(t, torch.Tensor):
-            if t.get_device() != torch.cuda.current_device():
-                raise EpError(EP_ERR_INVALID_ARG, f"{name} is on {t.device}, not on the current device")
-            return
+    stream the launch goes to); returns the raw stream."""
+    dev = _check_args(*specs)
+    if dev >= 0 and dev != _current_device():
+        raise EpError(EP_ERR_INVALID_ARG, f"the tensors are on cuda:{dev}, not on the current device")
+    if stream is None and dev >= 0 and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def ep_moe_layer_workspace_bytes(num_tokens: int, num_topk: int, num_experts: int, hidden: int, inter: int) -> int:
@@ -530,10 +534,10 @@ def ep_moe_layer(x, topk_idx, topk_weights, num_experts: int, inter: int, w_quan
              (workspace, "workspace", None, None, None), (out, "out", torch.bfloat16, (num_tokens, hidden), None)]
     if s1:
         specs += [(w1_scales, "w1_scales", torch.uint8, (s1,), None), (w2_scales, "w2_scales", torch.uint8, (s2,), None)]
-    _check_here(*specs)
+    stream = _check_here(stream, *specs)
     _check(_lib.ep_moe_layer(_ptr(x), num_tokens, hidden, _ptr(topk_idx), idx_dtype, _ptr(topk_weights), num_topk,
                              num_experts, inter, q, _ptr(w1), _ptr(w1_scales), _ptr(w2), _ptr(w2_scales),
-                             _ptr(workspace), _nbytes(workspace), _ptr(out), _stream(stream)))
+                             _ptr(workspace), _nbytes(workspace), _ptr(out), stream))
 
 
 @functools.lru_cache(maxsize=64)
@@ -550,16 +554,16 @@ def _score(score) -> int:
     return int(score)
 
 
-def _router_args(logits, topk_idx, topk_weights, name, extra):
+def _router_args(stream, logits, topk_idx, topk_weights, name, extra):
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in _FLOAT:
         raise EpError(EP_ERR_INVALID_ARG, "logits must be a float32, bfloat16 or float16 [num_tokens, num_experts] tensor")
     T, E = logits.shape
     n, k, idx_dtype = _idx_args(topk_idx, None, None, None)
     if n != T:
         raise EpError(EP_ERR_INVALID_ARG, f"topk_idx must have {T} rows (got {n})")
-    _check_here((logits, "logits", None, None, None), (topk_idx, "topk_idx", None, None, None),
-                (topk_weights, name, torch.float32, (T, k), None), extra)
-    return T, E, k, idx_dtype
+    stream = _check_here(stream, (logits, "logits", None, None, None), (topk_idx, "topk_idx", None, None, None),
+                         (topk_weights, name, torch.float32, (T, k), None), extra)
+    return T, E, k, idx_dtype, stream
 
 
 def ep_router(logits, topk_idx, topk_weights, *, score="softmax", bias=None, num_groups: int = 1,
@@ -568,11 +572,11 @@ def ep_router(logits, topk_idx, topk_weights, *, score="softmax", bias=None, num
     """Writes topk_idx [T, k] (int32 / int64) and topk_weights (float32 [T, k])
     from the logits [T, E] (float32, bf16 or fp16)."""
     E = logits.shape[-1] if isinstance(logits, torch.Tensor) and logits.dim() else 0
-    T, E, k, idx_dtype = _router_args(logits, topk_idx, topk_weights, "topk_weights",
-                                      (bias, "bias", torch.float32, (E,), None))
+    T, E, k, idx_dtype, stream = _router_args(stream, logits, topk_idx, topk_weights, "topk_weights",
+                                              (bias, "bias", torch.float32, (E,), None))
     _check(_lib.ep_router(_ptr(logits), _FLOAT[logits.dtype], T, E, k, _score(score), _ptr(bias), num_groups,
                           topk_groups, group_top, int(bool(renormalize)), scale, _ptr(topk_idx), idx_dtype,
-                          _ptr(topk_weights), _stream(stream)))
+                          _ptr(topk_weights), stream))
 
 
 def ep_router_backward(logits, topk_idx, grad_weights, grad_logits, *, score="softmax", renormalize: bool = True,
@@ -580,11 +584,11 @@ def ep_router_backward(logits, topk_idx, grad_weights, grad_logits, *, score="so
     """Writes grad_logits (the logits' shape and dtype) from the gradient of
     ep_router's topk_weights; score, renormalize and scale as given there."""
     like = (logits.dtype, tuple(logits.shape)) if isinstance(logits, torch.Tensor) else (None, None)
-    T, E, k, idx_dtype = _router_args(logits, topk_idx, grad_weights, "grad_weights",
-                                      (grad_logits, "grad_logits", *like, None))
+    T, E, k, idx_dtype, stream = _router_args(stream, logits, topk_idx, grad_weights, "grad_weights",
+                                              (grad_logits, "grad_logits", *like, None))
     _check(_lib.ep_router_backward(_ptr(logits), _FLOAT[logits.dtype], T, E, k, _score(score), int(bool(renormalize)),
                                    scale, _ptr(topk_idx), idx_dtype, _ptr(grad_weights), _ptr(grad_logits),
-                                   _stream(stream)))
+                                   stream))
 
 
 def ep_lora_workspace_bytes(rows: int, in_features: int, out_features: int, rank: int, num_adapters: int,
@@ -609,12 +613,13 @@ def ep_lora(handle: ep_handle_t, x, a, b, out, down, workspace, *, scale=None, b
     down float32 [T, rank] (kept for ep_lora_backward).  base may be out."""
     T, N, rank, fin, fout = _lora_shapes(handle, a, b)
     bf = torch.bfloat16
-    _check_here((x, "x", bf, (T, fin), None), (a, "a", bf, None, None), (b, "b", bf, (N, fout, rank), None),
-                (out, "out", bf, (T, fout), None), (down, "down", torch.float32, (T, rank), None),
-                (workspace, "workspace", None, None, None), (scale, "scale", torch.float32, (N,), None),
-                (base, "base", bf, (T, fout), None))
+    stream = _check_here(
+        stream, (x, "x", bf, (T, fin), None), (a, "a", bf, None, None), (b, "b", bf, (N, fout, rank), None),
+        (out, "out", bf, (T, fout), None), (down, "down", torch.float32, (T, rank), None),
+        (workspace, "workspace", None, None, None), (scale, "scale", torch.float32, (N,), None),
+        (base, "base", bf, (T, fout), None))
     _check(_lib.ep_lora(ctypes.byref(handle), _ptr(x), fin, fout, rank, _ptr(a), _ptr(b), _ptr(scale), _ptr(base),
-                        _ptr(out), _ptr(down), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+                        _ptr(out), _ptr(down), _ptr(workspace), _nbytes(workspace), stream))
 
 
 def ep_lora_backward(handle: ep_handle_t, grad_out, x, a, b, down, grad_x, grad_a, grad_b, workspace, *, scale=None,
@@ -623,14 +628,15 @@ def ep_lora_backward(handle: ep_handle_t, grad_out, x, a, b, down, grad_x, grad_
     be grad_x), grad_a and grad_b (float32, the shapes of a and b)."""
     T, N, rank, fin, fout = _lora_shapes(handle, a, b)
     bf, f32 = torch.bfloat16, torch.float32
-    _check_here((grad_out, "grad_out", bf, (T, fout), None), (x, "x", bf, (T, fin), None), (a, "a", bf, None, None),
-                (b, "b", bf, (N, fout, rank), None), (down, "down", f32, (T, rank), None),
-                (grad_x, "grad_x", bf, (T, fin), None), (grad_a, "grad_a", f32, (N, rank, fin), None),
-                (grad_b, "grad_b", f32, (N, fout, rank), None), (workspace, "workspace", None, None, None),
-                (scale, "scale", f32, (N,), None), (grad_base, "grad_base", bf, (T, fin), None))
+    stream = _check_here(
+        stream, (grad_out, "grad_out", bf, (T, fout), None), (x, "x", bf, (T, fin), None), (a, "a", bf, None, None),
+        (b, "b", bf, (N, fout, rank), None), (down, "down", f32, (T, rank), None),
+        (grad_x, "grad_x", bf, (T, fin), None), (grad_a, "grad_a", f32, (N, rank, fin), None),
+        (grad_b, "grad_b", f32, (N, fout, rank), None), (workspace, "workspace", None, None, None),
+        (scale, "scale", f32, (N,), None), (grad_base, "grad_base", bf, (T, fin), None))
     _check(_lib.ep_lora_backward(ctypes.byref(handle), _ptr(grad_out), _ptr(x), fin, fout, rank, _ptr(a), _ptr(b),
                                  _ptr(scale), _ptr(down), _ptr(grad_base), _ptr(grad_x), _ptr(grad_a), _ptr(grad_b),
-                                 _ptr(workspace), _nbytes(workspace), _stream(stream)))
+                                 _ptr(workspace), _nbytes(workspace), stream))
 
 
 def ep_read_status(handle: ep_handle_t, stream=None) -> int:
