@@ -656,6 +656,9 @@ ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num
     return fail(EP_ERR_INVALID_ARG, "%s: grad_weights is NULL or misaligned", fn);
   if (num_tokens > 0 && (!grad_logits || !aligned(grad_logits, dtype == EP_FLOAT_F32 ? 4 : 2)))
     return fail(EP_ERR_INVALID_ARG, "%s: grad_logits is NULL or not aligned to its dtype", fn);
+  const size_t bytes = (size_t)num_tokens * num_experts * (dtype == EP_FLOAT_F32 ? 4 : 2);
+  if (grad_logits != logits && overlap(grad_logits, bytes, logits, bytes))
+    return fail(EP_ERR_INVALID_ARG, "%s: grad_logits overlaps logits in part", fn);
   const ep::RouterArgs a{logits, dtype, num_tokens, num_experts, num_topk, score, nullptr, 1, 1, 1, renormalize,
                          scale};
   const hipError_t e = ep::launch_router_backward(a, topk_idx, idx_dtype == EP_IDX_INT64, grad_weights, grad_logits,

@@ -310,7 +310,7 @@ __device__ __forceinline__ int wave_route(const RouterArgs &a, int64_t t, WaveLd
           const double v = s.key[lane * size + j];
           if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) b1 = v;
         }
-        s.rank[lane] = a.top == 2 ? b0 + b1 : b0;
+        s.rank[lane] = a.top == 1 ? b0 : b1 > kNone ? b0 + b1 : kNone;   // no second key: last, even beside +inf
       }
       wave_lds_fence();
     }

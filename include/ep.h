@@ -424,7 +424,8 @@ ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, cons
  *   topk_weights[t, j] = scale * s_j, divided by the sum of the row's chosen
  *   s when renormalize is set
  * Without a bias the keys are the logits themselves (both scores rise with
- * them).  Keys with a bias are compared as float64.  An expert whose logit
+ * them).  Keys with a bias and sums of two scores are compared as float64, to
+ * 43 significant bits.  An expert whose logit
  * or key is -inf or NaN is never chosen (+inf counts as the largest finite
  * logit); a row that has fewer than k experts left gets -1 with weight 0 in its last places.
  *   logits       device [T, E] of dtype, aligned to it
@@ -444,9 +445,8 @@ ep_status_t ep_router(const void *logits, ep_float_t dtype, int64_t num_tokens, 
  * constants, the bias has none).
  *   topk_idx      device [T, k]: ep_router's ids (-1 and ids outside [0, E): no gradient)
  *   grad_weights  device float32 [T, k]
- *   grad_logits   device [T, E] of dtype, written in whole; may be logits'
- *                 own memory only if it is not needed afterwards and not
- *                 overlapped otherwise */
+ *   grad_logits   device [T, E] of dtype, written in whole; may be `logits`
+ *                 itself, not overlap it in part */
 ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num_tokens, int32_t num_experts,
                                int32_t num_topk, ep_score_t score, int32_t renormalize, float scale,
                                const void *topk_idx, ep_idx_dtype_t idx_dtype, const float *grad_weights,

@@ -56,7 +56,7 @@ def route_row(z, k, *, score="softmax", bias=None, num_groups=1, topk_groups=1, 
         rank = []
         for g in range(num_groups):
             best = sorted(by[g * size:(g + 1) * size], reverse=True)[:group_top]
-            rank.append((-sum(best), g))
+            rank.append((-sum(best) if min(best) > -np.inf else np.inf, g))
         kept = {g for _, g in sorted(rank)[:topk_groups]}
         key = np.array([key[e] if e // size in kept else -np.inf for e in range(E)])
     order = sorted((-key[e], e) for e in range(E) if key[e] > -np.inf)[:k]

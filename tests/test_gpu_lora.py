@@ -90,6 +90,8 @@ CASES = [
     (40, 64, 160, 72, 2), (40, 96, 64, 96, 3), (33, 64, 64, 112, 2), (64, 64, 64, 48, 1),
     # adapters of several pieces (256 tokens at rank 8), beside some of one and of none
     (1100, 64, 32, 8, 2), (900, 32, 96, 8, 9), (700, 160, 64, 16, 65), (2300, 32, 32, 40, 3),
+    # more tokens than the reduction axis is split for
+    (17000, 128, 64, 8, 3),
 ]
 
 

@@ -74,6 +74,7 @@ CASES = [
     (128, 128, 64, 3, 16),          # 2048 pairs, repeated ids
     (2, 1088, 64, 512, 8),
     (13, 64, 1088, 40, 6),
+    (64, 2048, 768, 16, 4),
 ]
 
 

@@ -192,3 +192,17 @@ def test_many_tokens_grouped(ep, T):
     assert np.array_equal(idx.cpu().numpy(), OR.route(z.double().numpy(), 8)[0])
     with pytest.raises(ep.EpError):
         ep.ep_router(torch.zeros(256, max(T, 2), device=DEV).t(), idx, w)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 4), (60, 5)])
+def test_infinite_biases(ep, E, groups):
+    """+inf chooses first, -inf and NaN never; a group with one key left ranks last by sums, even if it is +inf."""
+    size = E // groups
+    z = _logits(3, 12, E, torch.float32)
+    z[5, 1:size] = -float("inf")                              # group 0 of row 5 has one expert
+    bias = torch.zeros(E)
+    bias[0], bias[size], bias[size + 1], bias[2 * size] = float("inf"), float("nan"), -float("inf"), float("inf")
+    for top in (1, 2):
+        ids, _ = _check(ep, z, 6, score="sigmoid", bias=bias, num_groups=groups, topk_groups=2, group_top=top)
+        assert (ids[:, 0] == 0).sum() >= 11 and not np.isin(ids, [size, size + 1]).any()
+        _check(ep, z, 6, score="softmax", bias=bias, num_groups=groups, topk_groups=groups - 1, group_top=top)

@@ -40,7 +40,7 @@ def test_router_of_no_tokens_is_fine(ep):
 
 @pytest.mark.parametrize("kw", [dict(z=None), dict(dtype=5), dict(k=17), dict(score=-1), dict(renorm=-1),
                                 dict(idx=FAKE + 4), dict(grad=None), dict(grad=FAKE + 1), dict(dz=None),
-                                dict(dz=FAKE + 2)])
+                                dict(dz=FAKE + 2), dict(dz=FAKE + 64), dict(dz=FAKE - 64)])
 def test_router_backward_rejects(ep, kw):
     a = dict(z=FAKE, dtype=0, T=4, E=16, k=2, score=0, renorm=1, idx=FAKE, grad=FAKE, dz=FAKE)
     a.update(kw)
