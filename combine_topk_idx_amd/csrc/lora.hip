@@ -376,18 +376,45 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ of
     return;
   }
   const int unit = blockIdx.x - rest;
-  const int first = (unit % blocks * kWaves + wv) * 16 * NT;
+  const int block0 = unit % blocks * kWaves * 16 * NT, first = block0 + wv * 16 * NT;
   const Item it = find_item(offsets, N, 16 * STEPS, false, unit / blocks);
-  if (it.expert < 0 || first >= C) return;        // uniform
+  if (it.expert < 0) return;                      // uniform
   const int src = lane < it.n ? row_src[it.row0 + lane] : -1;
   const int col = first + NT * c;
-  bf16x8 wv16[NT][RS];
+  bf16x8 wv16[NT][RS];                            // ranks past R meet zeros in the operand
+  if constexpr (RS == 1 && !PART) {
+    // little of w and 64 rows to use it: read in the operand order, beside the base
+    if (first >= C) return;                       // uniform
 #pragma unroll
-  for (int o = 0; o < NT; ++o) {
-    const uint16_t *wr = w + ((size_t)it.expert * C + min(col + o, C - 1)) * R;
+    for (int o = 0; o < NT; ++o)
+      wv16[o][0] = *(const bf16x8 *)(w + ((size_t)it.expert * C + min(col + o, C - 1)) * R + min((g & 1) * 8, R - 8));
+  } else {
+    // The workgroup's columns of w are one run of memory, read as it lies (16
+    // bytes a thread: unit u) and turned to the operand order through LDS,
+    // where the units of a line of 8 lie exchanged by their lane's number, so
+    // that reads of 8 lanes fall in distinct banks.  4099 tokens at rank 64:
+    // 17 us, against 21 in the operand order (an access a lane); 8192 at rank
+    // 16: 54 against 51, the base waiting behind it.
+    constexpr int kUnits = kWaves * 16 * NT * 2 * RS, kLoads = kUnits / kThreads;
+    __shared__ __attribute__((aligned(16))) u32x4 s_w[kUnits];
+    const int per = R / 8, lane_units = NT * per; // units of a column, of a lane's columns
+    auto place = [&](int u) { return lane_units % 8 == 0 ? u ^ (u / lane_units & 7) : u; };
+    const u32x4 *from = (const u32x4 *)(w + ((size_t)it.expert * C + block0) * R);
+    const int here = min(kWaves * 16 * NT, C - block0) * per;
+    u32x4 in[kLoads];
 #pragma unroll
-    for (int k = 0; k < RS; ++k)                  // ranks past R meet zeros in the operand
-      wv16[o][k] = *(const bf16x8 *)(wr + min(k * 16 + (g & 1) * 8, R - 8));
+    for (int i = 0; i < kLoads; ++i) in[i] = from[min(i * kThreads + tid, here - 1)];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (i * kThreads + tid < here) s_w[place(i * kThreads + tid)] = in[i];
+    __syncthreads();
+    if (first >= C) return;                       // uniform
+#pragma unroll
+    for (int o = 0; o < NT; ++o)
+#pragma unroll
+      for (int k = 0; k < RS; ++k)
+        wv16[o][k] = __builtin_bit_cast(bf16x8, s_w[place((min(col + o, C - 1) - block0) * per +
+                                                          min(2 * k + (g & 1), per - 1))]);
   }
   // rows of padding come last in a block: none from the first on
   const int n = __popcll(__ballot(src >= 0));
