@@ -382,6 +382,9 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
                                                               const uint16_t *__restrict__ lists, float *y,
                                                               uint32_t *done, int blocks) {
   __shared__ __attribute__((aligned(16))) float s_tile[kWaves * NG * 16 * kWave];
+  constexpr int kRow = 32 * NG + 4;               // floats of a pair's row in LDS
+  __shared__ __attribute__((aligned(16))) float s_row[kTile * kRow];
+  __shared__ int s_pair[kTile];
   __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int blk = blockIdx.x % blocks, rank = blockIdx.x / blocks, P = (int)a.T * a.k;
@@ -405,13 +408,21 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
       if (r0 > 0) lds_barrier();
       leave_partials<NG>(s_tile, acc);
       lds_barrier();
+      // through LDS, so that a pair's 32 NG columns leave as whole lines: past
+      // the L2 every store is a write of its own (as 8-byte pieces of 16 lines
+      // they were 12 % of the launch at 128 tokens)
+      if (wv == 0 && lane < kTile) s_pair[lane] = pair;
       for (int qb = wv; qb < NG * 4; qb += kWaves) {
         const int q = qb >> 2, h = qb & 3;
-        if (r0 + (lane & 31) >= n) break;
-        const f32x4 v = summed<NG>(s_tile, q, h, lane);
-        uint64_t *to = (uint64_t *)(y + (size_t)pair * a.hidden + 32 * (g0 + q) + 8 * h + 4 * (lane >> 5));
-        put_shared(to, v.x, v.y);
-        put_shared(to + 1, v.z, v.w);
+        if ((lane & 31) < n - r0)
+          *(f32x4 *)(s_row + (lane & 31) * kRow + 32 * q + 8 * h + 4 * (lane >> 5)) = summed<NG>(s_tile, q, h, lane);
+      }
+      lds_barrier();
+      const int rows = min(kTile, n - r0);
+      for (int i = tid; i < rows * 16 * NG; i += kThreads) {
+        const int row = i / (16 * NG), two = i - row * (16 * NG);
+        const float *v = s_row + row * kRow + 2 * two;
+        put_shared((uint64_t *)(y + (size_t)s_pair[row] * a.hidden + 32 * g0) + two, v[0], v[1]);
       }
     }
     // y goes past the die's L2 (agent scope), and the wait below holds until
