@@ -306,14 +306,27 @@ __device__ __forceinline__ int wave_route(const RouterArgs &a, int64_t t, WaveLd
     if (a.groups > 1 && (pass == 0 || a.bias || !by_sum)) {
       const int size = E / a.groups;
       wave_lds_fence();
-      if (lane < a.groups) {
-        double b0 = kNone, b1 = kNone;
-        for (int j = 0; j < size; ++j) {
-          const double v = s.key[lane * size + j];
+      // `span` lanes look through a group, their best two are joined
+      int span = kWave;
+      while (span * a.groups > kWave) span >>= 1;
+      const int group = lane / span;
+      double b0 = kNone, b1 = kNone;
+      if (group < a.groups) {
+#pragma unroll 4
+        for (int j = lane % span; j < size; j += span) {
+          const double v = s.key[group * size + j];
           if (v > b0) { b1 = b0; b0 = v; } else if (v > b1) b1 = v;
         }
-        s.rank[lane] = a.top == 1 ? b0 : b1 > kNone ? b0 + b1 : kNone;   // no second key: last, even beside +inf
       }
+      for (int d = 1; d < span; d <<= 1) {
+        const double o0 = __shfl_xor(b0, d), o1 = __shfl_xor(b1, d);
+        const double lo = o0 < b0 ? o0 : b0, hi = o0 < b0 ? b0 : o0, second = o1 > b1 ? o1 : b1;
+        b0 = hi;
+        b1 = lo > second ? lo : second;
+      }
+      // no second key: last, even beside +inf
+      if (group < a.groups && lane % span == 0)
+        s.rank[group] = a.top == 1 ? b0 : b1 > kNone ? b0 + b1 : kNone;
       wave_lds_fence();
     }
   }
