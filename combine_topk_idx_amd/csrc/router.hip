@@ -213,14 +213,11 @@ __device__ __forceinline__ void sort_run(double (&v)[N]) {
             v[i + j + q] = min64(a, b);
           }
 }
-// The L largest of two descending lists, one here and one in the lane CTRL
-// names: the element-wise maximum against the other's reverse holds them as a
-// bitonic sequence, which log L exchange steps sort.
-template <int CTRL, int L>
-__device__ __forceinline__ void merge_step(double (&v)[L]) {
-  double o[L];
-#pragma unroll
-  for (int i = 0; i < L; ++i) o[i] = dpp<CTRL>(v[L - 1 - i]);
+// The L largest of two descending lists, v and the one whose reverse is o: the
+// element-wise maximum holds them as a bitonic sequence, which log L exchange
+// steps sort.
+template <int L>
+__device__ __forceinline__ void merge_lists(double (&v)[L], const double (&o)[L]) {
 #pragma unroll
   for (int i = 0; i < L; ++i) v[i] = max64(v[i], o[i]);
 #pragma unroll
@@ -232,6 +229,21 @@ __device__ __forceinline__ void merge_step(double (&v)[L]) {
         v[i] = max64(a, b);
         v[i + d] = min64(a, b);
       }
+}
+// with the list of the lane CTRL names / of lane ^ d
+template <int CTRL, int L>
+__device__ __forceinline__ void merge_step(double (&v)[L]) {
+  double o[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) o[i] = dpp<CTRL>(v[L - 1 - i]);
+  merge_lists(v, o);
+}
+template <int L>
+__device__ __forceinline__ void merge_rows(double (&v)[L], int d) {
+  double o[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) o[i] = __shfl_xor(v[L - 1 - i], d);
+  merge_lists(v, o);
 }
 
 // log of the score, up to a constant of the row: z for a softmax,
@@ -282,9 +294,9 @@ __device__ __forceinline__ int wave_route(const RouterArgs &a, int64_t t, WaveLd
     sum = 0.0;
     for (int e = lane; e < E; e += kWave) {
       const float z = usable(logit<DT>(a.logits, t * E + e));
-      sum += z > -INFINITY ? exp((double)z - (double)top) : 0.0;
+      sum += z > -INFINITY ? exp64(fmax((double)z - (double)top, -700.0)) : 0.0;
     }
-    sum = wave_sum(sum);
+    sum = rcp64(wave_sum(sum));
   }
   const bool by_sum = a.groups > 1 && a.top == 2;
   // the keys; without a bias the group sums need the scores first
@@ -296,7 +308,7 @@ __device__ __forceinline__ int wave_route(const RouterArgs &a, int64_t t, WaveLd
         if (pass == 1 && !a.bias) {
           c = (double)z;
         } else {
-          c = softmax ? exp((double)z - (double)top) / sum : 1.0 / (1.0 + exp(-(double)z));
+          c = softmax ? exp64(fmax((double)z - (double)top, -700.0)) * sum : sigmoid64(z);
           if (a.bias) c += (double)a.bias[e];
         }
         if (!(c > kNone)) c = kNone;              // a NaN bias
@@ -344,23 +356,27 @@ __device__ __forceinline__ int wave_route(const RouterArgs &a, int64_t t, WaveLd
     for (int e = lane; e < E; e += kWave)
       if (!((kept >> (e / size)) & 1)) s.key[e] = kNone;
   }
-  int my_id = -1;
-  for (int j = 0; j < a.k; ++j) {
-    double best = kNone;
-    int at = INT32_MAX;
-    for (int e = lane; e < E; e += kWave)
-      if (s.key[e] > best) { best = s.key[e]; at = e; }
+  // the selection as on the row path, over the whole wave
+  double v[kMaxExperts / kWave], best[kMaxTopk];
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const double ob = __shfl_xor(best, d);
-      const int oa = __shfl_xor(at, d);
-      if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
-    }
-    if (!(best > kNone)) break;                   // uniform: nothing left
-    if (lane == j) my_id = at;
-    if ((at & (kWave - 1)) == lane) s.key[at] = kNone;
+  for (int i = 0; i < kMaxExperts / kWave; ++i) {
+    const int e = lane + i * kWave;
+    const double key = e < E ? s.key[e] : kNone;
+    v[i] = pack_key(key > kNone ? fmin(key, 1e300) + 0.0 : kNoKey, e);
   }
-  return my_id;
+  sort_run(v);
+#pragma unroll
+  for (int i = 0; i < kMaxTopk; ++i) best[i] = i < kMaxExperts / kWave ? v[i < kMaxExperts / kWave ? i : 0] : kNoKey;
+  merge_step<kXor1>(best);
+  merge_step<kXor2>(best);
+  merge_step<kRor4>(best);
+  merge_step<kRor8>(best);
+  merge_rows(best, 16);
+  merge_rows(best, 32);
+  double mine = best[0];
+#pragma unroll
+  for (int i = 1; i < kMaxTopk; ++i) mine = lane == i ? best[i] : mine;
+  return lane < a.k && is_key(mine) ? expert_in(mine) : -1;
 }
 
 // The weight of choice `lane` (of 16 lanes, id -1: none) and its store;
