@@ -87,11 +87,6 @@ __device__ __forceinline__ T pin(T v) {
   return v;
 }
 
-// Loads issued before this point stay before it: without it the optimizer
-// moves the loads of a software ring from the end of one iteration to the
-// start of the next, right before their use.
-__device__ __forceinline__ void keep_loads() { asm volatile("" ::: "memory"); }
-
 // DPP lane exchanges (wave64, no LDS traffic).  Controls: quad_perm
 // [1,0,3,2] = 0xB1, [2,3,0,1] = 0x4E; row_ror:n = 0x120 + n (rotate within a
 // row of 16 lanes).

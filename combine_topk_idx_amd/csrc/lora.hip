@@ -26,6 +26,7 @@
 #include "common.hpp"
 #include "formats.hpp"
 #include "lora.hpp"
+#include "ring.hpp"
 
 namespace ep {
 

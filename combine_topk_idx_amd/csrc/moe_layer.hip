@@ -25,6 +25,7 @@
 #include "common.hpp"
 #include "formats.hpp"
 #include "moe_layer.hpp"
+#include "ring.hpp"
 
 namespace ep {
 
