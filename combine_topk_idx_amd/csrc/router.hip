@@ -255,7 +255,10 @@ __device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(
 
 // ------------------------------------------------------------ wave path
 // One token per wave with its keys in LDS: group shapes that do not fall on
-// whole lanes.
+// whole lanes, whose ranks are found by all lanes from the keys there.  The
+// selection then is the row path's over 64 lanes (two more merges).  800
+// tokens of 238 experts in 2 groups 9.6 us a call; ranking every key against
+// its group and k reductions over the wave instead took 27.
 struct WaveLds {
   double key[kMaxExperts], rank[kMaxGroups];
 };
