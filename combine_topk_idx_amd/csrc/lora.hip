@@ -429,28 +429,47 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ of
   }
 }
 
-// dst[n][j][i] = src[n][i][j] of two stacks of matrices, in 32 x 32 tiles
+// dst[n][j][i] = src[n][i][j] of two stacks of matrices, in 64 x 64 tiles read
+// and written in 16-byte chunks (rows and columns are multiples of 8), for the
+// adapters with rows only.  A tile's rows are 33 words apart in LDS: a chunk's
+// 8 rows read down a column by 64 lanes fall in distinct banks.  38 adapters
+// of rank 64, half of them in use, 5888 + 3392 wide: 9.6 us; 32 x 32 tiles of
+// 2-byte accesses over all of them took 32.
 struct Transpose {
   const uint16_t *src;
   int rows, cols;
   uint16_t *dst;
 };
-__global__ __launch_bounds__(256) void transpose_kernel(Transpose a, Transpose b, int tiles_a) {
-  __shared__ uint16_t tile[32][33];
+constexpr int kTurn = 64;
+__global__ __launch_bounds__(256) void transpose_kernel(const int *__restrict__ offsets, Transpose a, Transpose b,
+                                                        int tiles_a) {
+  __shared__ uint32_t tile[kTurn * 33];
   const Transpose &m = (int)blockIdx.x < tiles_a ? a : b;
   const int at = (int)blockIdx.x < tiles_a ? blockIdx.x : blockIdx.x - tiles_a;
   const int rows = m.rows, cols = m.cols;
-  const int tr = (rows + 31) / 32, tc = (cols + 31) / 32;
+  const int tr = (rows + kTurn - 1) / kTurn, tc = (cols + kTurn - 1) / kTurn;
   const int n = at / (tr * tc), in = at % (tr * tc);
-  const int i0 = in / tc * 32, j0 = in % tc * 32;
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  if (offsets[n] == offsets[n + 1]) return;       // uniform; nothing reads it
+  const int i0 = in / tc * kTurn, j0 = in % tc * kTurn;
   const uint16_t *s = m.src + (size_t)n * rows * cols;
   uint16_t *d = m.dst + (size_t)n * rows * cols;
-  for (int i = y; i < 32; i += 8)
-    if (i0 + i < rows && j0 + x < cols) tile[i][x] = s[(size_t)(i0 + i) * cols + j0 + x];
+  const int q = threadIdx.x & 7, y = threadIdx.x >> 3;   // chunk of a line, line
+  for (int i = y; i < kTurn; i += 32)
+    if (i0 + i < rows && j0 + 8 * q < cols) {
+      const u32x4 v = *(const u32x4 *)(s + (size_t)(i0 + i) * cols + j0 + 8 * q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tile[i * 33 + 4 * q + k] = v[k];
+    }
   __syncthreads();
-  for (int j = y; j < 32; j += 8)
-    if (j0 + j < cols && i0 + x < rows) d[(size_t)(j0 + j) * rows + i0 + x] = tile[x][j];
+  const uint16_t *half = (const uint16_t *)tile;
+  for (int j = y; j < kTurn; j += 32)
+    if (j0 + j < cols && i0 + 8 * q < rows) {
+      u32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = half[(8 * q + 2 * k) * 66 + j] | (uint32_t)half[(8 * q + 2 * k + 1) * 66 + j] << 16;
+      *(u32x4 *)(d + (size_t)(j0 + j) * rows + i0 + 8 * q) = v;
+    }
 }
 
 // Outer products: grad[e][r][c] (or [c][r] if T_OUT) = by * sum over the
@@ -479,6 +498,18 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
   const int c0 = (blockIdx.x % blocks) * 16 * NT;
   const Item it = find_item(offsets, N, chunk, true, blockIdx.x / blocks);
   if (it.expert < 0) return;                      // uniform
+  if (it.n == 0) {                                // uniform: zeros, in whole lines
+    const int here = min(16 * NT, C - c0);
+    float *to = grad + (size_t)it.expert * R * C;
+    if constexpr (T_OUT) {
+      for (int i = tid; i < here * R / 4; i += kThreads) *(f32x4 *)(to + (size_t)c0 * R + i * 4) = f32x4{};
+    } else {
+      const int quads = here / 4;
+      for (int i = tid; i < R * quads; i += kThreads)
+        *(f32x4 *)(to + (size_t)(i / quads) * C + c0 + i % quads * 4) = f32x4{};
+    }
+    return;
+  }
   const int padded = (it.n + 31) / 32 * 32;
   for (int i = tid; i < padded; i += kThreads) s_src[i] = i < it.n ? row_src[it.row0 + i] : -1;
   __syncthreads();
@@ -544,30 +575,43 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
     if (f > 0) __syncthreads();
+    // ranks 16 f + 4 g + 0..3 of columns c0 + NT c + o
+    const int r = f * 16 + 4 * g;
+    if constexpr (T_OUT) {                        // a wave takes tiles
 #pragma unroll
-    for (int o = 0; o < NT; ++o) s_tile[(o * kWaves + wv) * kWave + lane] = acc[f][o];
-    __syncthreads();
-    // ranks 16 f + 4 g + 0..3 of columns c0 + NT c + o for this wave's tiles
-    const int r = f * 16 + 4 * g, o0 = wv * kMine, cc = c0 + NT * c + o0;
-    f32x4 v[kMine];
+      for (int o = 0; o < NT; ++o) s_tile[(o * kWaves + wv) * kWave + lane] = acc[f][o];
+      __syncthreads();
+      const int o0 = wv * kMine, cc = c0 + NT * c + o0;
+      f32x4 v[kMine];
 #pragma unroll
-    for (int d = 0; d < kMine; ++d) {
-      v[d] = s_tile[(o0 + d) * kWaves * kWave + lane];
+      for (int d = 0; d < kMine; ++d) {
+        v[d] = s_tile[(o0 + d) * kWaves * kWave + lane];
 #pragma unroll
-      for (int k = 1; k < kWaves; ++k) v[d] += s_tile[((o0 + d) * kWaves + k) * kWave + lane];
-      v[d] *= by;
-    }
-    if (r < R && cc < C) {
-      if constexpr (T_OUT) {
+        for (int k = 1; k < kWaves; ++k) v[d] += s_tile[((o0 + d) * kWaves + k) * kWave + lane];
+        v[d] *= by;
+      }
+      if (r < R && cc < C) {
 #pragma unroll
         for (int d = 0; d < kMine; ++d) *(f32x4 *)(to + (size_t)(cc + d) * R + r) = v[d];
-      } else {
+      }
+    } else {                                      // a wave takes every fourth rank: NT columns in a row a lane
+      float *s_sum = (float *)s_tile;             // [tile][wave][rank of four][lane]
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float *line = to + (size_t)(r + i) * C + cc;
-          if constexpr (kMine == 2) *(f32x2 *)line = f32x2{v[0][i], v[kMine - 1][i]};
-          else *line = v[0][i];
-        }
+      for (int o = 0; o < NT; ++o)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_sum[((o * kWaves + wv) * 4 + i) * kWave + lane] = acc[f][o][i];
+      __syncthreads();
+      f32x4 v[NT / 4];
+#pragma unroll
+      for (int o = 0; o < NT; ++o) {
+        float x = s_sum[(o * kWaves * 4 + wv) * kWave + lane];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k) x += s_sum[((o * kWaves + k) * 4 + wv) * kWave + lane];
+        v[o / 4][o % 4] = x * by;
+      }
+      if (r < R && c0 + NT * c < C) {
+#pragma unroll
+        for (int d = 0; d < NT / 4; ++d) *(f32x4 *)(to + (size_t)(r + wv) * C + c0 + NT * c + 4 * d) = v[d];
       }
     }
   }
@@ -600,17 +644,20 @@ int64_t items_upper(const ep_handle_t &h, int tile) {
 }
 
 // Shares of a down product's axis.  Split where the tiles leave CUs idle, to
-// about two workgroups a CU with eight steps each; the up product then adds up
-// the shares in every column block, which costs more than it gains from about
-// half a tile a CU on.  Measured (us, down + up; in 7168): 128 tokens of 64
-// adapters of rank 16 (68 tiles) 10.8 + 7.2 whole, 7.3 + 9.0 in two shares,
-// 5.9 + 9.6 in four; 4099 tokens at rank 64 (136 tiles) 24 + 19 whole, 19 + 38
-// in two.
-int down_splits(const ep_handle_t &h, int K) {
+// about two workgroups a CU with eight steps each.  The up product then adds
+// up the shares of its rows' ranks in every column block, so shares x rows x
+// rank stays a third of the axis at most.  Measured (us, a whole call in 1, 2,
+// 4, 8 shares): 16 tokens of 8 adapters, 4096 wide, rank 128 33, 28, 27, 31;
+// rank 64 18.8, 17.1, 16.5, 17.4; 128 tokens of 16, 7168 wide, rank 32 20.9,
+// 17.8, 17.0, 18.6; rank 64 28, 24, 25, 30; 128 of 8, 4096 wide, rank 128 35,
+// 35, 38, 51; 600 of 8 39, 54, 67, 99.  From about half a tile a CU on whole:
+// 4099 tokens at rank 64 (136 tiles) 24 + 19, 19 + 38 in two.
+int down_splits(const ep_handle_t &h, int K, int R) {
   const int64_t items = items_upper(h, kTile);
   int s = 1;
   if (lora_rows(h) > kLoraSplitRows || items > 128) return s;
-  while (s < kLoraSplits && items * s * 2 <= 512 && K / 64 >= 2 * s * 8) s *= 2;
+  const int64_t rows = (h.num_tokens + h.num_experts - 1) / h.num_experts, mine = rows < kTile ? rows : kTile;
+  while (s < kLoraSplits && items * s * 2 <= 512 && K / 64 >= 2 * s * 8 && 2 * s * mine * R * 3 <= K) s *= 2;
   return s;
 }
 
@@ -690,7 +737,7 @@ hipError_t launch_lora(const LoraArgs &p, hipStream_t s) {
   if (p.h.num_tokens == 0) return hipSuccess;
   const LoraWs ws = lora_ws(lora_rows(p.h), p.in, p.out_features, p.rank, p.h.num_experts, 0);
   char *operand = p.ws + ws.operand, *part = p.ws + ws.part;
-  const Down down{(const uint16_t *)operand, (const float *)part, down_splits(p.h, p.in), 0, p.h.max_rows, p.scale, p.down};
+  const Down down{(const uint16_t *)operand, (const float *)part, down_splits(p.h, p.in, p.rank), 0, p.h.max_rows, p.scale, p.down};
   hipError_t e = run_down(p.h, p.x, p.in, p.a, p.rank, down, operand, part, s);
   if (e == hipSuccess) e = run_up(p.h, down, p.b, p.rank, p.base, p.out, p.out_features, s);
   return e;
@@ -709,10 +756,12 @@ hipError_t launch_lora_backward(const LoraGradArgs &p, hipStream_t s) {
     return e;
   }
   const Transpose tb{(const uint16_t *)p.b, p.out_features, R, bt}, ta{(const uint16_t *)p.a, R, p.in, at};
-  const int64_t rt = (R + 31) / 32, tiles_b = N * rt * ((p.out_features + 31) / 32), tiles_a = N * rt * ((p.in + 31) / 32);
-  hipLaunchKernelGGL(transpose_kernel, dim3((unsigned)(tiles_a + tiles_b)), dim3(256), 0, s, tb, ta, (int)tiles_b);
+  auto turns = [](int n) { return (int64_t)((n + kTurn - 1) / kTurn); };
+  const int64_t tiles_b = N * turns(R) * turns(p.out_features), tiles_a = N * turns(R) * turns(p.in);
+  hipLaunchKernelGGL(transpose_kernel, dim3((unsigned)(tiles_a + tiles_b)), dim3(256), 0, s, p.h.offsets, tb, ta,
+                     (int)tiles_b);
   e = hipGetLastError();
-  const Down down{(const uint16_t *)operand, (const float *)part, down_splits(p.h, p.out_features), 1, p.h.max_rows, p.scale,
+  const Down down{(const uint16_t *)operand, (const float *)part, down_splits(p.h, p.out_features, R), 1, p.h.max_rows, p.scale,
                   u};
   if (e == hipSuccess) e = run_down(p.h, p.grad_out, p.out_features, bt, R, down, operand, part, s);
   // grad_out once more while the last-level cache may still hold it

@@ -6,7 +6,7 @@
 namespace ep {
 
 constexpr int32_t kMaxRank = 128;
-constexpr int kLoraSplits = 8;                    // most shares of a down product's reduction axis
+constexpr int kLoraSplits = 4;                    // most shares of a down product's reduction axis
 constexpr int64_t kLoraSplitRows = 16384;         // and the most rows it is split for
 
 // Tokens of a piece of an adapter's gradient: its R x C partial sums then

@@ -104,6 +104,20 @@ def test_lora(ep, i):
     l.check(d)
 
 
+@pytest.mark.parametrize("T,fin,fout,r,n", [
+    # long axes and few rows an adapter: the down products in several shares, at every number of rank steps
+    (2, 2112, 2080, 24, 3), (5, 2080, 1056, 40, 7), (3, 3104, 2112, 64, 4), (2, 2080, 2080, 88, 5), (2, 3104, 4160, 128, 70),
+    # adapters without tokens beside some with: their gradients are zeros, whole or in part of a column block
+    (3, 160, 96, 32, 60), (40, 608, 32, 72, 33), (9, 32, 1184, 16, 500),
+])
+def test_lora_long_axes_and_idle_adapters(ep, T, fin, fout, r, n):
+    print(f"\n[case] lora {(T, fin, fout, r, n)}", flush=True)
+    l = Lora(ep, 90 + r, T, fin, fout, r, n, none=0.0, skew=False)
+    d = l.buffers()
+    l.run(d, l.handle())
+    l.check(d)
+
+
 @pytest.mark.parametrize("layout", [dict(row_align=48), dict(row_align=1024), dict(expert_capacity=70)])
 def test_lora_padded_layouts(ep, layout):
     l = Lora(ep, 60, 66, 96, 64, 16, 4, tmax=90, **layout)
