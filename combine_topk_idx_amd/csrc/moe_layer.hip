@@ -1,5 +1,5 @@
-// The whole expert layer of a MoE block for a few tokens, in two launches:
-// no receive rows, no layout, no combine pass.
+// The whole expert layer of a MoE block for a few tokens, in two launches
+// (three above 8 tokens): no receive rows, no layout, no combine pass.
 //
 // What is computed, for token t with ids e_j = topk_idx[t, j]:
 //   a_j    = silu(G[e_j] x_t) * (U[e_j] x_t)
@@ -19,7 +19,8 @@
 // float32 rows D a_j in the workspace, and the last workgroup to finish a
 // block of output columns (a counter per block, cleared by launch 1) sums
 // them over j in ascending order: the result does not depend on which
-// workgroup that is.
+// workgroup that is.  For more than 8 tokens a third launch sums them, in the
+// same order.
 #include <math.h>
 
 #include "common.hpp"
@@ -377,9 +378,9 @@ __global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerArgs a, uint16_
   }
 }
 
-// Launch 2: y[p] = D act[p], then out[t] = sum_j w y[t k + j] by the last
-// workgroup of each block of 32 NG columns.  W2 is read at 4.5 TB/s for one
-// token (27 us), 5.2 TB/s for 128 (725 us): a workgroup has 32 steps for its
+// Launch 2: y[p] = D act[p], then, if `join`, out[t] = sum_j w y[t k + j] by the
+// last workgroup of each block of 32 NG columns.  W2 is read at 4.5 TB/s for one
+// token (27 us), 5.2 TB/s for 128 (725 us, joined): a workgroup has 32 steps for its
 // four waves, and without the wait for its rows' arrival and the count the
 // launch takes 7 % less, without writing the rows another 12 %.  Several
 // column blocks a workgroup, which wait once, were slower (890 us for four):
@@ -388,7 +389,7 @@ template <int Q, int NG, typename IdxT>
 __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const uint16_t *__restrict__ act,
                                                               const Head *__restrict__ heads,
                                                               const uint16_t *__restrict__ lists, float *y,
-                                                              uint32_t *done, int blocks) {
+                                                              uint32_t *done, int blocks, int join) {
   __shared__ __attribute__((aligned(16))) float s_tile[kWaves * NG * 16 * kWave];
   constexpr int kRow = 32 * NG + 4;               // floats of a pair's row in LDS
   __shared__ __attribute__((aligned(16))) float s_row[kTile * kRow];
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int blk = blockIdx.x % blocks, rank = blockIdx.x / blocks, P = (int)a.T * a.k;
   const int expert = heads[rank].expert, n = heads[rank].n, used = heads[rank].used;
-  if (expert < 0 && !(rank == 0 && used == 0)) return;             // uniform
+  if (expert < 0 && !(join && rank == 0 && used == 0)) return;             // uniform
   const int K = a.inter, ksteps = K / 64, groups = a.hidden / 32;
   const int g0 = min(blk * NG, groups - NG);
   if (expert >= 0) {
@@ -429,9 +430,12 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
       for (int i = tid; i < rows * 16 * NG; i += kThreads) {
         const int row = i / (16 * NG), two = i - row * (16 * NG);
         const float *v = s_row + row * kRow + 2 * two;
-        put_shared((uint64_t *)(y + (size_t)s_pair[row] * a.hidden + 32 * g0) + two, v[0], v[1]);
+        uint64_t *to = (uint64_t *)(y + (size_t)s_pair[row] * a.hidden + 32 * g0) + two;
+        if (join) put_shared(to, v[0], v[1]);     // uniform
+        else *to = (uint64_t)__float_as_uint(v[1]) << 32 | __float_as_uint(v[0]);
       }
     }
+    if (!join) return;                            // uniform
     // y goes past the die's L2 (agent scope), and the wait below holds until
     // it has arrived: the count can then rise without a fence, which would
     // write back the whole L2 (at 128 tokens launch 2 took 12 times as long
@@ -475,6 +479,42 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
   }
 }
 
+// Calls of more tokens sum the pairs' rows in a launch of their own: the last
+// workgroups of launch 2 are one per block of columns, too few to read many
+// rows.  Measured (us a call, summed in launch 2 against by a third): one token
+// of 256 MXFP8 experts (7168 x 2048, top 8) 72.8, 74; 3 tokens of 32 (2048 x
+// 768, top 4) 23.6, 24.5; 8 tokens 34.0, 34.3; 13 tokens of 64 bf16 experts
+// (4096 x 1536, top 8) 349, 342; 128 of 64 (2048 x 768, top 8) 173, 132; 128 of
+// 256 MXFP8 1810, 1800.
+constexpr int64_t kJoinTokens = 8;
+
+// out[t] = sum_j w y[t k + j] in ascending j, four columns a thread.
+template <typename IdxT>
+__global__ __launch_bounds__(256) void layer_sum_kernel(LayerArgs a, const float *__restrict__ y) {
+  const int quads = a.hidden / 4, job = blockIdx.x * 256 + threadIdx.x, t = job / quads, c = 4 * (job - t * quads);
+  if (t >= a.T) return;
+  const IdxT *idx = (const IdxT *)a.idx + (int64_t)t * a.k;
+  const float *weights = a.weights + (int64_t)t * a.k;
+  f32x4 o = {};
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    f32x4 v[8];
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int p = min(j0 + j, a.k - 1);
+      const int64_t e = (int64_t)idx[p];
+      const bool on = j0 + j < a.k && e >= 0 && e < a.E;
+      w[j] = weights[p];
+      v[j] = f32x4{};
+      if (on) v[j] = *(const f32x4 *)(y + ((size_t)t * a.k + p) * a.hidden + c);
+      if (!on) w[j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o += w[j] * v[j];
+  }
+  *(u32x2 *)((uint16_t *)a.out + (size_t)t * a.hidden + c) = u32x2{pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w)};
+}
+
 template <int Q, int NG, typename IdxT>
 hipError_t layer_launch(const LayerArgs &a, hipStream_t s) {
   const LayerWs ws = layer_ws(a.T, a.k, a.E, a.hidden, a.inter);
@@ -485,12 +525,16 @@ hipError_t layer_launch(const LayerArgs &a, hipStream_t s) {
   uint16_t *lists = (uint16_t *)(a.ws + ws.lists);
   const int64_t P = a.T * a.k, used = P < a.E ? P : a.E;
   const int up_blocks = (a.inter / 16 + NG - 1) / NG, down_blocks = (a.hidden / 32 + NG - 1) / NG;
+  const int join = a.T <= kJoinTokens;
   hipLaunchKernelGGL((layer_up_kernel<Q, NG, IdxT>), dim3((unsigned)(used * up_blocks)), dim3(kThreads), 0, s, a, act,
                      heads, lists, done, up_blocks);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((layer_down_kernel<Q, NG, IdxT>), dim3((unsigned)(used * down_blocks)), dim3(kThreads), 0, s, a,
-                     act, heads, lists, y, done, down_blocks);
+                     act, heads, lists, y, done, down_blocks, join);
+  e = hipGetLastError();
+  if (e != hipSuccess || join) return e;
+  hipLaunchKernelGGL((layer_sum_kernel<IdxT>), dim3((unsigned)((a.T * (a.hidden / 4) + 255) / 256)), dim3(256), 0, s, a, y);
   return hipGetLastError();
 }
 template <int Q>

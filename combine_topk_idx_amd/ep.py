@@ -518,7 +518,7 @@ def ep_moe_layer_workspace_bytes(num_tokens: int, num_topk: int, num_experts: in
 def ep_moe_layer(x, topk_idx, topk_weights, num_experts: int, inter: int, w_quant, w1, w1_scales, w2, w2_scales,
                  workspace, out, *, stream=None) -> None:
     """The whole expert layer for a few tokens (num_tokens * num_topk <= 2048)
-    in two launches.  x, out: bf16 [T, H]; the weights as pack_moe_weights
+    in two or three launches.  x, out: bf16 [T, H]; the weights as pack_moe_weights
     returns them for ``w_quant`` ("none", "mxfp8" or "mxfp4")."""
     num_tokens, num_topk, idx_dtype = _idx_args(topk_idx, None, None, None)
     if not isinstance(x, torch.Tensor) or x.dim() != 2:

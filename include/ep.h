@@ -383,7 +383,7 @@ ep_status_t ep_moe_pack_weights_ex(const void *weights, const void *scales, int3
                                    int32_t k, ep_quant_t quant, int32_t gate_up, void *packed_weights,
                                    void *packed_scales, void *stream);
 
-/* The whole expert layer for a few tokens, in two launches: dispatch, both
+/* The whole expert layer for a few tokens, in two or three launches: dispatch, both
  * expert products, SwiGLU and combine without receive rows (a decoding
  * step's form of ep_layout_dispatch, ep_moe_gmm1, ep_moe_gmm2, ep_combine).
  *   x             device bf16 [T, H], 16-byte aligned; not quantised

@@ -103,6 +103,22 @@ def test_layer_masks(ep, quant):
     assert not l.run().float().any()
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(7, 192, 128, 6, 3), (8, 320, 64, 9, 11), (9, 320, 64, 9, 11), (10, 64, 128, 3, 2)])
+def test_layer_masks_around_the_third_launch(ep, T, H, I, E, k):
+    """Calls of up to 8 tokens sum their pairs in the second launch, larger ones in a third."""
+    l = Layer(ep, 70 + T, T, H, I, E, k, "mxfp8")
+    l.ids[0, 1:] = -1
+    l.ids[1] = -1
+    l.ids[2, 0] = E
+    l.x[1] = 0x7FC0
+    got = l.run()
+    assert not got[1].float().any()
+    l.x[1] = 0
+    l.check(got)
+    l.ids[:] = -1
+    assert not l.run().float().any()
+
+
 def test_layer_weight_codes(ep):
     """Every MXFP8 and MXFP4 code under every scale byte that keeps the product in bf16's normal range, one at a
     time through the down product: the output is the code's value exactly."""
