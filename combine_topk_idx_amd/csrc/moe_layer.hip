@@ -380,9 +380,9 @@ __global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerArgs a, uint16_
 
 // Launch 2: y[p] = D act[p], then, if `join`, out[t] = sum_j w y[t k + j] by the
 // last workgroup of each block of 32 NG columns.  W2 is read at 4.5 TB/s for one
-// token (27 us), 5.2 TB/s for 128 (725 us, joined): a workgroup has 32 steps for its
-// four waves, and without the wait for its rows' arrival and the count the
-// launch takes 7 % less, without writing the rows another 12 %.  Several
+// token (27 us), 5.6 TB/s for 128 (677 us; joined 725): a workgroup has 32 steps
+// for its four waves.  Joined, without the wait for its rows' arrival and the
+// count the launch takes 7 % less, without writing the rows another 12 %.  Several
 // column blocks a workgroup, which wait once, were slower (890 us for four):
 // the loads of many workgroups hide the wait better.
 template <int Q, int NG, typename IdxT>
