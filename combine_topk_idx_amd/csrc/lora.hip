@@ -636,6 +636,13 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(const int *__restrict__ 
   }
 }
 
+// Zeros for the gradients of a call without tokens.
+constexpr int kZeroBlocks = 2048;                 // eight workgroups a CU, each then walks on
+__global__ __launch_bounds__(256) void zero_kernel(f32x4 *__restrict__ a, int64_t na, f32x4 *__restrict__ b, int64_t nb) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < na + nb; i += (int64_t)gridDim.x * 256)
+    (i < na ? a + i : b + (i - na))[0] = f32x4{};
+}
+
 // Work items of a layout, at most: its rows in whole tiles and one partial
 // tile per adapter (and no more than one per row).
 int64_t items_upper(const ep_handle_t &h, int tile) {
@@ -749,12 +756,16 @@ hipError_t launch_lora_backward(const LoraGradArgs &p, hipStream_t s) {
   char *operand = p.ws + ws.operand, *part = p.ws + ws.part;
   float *u = (float *)(p.ws + ws.u), *outer = (float *)(p.ws + ws.outer);
   uint16_t *bt = (uint16_t *)(p.ws + ws.bt), *at = (uint16_t *)(p.ws + ws.at);
-  hipError_t e = hipSuccess;
-  if (p.h.num_tokens == 0) {                      // no row is read: the gradients are zeros
-    e = run_outer<false>(p.h, u, R, p.x, p.in, nullptr, p.grad_a, outer, s);
-    if (e == hipSuccess) e = run_outer<true>(p.h, p.down, R, p.grad_out, p.out_features, p.scale, p.grad_b, outer, s);
-    return e;
+  if (p.h.num_tokens == 0) {
+    // the layout is not asked: blocks of a fixed capacity hold rows of padding
+    // also without tokens, and there is no token whose row could stand for them
+    const int64_t quads_a = (int64_t)N * R * p.in / 4, quads_b = (int64_t)N * R * p.out_features / 4;
+    const int64_t blocks = (quads_a + quads_b + 255) / 256;
+    hipLaunchKernelGGL(zero_kernel, dim3((unsigned)(blocks < kZeroBlocks ? blocks : kZeroBlocks)), dim3(256), 0, s,
+                       (f32x4 *)p.grad_a, quads_a, (f32x4 *)p.grad_b, quads_b);
+    return hipGetLastError();
   }
+  hipError_t e = hipSuccess;
   const Transpose tb{(const uint16_t *)p.b, p.out_features, R, bt}, ta{(const uint16_t *)p.a, R, p.in, at};
   auto turns = [](int n) { return (int64_t)((n + kTurn - 1) / kTurn); };
   const int64_t tiles_b = N * turns(R) * turns(p.out_features), tiles_a = N * turns(R) * turns(p.in);

@@ -205,3 +205,16 @@ def test_lora_same_bits_every_time(ep):
         l.run(d, h)
         for n in names:
             assert torch.equal(d[n], ref[n]), n
+
+
+@pytest.mark.parametrize("layout", [dict(expert_capacity=70), dict(expert_capacity=600), dict(row_align=48),
+                                    dict(row_align=1024)])
+@pytest.mark.parametrize("r", [8, 128])
+def test_lora_no_tokens_in_padded_layouts(ep, layout, r):
+    """No tokens and blocks of padding all the same (also several pieces of them): the gradients are zeros, and no
+    row is read (x, grad_out and down are empty, their pointers NULL)."""
+    print(f"\n[case] lora without tokens {layout} rank {r}", flush=True)
+    l = Lora(ep, 69, 0, 96, 64, r, 4, tmax=9, **layout)
+    d = l.buffers()
+    l.run(d, l.handle())
+    assert not d["grad_a"].any() and not d["grad_b"].any()
