@@ -513,7 +513,9 @@ __global__ __launch_bounds__(kThreads) void row_router_kernel(RouterArgs a, void
     double rank = key_in(b0);
     if (a.top == 2) {
       if (biased) {
-        rank = is_key(b1) ? rank + key_in(b1) : kNoKey;
+        // beside +inf (held at 1e300) the second key changes nothing: groups
+        // with one and with two such keys rank alike
+        rank = !is_key(b1) ? kNoKey : rank > 1e299 ? rank : rank + key_in(b1);
       } else {
         // sums of two scores (a softmax's up to the row's factor)
         const float k0 = (float)key_in(b0), k1 = (float)key_in(b1);

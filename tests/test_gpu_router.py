@@ -206,3 +206,27 @@ def test_infinite_biases(ep, E, groups):
         ids, _ = _check(ep, z, 6, score="sigmoid", bias=bias, num_groups=groups, topk_groups=2, group_top=top)
         assert (ids[:, 0] == 0).sum() >= 11 and not np.isin(ids, [size, size + 1]).any()
         _check(ep, z, 6, score="softmax", bias=bias, num_groups=groups, topk_groups=groups - 1, group_top=top)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 4), (256, 8), (32, 16), (60, 5), (238, 2)])
+def test_several_infinite_biases_in_a_group(ep, E, groups):
+    """A group's sum is infinite with one +inf key and with two: among such groups the lower ones stay, whichever
+    path the group shape takes."""
+    size = E // groups
+    last = groups - 1
+    z = _logits(4, 20, E, torch.float32)
+    one_two, two_one = torch.zeros(E), torch.zeros(E)
+    one_two[[0, last * size, last * size + 1]] = float("inf")
+    two_one[[0, 1, last * size]] = float("inf")
+    for score in ("softmax", "sigmoid"):
+        for bias in (one_two, two_one):
+            for keep in (1, max(1, groups - 1)):
+                ids, _ = _check(ep, z, min(3, size), score=score, bias=bias, num_groups=groups, topk_groups=keep,
+                                group_top=2)
+                assert (ids[:, 0] == 0).all()
+    # every group infinite, in one place or two: the order of the groups decides
+    bias = torch.zeros(E)
+    bias[::size] = float("inf")
+    bias[1 + size * (groups // 2)::2 * size] = float("inf")
+    _check(ep, z, min(4, size), score="sigmoid", bias=bias, num_groups=groups, topk_groups=max(1, groups // 2),
+           group_top=2)
