@@ -22,7 +22,12 @@
 //          walks the adapter's rows, its waves sharing them out; the float32
 //          factor is cut into three bf16 parts (24 bits), so the products are
 //          those of the float32 values.
-// All sums are float32 and in a fixed order.
+// All sums are float32 and in a fixed order.  Infinities give what the
+// products above give: parts of zero and ranks that fill up a step meet none.
+#include <math.h>
+
+#include <type_traits>
+
 #include "common.hpp"
 #include "formats.hpp"
 #include "lora.hpp"
@@ -105,6 +110,18 @@ __device__ __forceinline__ Item find_item(const int *__restrict__ offsets, int N
 // [8 g, 8 g + 8) of row / column c; its sums are column c, rows 4 g + i.
 __device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// The largest bf16.  Factors are held to it before they are rounded to their
+// high part, so that a value near the largest float keeps a finite one and an
+// infinity leaves infinity as its rest (its own high part would leave inf - inf).
+constexpr float kLargest = 3.38953139e38f;
+__device__ __forceinline__ float high_of(float x) { return __builtin_amdgcn_fmed3f(x, -kLargest, kLargest); }
+
+// Two floats as bf16 parts: a word of the high ones and one of what they leave.
+__device__ __forceinline__ u32x2 split2(float x, float y) {
+  const uint32_t hi = pack_bf16x2(high_of(x), high_of(y));
+  return {hi, pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi))};
 }
 
 // Down product: v[r] = sum over i of w[e][r][i] rows[t][i], t the token of the
@@ -232,24 +249,56 @@ __global__ __launch_bounds__(W *kWave) void down_kernel(const int *__restrict__ 
         const f32x4 by = v * sc;
         if (r < R) *(f32x4 *)(sum + (size_t)t * R + r) = scaled ? by : v;
         uint16_t *to = operand + (size_t)(it.row0 + row) * 2 * r16 + f * 32 + 4 * g;
-        const u32x2 hi = {pack_bf16x2(by.x, by.y), pack_bf16x2(by.z, by.w)};
-        *(u32x2 *)to = hi;
-        *(u32x2 *)(to + 16) = u32x2{pack_bf16x2(by.x - bf16_lo(hi.x), by.y - bf16_hi(hi.x)),
-                                    pack_bf16x2(by.z - bf16_lo(hi.y), by.w - bf16_hi(hi.y))};
+        const u32x2 xy = split2(by.x, by.y), zw = split2(by.z, by.w);
+        *(u32x2 *)to = u32x2{xy.x, zw.x};
+        *(u32x2 *)(to + 16) = u32x2{xy.y, zw.y};
       }
     }
   }
 }
 
-// x as bf16 parts: each the rounding of what the ones before it leave
+// x as bf16 parts: each the rounding of what the ones before it leave.  SAFE:
+// beyond the largest bf16 too, an infinity in the last part (as in split2).
+template <bool SAFE>
 __device__ __forceinline__ void split3(const float (&v)[8], bf16x8 &hi, bf16x8 &mid, bf16x8 &lo) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    hi[i] = (__bf16)v[i];
+    hi[i] = (__bf16)(SAFE ? high_of(v[i]) : v[i]);
     const float rest = v[i] - (float)hi[i];
-    mid[i] = (__bf16)rest;
+    mid[i] = (__bf16)(SAFE ? high_of(rest) : rest);
     lo[i] = (__bf16)(rest - (float)mid[i]);
   }
+}
+
+// Infinities (and NaN) of bf16 operands become +-1: an infinity times a lower
+// part of zero would be NaN, and what it makes of the highest part is the whole
+// product (a lower part that is itself infinite has the highest one's sign).
+__device__ __forceinline__ bf16x8 finite_only(const bf16x8 &v) {
+  u32x4 d = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if ((d[j] & 0x7f80u) == 0x7f80u) d[j] = (d[j] & 0xffff8000u) | 0x3f80u;
+    if ((d[j] & 0x7f800000u) == 0x7f800000u) d[j] = (d[j] & 0x8000ffffu) | 0x3f800000u;
+  }
+  return __builtin_bit_cast(bf16x8, d);
+}
+
+// Whether the 16 bytes hold an infinity (or NaN); `top` carries it on.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void look(const u32x4 &d, u16x2 &top) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, d[j] & 0x7fff7fffu));
+}
+__device__ __forceinline__ bool not_finite(const u16x2 &top) { return max(top.x, top.y) >= 0x7f80; }
+
+// The up product's w in the lanes that hold the low parts, without infinities.
+template <int NT, int RS>
+__device__ __forceinline__ void drop_infinities(bf16x8 (&w)[NT][RS], bool low) {
+#pragma unroll
+  for (int o = 0; o < NT; ++o)
+#pragma unroll
+    for (int k = 0; k < RS; ++k)
+      if (low) w[o][k] = finite_only(w[o][k]);
 }
 
 // Up product: out[t] = base[t] + w[e] (s v[t]) of up to 16 STEPS rows over a
@@ -282,7 +331,7 @@ struct Down {
 
 template <int RS, int NT, int STEPS, bool PART>
 __device__ __forceinline__ void up_rows(int src, const Item &it, int from_row, int n, const Down &down, int R, bool leave,
-                                        const bf16x8 (&wv16)[NT][RS], const uint16_t *base, uint16_t *out, int C, int col,
+                                        bf16x8 (&wv16)[NT][RS], const uint16_t *base, uint16_t *out, int C, int col,
                                         bool on) {
   typedef typename Run<NT>::type Cols;
   const int lane = threadIdx.x & (kWave - 1), c = lane & 15, g = lane >> 4;
@@ -328,14 +377,28 @@ __device__ __forceinline__ void up_rows(int src, const Item &it, int from_row, i
           *(f32x4 *)(down.sum + (size_t)t * R + r) = p0 * by;
           *(f32x4 *)(down.sum + (size_t)t * R + r + 4) = p1 * by;
         }
+        u32x4 part;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = r < R ? (i < 4 ? p0[i & 3] : p1[i & 3]) * sc : 0.0f;
-          const __bf16 hi = (__bf16)x;
-          v[s][k][i] = g < 2 ? hi : (__bf16)(x - (float)hi);
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 &p = i < 2 ? p0 : p1;
+          const u32x2 two = split2(r < R ? p[2 * (i & 1)] * sc : 0.0f, r < R ? p[2 * (i & 1) + 1] * sc : 0.0f);
+          part[i] = g < 2 ? two.x : two.y;
         }
+        v[s][k] = __builtin_bit_cast(bf16x8, part);
       }
     }
+  if constexpr (RS == 1 && !PART) {
+    // w as it was loaded; here, where every load is on its way
+    if (R == 8) {                                 // uniform
+#pragma unroll
+      for (int o = 0; o < NT; ++o)
+        if (g & 1) wv16[o][0] = bf16x8{};
+    }
+    u16x2 top = {};
+#pragma unroll
+    for (int o = 0; o < NT; ++o) look(__builtin_bit_cast(u32x4, wv16[o][0]), top);
+    if (__builtin_expect(__any(not_finite(top)), 0)) drop_infinities(wv16, g >= 2);   // uniform
+  }
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     f32x4 acc[NT];
@@ -383,7 +446,8 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ of
   if (it.expert < 0) return;                      // uniform
   const int src = lane < it.n ? row_src[it.row0 + lane] : -1;
   const int col = first + NT * c;
-  bf16x8 wv16[NT][RS];                            // ranks past R meet zeros in the operand
+  bf16x8 wv16[NT][RS];                            // ranks past R: zeros, as in the operand
+  bool bad = false;                               // w holds an infinity
   if constexpr (RS == 1 && !PART) {
     // little of w and 64 rows to use it: read in the operand order, beside the base
     if (first >= C) return;                       // uniform
@@ -398,7 +462,9 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ of
     // 17 us, against 21 in the operand order (an access a lane); 8192 at rank
     // 16: 54 against 51, the base waiting behind it.
     constexpr int kUnits = kWaves * 16 * NT * 2 * RS, kLoads = kUnits / kThreads;
-    __shared__ __attribute__((aligned(16))) u32x4 s_w[kUnits];
+    // Unit kUnits holds zeros, for ranks past R.
+    __shared__ __attribute__((aligned(16))) u32x4 s_w[kUnits + 1];
+    __shared__ int s_bad[kWaves];                 // the wave saw an infinity
     const int per = R / 8, lane_units = NT * per; // units of a column, of a lane's columns
     auto place = [&](int u) { return lane_units % 8 == 0 ? u ^ (u / lane_units & 7) : u; };
     const u32x4 *from = (const u32x4 *)(w + ((size_t)it.expert * C + block0) * R);
@@ -406,22 +472,31 @@ __global__ __launch_bounds__(kThreads) void up_kernel(const int *__restrict__ of
     u32x4 in[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) in[i] = from[min(i * kThreads + tid, here - 1)];
+    u16x2 top = {};
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
+    for (int i = 0; i < kLoads; ++i) {
+      look(in[i], top);
       if (i * kThreads + tid < here) s_w[place(i * kThreads + tid)] = in[i];
+    }
+    const bool saw = __any(not_finite(top));
+    if (lane == 0) s_bad[wv] = saw;
+    if (tid == 0) s_w[kUnits] = u32x4{};
     __syncthreads();
     if (first >= C) return;                       // uniform
+    bad = __builtin_amdgcn_readfirstlane(s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3]);
 #pragma unroll
     for (int o = 0; o < NT; ++o)
 #pragma unroll
-      for (int k = 0; k < RS; ++k)
-        wv16[o][k] = __builtin_bit_cast(bf16x8, s_w[place((min(col + o, C - 1) - block0) * per +
-                                                          min(2 * k + (g & 1), per - 1))]);
+      for (int k = 0; k < RS; ++k) {
+        const int q = 2 * k + (g & 1), u = (min(col + o, C - 1) - block0) * per + q;
+        wv16[o][k] = __builtin_bit_cast(bf16x8, s_w[q < per ? place(u) : kUnits]);
+      }
   }
   // rows of padding come last in a block: none from the first on
   const int n = __popcll(__ballot(src >= 0));
   if (n == 0) return;                             // uniform
-  if (PART || n <= 16) {
+  if (PART || n <= 16 || __builtin_expect(bad, 0)) {
+    if (__builtin_expect(bad, 0)) drop_infinities(wv16, g >= 2);   // uniform
     for (int r = 0; r < n; r += 16)
       up_rows<RS, NT, 1, PART>(src, it, r, n, down, R, first == 0, wv16, base, out, C, col, col < C);
   } else {
@@ -480,9 +555,11 @@ __global__ __launch_bounds__(256) void transpose_kernel(const int *__restrict__ 
 // cores' token-major operands in registers.  Bound by q's bytes: 8192 tokens
 // of rank 16, 7168 columns, 25 us with q in the last-level cache, 36 us from
 // memory (3.2 TB/s).  An adapter of one piece is done; the pieces of the others go to `part` (a slot of R x C each), which
-// outer_sum_kernel adds up.
+// outer_sum_kernel adds up.  Registers for two waves a SIMD up to 64 ranks: the
+// second pass for infinities would take the second wave away (30 tokens of 38
+// adapters of rank 64, forward and gradients, 110 us against 90).
 template <int MF, int NT, bool T_OUT>
-__global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__ offsets,
+__global__ __launch_bounds__(kThreads, MF <= 4 ? 2 : 1) void outer_kernel(const int *__restrict__ offsets,
                                                          const int *__restrict__ row_src, int N, int chunk,
                                                          const float *__restrict__ p, int R,
                                                          const uint16_t *__restrict__ q, int C,
@@ -533,7 +610,8 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
     }
     keep_loads();
   };
-  auto multiply = [&](int k, int t0) {
+  auto multiply = [&](int k, int t0, auto safe) {
+    constexpr bool kSafe = decltype(safe)::value;
     bf16x8 b[NT];
     const int *src = s_src + t0 + g * 8;
 #pragma unroll
@@ -548,11 +626,15 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
       bf16x8 a0, a1, a2;
-      split3(pv[k][f], a0, a1, a2);
+      split3<kSafe>(pv[k][f], a0, a1, a2);
 #pragma unroll
-      for (int o = 0; o < NT; ++o) acc[f][o] = mfma(a0, b[o], mfma(a1, b[o], mfma(a2, b[o], acc[f][o])));
+      for (int o = 0; o < NT; ++o) {
+        const bf16x8 rest = kSafe ? finite_only(b[o]) : b[o];
+        acc[f][o] = mfma(a0, b[o], mfma(a1, rest, mfma(a2, rest, acc[f][o])));
+      }
     }
   };
+  constexpr std::false_type kFast{};
   constexpr int kStep = kWaves * 32;
   if (wv * 32 < padded) {                         // uniform
     const int last = padded - 32;
@@ -562,13 +644,33 @@ __global__ __launch_bounds__(kThreads) void outer_kernel(const int *__restrict__
     for (; t0 + (kRing - 1) * kStep < padded; t0 += kRing * kStep) {
 #pragma unroll
       for (int k = 0; k < kRing; ++k) {
-        multiply(k, t0 + k * kStep);
+        multiply(k, t0 + k * kStep, kFast);
         load(k, min(t0 + (k + kRing) * kStep, last));   // past the end: never used
       }
     }
 #pragma unroll
     for (int k = 0; k < kRing - 1; ++k)
-      if (t0 + k * kStep < padded) multiply(k, t0 + k * kStep);   // uniform
+      if (t0 + k * kStep < padded) multiply(k, t0 + k * kStep, kFast);   // uniform
+    // A sum is NaN where an infinity, or a factor past the largest bf16, met
+    // the factor's lower parts: only then the wave's steps once more, with
+    // infinities against the highest part alone.
+    bool nan = false;
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+#pragma unroll
+      for (int o = 0; o < NT; ++o)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nan |= acc[f][o][i] != acc[f][o][i];
+    if (__builtin_expect(__any(nan), 0)) {        // uniform
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+#pragma unroll
+        for (int o = 0; o < NT; ++o) acc[f][o] = f32x4{};
+      for (t0 = wv * 32; t0 < padded; t0 += kStep) {
+        load(0, t0);
+        multiply(0, t0, std::true_type{});
+      }
+    }
   }
   const float by = scale ? scale[it.expert] : 1.0f;
   float *to = it.pieces > 1 ? part + (size_t)it.slot * R * C : grad + (size_t)it.expert * R * C;

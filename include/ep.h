@@ -458,7 +458,9 @@ ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num
  * adapter e:
  *   down[t] = A[e] x[t]                        (float32 [rank])
  *   out[t]  = bf16( base[t] + scale[e] * (B[e] down[t]) )
- * and out[t] = base[t] for a token without one.
+ * and out[t] = base[t] for a token without one.  An infinity in x, A or B (or
+ * grad_out) gives infinities and NaN where these sums of products hold it, and
+ * nowhere else.
  *   handle       host; num_topk must be 1, num_experts is the number of
  *                adapters N; any of the row arrangements
  *   x            device bf16 [T, in], out_features and in_features positive

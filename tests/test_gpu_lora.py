@@ -218,3 +218,71 @@ def test_lora_no_tokens_in_padded_layouts(ep, layout, r):
     d = l.buffers()
     l.run(d, l.handle())
     assert not d["grad_a"].any() and not d["grad_b"].any()
+
+
+def _check_nonfinite(l, d, under=0.0):
+    """As Lora.check, but infinities and NaN have to stand where the definition (float64) has them; finite values
+    are within their bounds (``under``: what float32's smallest number adds to grad_x)."""
+    T, fin, fout, r, N = l.shape
+    x, a, b = _f64(l.x), _f64(l.a), _f64(l.b)
+    with np.errstate(all="ignore"):
+        out, bound, down, dv = OY.lora(x, l.ids, a, b, l.scale.astype(np.float64), _f64(l.base))
+        want = OY.lora_backward(x, l.ids, a, b, l.scale.astype(np.float64), _f64(l.dy), _f64(l.gb), down, dv)
+        want["out"] = (out, bound)
+        want["grad_x"] = (want["grad_x"][0], want["grad_x"][1] + under)
+        for n, (v, lim) in want.items():
+            got = d[n].double().cpu().numpy()
+            fin = np.isfinite(v)
+            assert np.array_equal(np.isnan(got), np.isnan(v)), f"{n}: NaN in the wrong places"
+            assert np.array_equal(got[np.isinf(v)], v[np.isinf(v)]), f"{n}: infinities"
+            assert np.all(np.abs(got - v)[fin] <= lim[fin]), n
+
+
+INF_BF16 = 0x7F80
+
+
+@pytest.mark.parametrize("where", ["a", "b", "x", "grad_out"])
+@pytest.mark.parametrize("T,fin,fout,r,N", [
+    (40, 64, 96, 8, 2), (33, 64, 160, 24, 2), (37, 96, 64, 40, 3), (90, 96, 64, 72, 2),
+    # the down product in several shares
+    (5, 2080, 1056, 40, 3), (4, 2080, 2080, 8, 2),
+    # an adapter's gradient in several pieces
+    (1100, 64, 32, 8, 2),
+])
+def test_lora_infinities(ep, where, T, fin, fout, r, N):
+    """One infinity in A, B, x or grad_out: out and the gradients are infinite or NaN where the products of the
+    definition are, and nowhere else (the last rank is the one that stands in for ranks that are filled up)."""
+    print(f"\n[case] lora infinity in {where} {(T, fin, fout, r, N)}", flush=True)
+    l = Lora(ep, 300 + r, T, fin, fout, r, N, none=0.0)
+    l.ids[0] = 0
+    l.a[l.a == 0], l.b[l.b == 0], l.x[l.x == 0], l.dy[l.dy == 0] = 0x3C00, 0x3C00, 0x3C00, 0x3C00   # inf * 0 by none
+    if where == "a":
+        l.a[0, r - 1, 3] = INF_BF16
+    elif where == "b":
+        l.b[0, fout - 5, r - 1] = INF_BF16 | 0x8000
+    elif where == "x":
+        l.x[0, fin - 2] = INF_BF16
+    else:
+        l.dy[0, 7] = INF_BF16
+    d = l.buffers()
+    l.run(d, l.handle())
+    _check_nonfinite(l, d)
+
+
+def test_lora_largest_floats(ep):
+    """down values between the largest bf16 and the largest float32 are cut into parts like any other."""
+    T, fin, fout, r, N = 40, 64, 96, 8, 2
+    l = Lora(ep, 310, T, fin, fout, r, N, none=0.0)
+    l.ids[:] = np.arange(T) % N
+    l.scale[:] = 1.0
+    l.a[:], l.b[:], l.x[:], l.dy[:], l.base[:], l.gb[:] = 0, 0, 0, 0, 0, 0
+    # the largest bf16, 2^128 - 2^120, and three quarters of its step (bf16 rounds 2^128 - 2^118 to infinity)
+    l.a[:, 2, 0], l.a[:, 2, 1], l.a[:, 2, 2] = 0x7F7F, 0x7B00, 0x7A80
+    l.x[:, :3] = 0x3F80
+    l.b[:, :, 2], l.b[:, 1::2, 2] = 0x0080, 0x8080           # +- 2^-126
+    l.dy[:, 5] = 0x0080
+    d = l.buffers()
+    l.run(d, l.handle())
+    assert float(d["down"].max()) > 3.397e38 and bool(torch.isfinite(d["down"]).all())
+    # u = b dy is one product 2^-126 2^-126 a token, 0 in float32: grad_x = a u lacks up to 3 2^128 2^-252 < 2^-122
+    _check_nonfinite(l, d, 2.0 ** -122)
