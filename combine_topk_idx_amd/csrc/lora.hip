@@ -184,8 +184,10 @@ __global__ __launch_bounds__(W *kWave) void down_kernel(const int *__restrict__ 
   };
   // the line's chunks [0, 4 M) are multiplied
   auto multiply = [&](int q, int M) {
+    wave_lds_fence();                             // the step before has been read
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) mine[(8 * i + (lane >> 3)) * 8 + (chunk ^ (lane >> 3))] = in[q][i];
+    wave_lds_fence();
     auto operand_at = [&](int row, int m) {
       return __builtin_bit_cast(bf16x8, mine[row * 8 + ((m * 4 + g) ^ (row & 7))]);
     };

@@ -30,6 +30,7 @@
 
 #include "common.hpp"
 #include "formats.hpp"
+#include "ring.hpp"
 #include "router.hpp"
 
 namespace ep {
@@ -262,13 +263,6 @@ __device__ __forceinline__ float sigmoidf(float z) { return 1.0f / (1.0f + expf(
 struct WaveLds {
   double key[kMaxExperts], rank[kMaxGroups];
 };
-
-// LDS written by some lanes of a wave is read by others: its accesses
-// complete in order, the compiler must not move them across.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
 
 template <typename T>
 __device__ __forceinline__ T wave_max(T v) {
