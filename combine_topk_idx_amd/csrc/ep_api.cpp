@@ -603,6 +603,9 @@ ep_status_t check_lora(const char *fn, const ep_handle_t *h, int32_t in, int32_t
     return fail(EP_ERR_UNSUPPORTED, "%s: in / out features above %d", fn, kMaxHidden);
   if (rank < 8 || rank > ep::kMaxRank || rank % 8 != 0)
     return fail(EP_ERR_INVALID_ARG, "%s: rank must be a multiple of 8 in [8, %d] (got %d)", fn, ep::kMaxRank, rank);
+  if (!ep::lora_fits(*h, in, out, rank, backward))
+    return fail(EP_ERR_UNSUPPORTED, "%s: %lld rows of %d and %d features are more than one launch holds; split the tokens, "
+                "or take blocks of a smaller capacity", fn, (long long)h->max_rows, in, out);
   if (!a || !aligned(a, 16) || !b || !aligned(b, 16))
     return fail(EP_ERR_INVALID_ARG, "%s: a / b NULL or not 16-byte aligned", fn);
   if (scale && !aligned(scale, 4)) return fail(EP_ERR_INVALID_ARG, "%s: scale is misaligned", fn);

@@ -788,15 +788,30 @@ hipError_t run_down(const ep_handle_t &h, const void *rows, int K, const void *w
   return hipGetLastError();
 }
 
+// The up product's tiles (see the switch below): columns and rows of a workgroup.
+int up_blocks(int C, int R) {
+  const int cols = kWaves * 16 * (operand_ranks(R) <= 32 ? 8 : 4);
+  return (C + cols - 1) / cols;
+}
+// Tokens a wave looks at for the rows without an adapter: 256 workgroups, then more tokens.
+int64_t tokens_looked_at(const ep_handle_t &h) {
+  const int64_t per = h.num_tokens / (256 * kWaves) + 1;
+  return per < kWave ? per : kWave;
+}
+int64_t up_rest(const ep_handle_t &h, bool copies) {
+  const int64_t tokens = kWaves * tokens_looked_at(h);
+  return copies ? (h.num_tokens + tokens - 1) / tokens : 0;
+}
+int64_t up_units(const ep_handle_t &h, int C, int R, bool copies) {
+  return items_upper(h, operand_ranks(R) <= 32 ? 64 : 32) * up_blocks(C, R) + up_rest(h, copies);
+}
+
 hipError_t run_up(const ep_handle_t &h, const Down &down, const void *w, int R, const void *base, void *out, int C,
                   hipStream_t s) {
-  const int rs = operand_ranks(R) / 16, nt = rs <= 2 ? 8 : 4;
-  const int blocks = (C + kWaves * 16 * nt - 1) / (kWaves * 16 * nt);
-  // tokens a wave looks at for the rows without an adapter: 256 workgroups, then more tokens
-  const int64_t per = h.num_tokens / (256 * kWaves) + 1, rest_tokens = per < kWave ? per : kWave;
-  const int64_t rest = out == base ? 0 : (h.num_tokens + kWaves * rest_tokens - 1) / (kWaves * rest_tokens);
-  const int64_t items = items_upper(h, rs <= 2 ? 64 : 32);
-  const dim3 grid((unsigned)(items * blocks + rest)), block(kThreads);
+  const int rs = operand_ranks(R) / 16;
+  const int64_t rest_tokens = tokens_looked_at(h), rest = up_rest(h, out != base);
+  const int blocks = up_blocks(C, R);
+  const dim3 grid((unsigned)up_units(h, C, R, out != base)), block(kThreads);
 #define EP_UP_PART(RS, NT, STEPS, PART)                                                                        \
   hipLaunchKernelGGL((up_kernel<RS, NT, STEPS, PART>), grid, block, 0, s, h.offsets, h.row_src, h.slot,        \
                      h.num_experts, down, h.num_tokens, (const uint16_t *)w, R, (const uint16_t *)base,        \
@@ -817,13 +832,20 @@ hipError_t run_up(const ep_handle_t &h, const Down &down, const void *w, int R, 
   return hipGetLastError();
 }
 
+// Column blocks of the outer products, and their workgroups at most.
+int outer_blocks(int C, int R) {
+  const int cols = 16 * (R <= 32 ? 8 : 4);
+  return (C + cols - 1) / cols;
+}
+int64_t outer_units(const ep_handle_t &h, int C, int R) {
+  return (h.max_rows / outer_chunk(R) + h.num_experts) * outer_blocks(C, R);
+}
+
 template <bool T_OUT>
 hipError_t run_outer(const ep_handle_t &h, const float *p, int R, const void *q, int C, const float *scale, float *grad,
                      float *part, hipStream_t s) {
-  const int chunk = outer_chunk(R), mf = (R + 15) / 16, nt = mf <= 2 ? 8 : 4;
-  const int blocks = (C + 16 * nt - 1) / (16 * nt);
-  const int64_t items = h.max_rows / chunk + h.num_experts;
-  const dim3 grid((unsigned)(items * blocks)), block(kThreads);
+  const int chunk = outer_chunk(R), mf = (R + 15) / 16, blocks = outer_blocks(C, R);
+  const dim3 grid((unsigned)outer_units(h, C, R)), block(kThreads);
   const size_t lds = (size_t)chunk * 4;
 #define EP_OUTER(MF, NT)                                                                                      \
   hipLaunchKernelGGL((outer_kernel<MF, NT, T_OUT>), grid, block, lds, s, h.offsets, h.row_src, h.num_experts, chunk, p, \
@@ -843,6 +865,14 @@ hipError_t run_outer(const ep_handle_t &h, const float *p, int R, const void *q,
 }
 
 }  // namespace
+
+bool lora_fits(const ep_handle_t &h, int32_t in, int32_t out, int32_t R, int backward) {
+  const int64_t chunk = outer_chunk(R), most = (int64_t)UINT32_MAX / kThreads;
+  const int64_t most_down = (int64_t)UINT32_MAX / (8 * kWave);   // its largest workgroup; shares: up to 512 workgroups only
+  if (h.max_rows > INT32_MAX - (chunk > 64 ? chunk : 64) || items_upper(h, kTile) > most_down) return false;
+  if (up_units(h, out, R, true) > most) return false;
+  return !backward || (up_units(h, in, R, true) <= most && outer_units(h, in, R) <= most && outer_units(h, out, R) <= most);
+}
 
 hipError_t launch_lora(const LoraArgs &p, hipStream_t s) {
   if (p.h.num_tokens == 0) return hipSuccess;

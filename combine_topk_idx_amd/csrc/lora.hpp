@@ -27,6 +27,11 @@ __host__ __device__ constexpr int operand_ranks(int R) {
   return 16 * (steps <= 4 ? steps : steps <= 6 ? 6 : 8);
 }
 
+// Whether the work of a call fits the launches of its kernels: grids of fewer
+// than 2^32 threads (a larger one is not refused by the runtime but cut to 32
+// bits) and row numbers that a tile added to them leaves within 32 bits.
+bool lora_fits(const ep_handle_t &h, int32_t in, int32_t out, int32_t R, int backward);
+
 struct LoraWs {                                   // byte offsets of the workspace sub-arrays
   size_t operand, part, u, bt, at, outer, total;
 };

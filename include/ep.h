@@ -462,7 +462,9 @@ ep_status_t ep_router_backward(const void *logits, ep_float_t dtype, int64_t num
  * grad_out) gives infinities and NaN where these sums of products hold it, and
  * nowhere else.
  *   handle       host; num_topk must be 1, num_experts is the number of
- *                adapters N; any of the row arrangements
+ *                adapters N; any of the row arrangements (more rows than a
+ *                launch of 2^32 threads holds: EP_ERR_UNSUPPORTED; 2^28 rows
+ *                of up to 512 features fit, 2^24 of up to 8192)
  *   x            device bf16 [T, in], out_features and in_features positive
  *                multiples of 32
  *   rank         a multiple of 8, 8 .. 128 (adapters of lower rank: zero rows)

@@ -184,3 +184,36 @@ def test_binding_rejects(ep):
         bad(match, ep.ep_lora, *ok[:i], t, *ok[i + 1:])
     bad("scale must have shape", ep.ep_lora, *ok, scale=torch.zeros(3))
     bad("base must be", ep.ep_lora, *ok, base=torch.zeros(4, 96))
+
+
+@pytest.mark.parametrize("N,cap,fin,fout,r", [
+    (512, 4194303, 65536, 65536, 128),                       # units past 2^32: the count used to be cut to 32 bits
+    (512, 4194303, 64, 65536, 8),
+    (1, (1 << 31) - 1, 64, 96, 16),                           # a block whose rows and a tile pass 2^31
+    (512, 4000000, 4096, 4096, 128),                          # units times threads past 2^32
+])
+def test_lora_refuses_layouts_past_a_launch(ep, N, cap, fin, fout, r):
+    """Capacity layouts whose work items do not fit one launch (or 32-bit rows) are refused before anything runs."""
+    h = ep.ep_handle_t()
+    h.num_tokens, h.num_max_tokens, h.max_rows = 4, 8, N * cap
+    h.num_topk, h.num_experts, h.row_align, h.expert_capacity = 1, N, 1, cap
+    h.offsets = h.slot = h.row_src = h.status = FAKE
+    far = [FAKE * (i + 1) for i in range(12)]                # apart by more than any buffer's bytes
+    rc = ep._lib.ep_lora(ctypes.byref(h), far[0], fin, fout, r, far[1], far[2], None, None, far[3], far[4], far[5],
+                         1 << 50, None)
+    assert rc == ep.EP_ERR_UNSUPPORTED, ep.ep_last_error()
+    assert ep.ep_last_error().startswith("ep_lora:")
+    rc = ep._lib.ep_lora_backward(ctypes.byref(h), far[6], far[0], fin, fout, r, far[1], far[2], None, far[4], None,
+                                  far[7], far[8], far[9], far[5], 1 << 50, None)
+    assert rc == ep.EP_ERR_UNSUPPORTED, ep.ep_last_error()
+    assert ep.ep_last_error().startswith("ep_lora_backward:")
+
+
+def test_lora_takes_layouts_within_a_launch(ep):
+    """Large blocks whose work items do fit get past that check (to the workspace's)."""
+    h = ep.ep_handle_t()
+    h.num_tokens, h.num_max_tokens, h.max_rows = 4, 8, 512 * 65536
+    h.num_topk, h.num_experts, h.row_align, h.expert_capacity = 1, 512, 1, 65536
+    h.offsets = h.slot = h.row_src = h.status = FAKE
+    rc = ep._lib.ep_lora(ctypes.byref(h), FAKE, 512, 512, 16, FAKE, FAKE, None, None, 2 * FAKE, FAKE, FAKE, 64, None)
+    assert rc == ep.EP_ERR_BUFFER_TOO_SMALL, ep.ep_last_error()
