@@ -700,25 +700,47 @@ hipError_t backward_dt(const RouterArgs &a, const void *idx, int idx64, const fl
   return backward_i<DT, 32>(a, idx, idx64, grad, dz, s);
 }
 
+// A launch holds fewer than 2^32 threads (the runtime cuts larger counts to 32
+// bits); the wave path takes 64 a token.  More tokens go in several.
+constexpr int64_t kLaunchTokens = 1 << 25;
+const char *element(const void *p, int64_t i, int bytes) { return (const char *)p + i * bytes; }
+int logit_bytes(int dtype) { return dtype == EP_FLOAT_F32 ? 4 : 2; }
+
 }  // namespace
 
-hipError_t launch_router(const RouterArgs &a, void *idx, int idx64, float *weights, hipStream_t s) {
-  if (a.T == 0) return hipSuccess;
-  switch (a.dtype) {
-    case EP_FLOAT_F32: return router_dt<EP_FLOAT_F32>(a, idx, idx64, weights, s);
-    case EP_FLOAT_BF16: return router_dt<EP_FLOAT_BF16>(a, idx, idx64, weights, s);
-    default: return router_dt<EP_FLOAT_F16>(a, idx, idx64, weights, s);
+hipError_t launch_router(const RouterArgs &all, void *idx, int idx64, float *weights, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  for (int64_t t = 0; t < all.T && e == hipSuccess; t += kLaunchTokens) {
+    RouterArgs a = all;
+    a.T = all.T - t < kLaunchTokens ? all.T - t : kLaunchTokens;
+    a.logits = element(all.logits, t * a.E, logit_bytes(a.dtype));
+    void *to = (void *)element(idx, t * a.k, idx64 ? 8 : 4);
+    switch (a.dtype) {
+      case EP_FLOAT_F32: e = router_dt<EP_FLOAT_F32>(a, to, idx64, weights + t * a.k, s); break;
+      case EP_FLOAT_BF16: e = router_dt<EP_FLOAT_BF16>(a, to, idx64, weights + t * a.k, s); break;
+      default: e = router_dt<EP_FLOAT_F16>(a, to, idx64, weights + t * a.k, s);
+    }
   }
+  return e;
 }
 
-hipError_t launch_router_backward(const RouterArgs &a, const void *idx, int idx64, const float *grad_weights,
+hipError_t launch_router_backward(const RouterArgs &all, const void *idx, int idx64, const float *grad_weights,
                                   void *grad_logits, hipStream_t s) {
-  if (a.T == 0) return hipSuccess;
-  switch (a.dtype) {
-    case EP_FLOAT_F32: return backward_dt<EP_FLOAT_F32>(a, idx, idx64, grad_weights, grad_logits, s);
-    case EP_FLOAT_BF16: return backward_dt<EP_FLOAT_BF16>(a, idx, idx64, grad_weights, grad_logits, s);
-    default: return backward_dt<EP_FLOAT_F16>(a, idx, idx64, grad_weights, grad_logits, s);
+  hipError_t e = hipSuccess;
+  for (int64_t t = 0; t < all.T && e == hipSuccess; t += kLaunchTokens) {
+    RouterArgs a = all;
+    a.T = all.T - t < kLaunchTokens ? all.T - t : kLaunchTokens;
+    a.logits = element(all.logits, t * a.E, logit_bytes(a.dtype));
+    const void *from = element(idx, t * a.k, idx64 ? 8 : 4);
+    void *to = (void *)element(grad_logits, t * a.E, logit_bytes(a.dtype));
+    const float *grad = grad_weights + t * a.k;
+    switch (a.dtype) {
+      case EP_FLOAT_F32: e = backward_dt<EP_FLOAT_F32>(a, from, idx64, grad, to, s); break;
+      case EP_FLOAT_BF16: e = backward_dt<EP_FLOAT_BF16>(a, from, idx64, grad, to, s); break;
+      default: e = backward_dt<EP_FLOAT_F16>(a, from, idx64, grad, to, s);
+    }
   }
+  return e;
 }
 
 }  // namespace ep

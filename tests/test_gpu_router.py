@@ -230,3 +230,26 @@ def test_several_infinite_biases_in_a_group(ep, E, groups):
     bias[1 + size * (groups // 2)::2 * size] = float("inf")
     _check(ep, z, min(4, size), score="sigmoid", bias=bias, num_groups=groups, topk_groups=max(1, groups // 2),
            group_top=2)
+
+
+@pytest.mark.parametrize("T,E,groups", [((1 << 28) + 37, 2, 1), ((1 << 26) + 21, 6, 3)])
+def test_more_tokens_than_a_launch_holds(ep, T, E, groups):
+    """One thread short of 2^32 is the most a launch takes: 16 threads a token on the row path, 64 on the wave path."""
+    print(f"\n[case] router of {T} tokens", flush=True)
+    z = torch.randint(-8, 9, (T, E), dtype=torch.int8, device=DEV).to(torch.bfloat16)
+    idx = torch.full((T, 1), 77, dtype=torch.int32, device=DEV)
+    w = torch.full((T, 1), float("nan"), device=DEV)
+    ep.ep_router(z, idx, w, renormalize=True, num_groups=groups, topk_groups=1, scale=2.0)
+    best = z[:, 0].clone()
+    want = torch.zeros(T, dtype=torch.int32, device=DEV)
+    for e in range(1, E):                                     # the first of the largest
+        more = z[:, e] > best
+        want[more] = e
+        best = torch.maximum(best, z[:, e])
+    assert torch.equal(idx[:, 0], want)
+    assert bool((w == 2.0).all())
+    if groups > 1:
+        return
+    dz = torch.full((T, E), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ep.ep_router_backward(z, idx, w, dz, renormalize=True, scale=2.0)
+    assert not dz.any()                                       # one choice, renormalised: its weight is constant
