@@ -529,8 +529,9 @@ ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, cons
     return fail(EP_ERR_INVALID_ARG, "%s: num_experts must be in (0, 512] (got %d)", fn, num_experts);
   if (num_tokens < 0) return fail(EP_ERR_INVALID_ARG, "%s: negative token count", fn);
   if (num_tokens > ep::kLayerMaxPairs / num_topk)
-    return fail(EP_ERR_UNSUPPORTED, "%s: more than %lld (token, j) pairs; use dispatch, the expert GEMMs and combine",
-                fn, (long long)ep::kLayerMaxPairs);
+    return fail(EP_ERR_UNSUPPORTED, "%s: more than %lld (token, j) pairs; split the tokens over several calls%s", fn,
+                (long long)ep::kLayerMaxPairs,
+                w_quant == EP_QUANT_MXFP8 ? ", or use dispatch, the expert GEMMs and combine" : "");
   if (hidden <= 0 || hidden % 64 != 0 || inter <= 0 || inter % 64 != 0)
     return fail(EP_ERR_INVALID_ARG, "%s: hidden and inter must be positive multiples of 64 (got %d, %d)", fn, hidden,
                 inter);

@@ -387,8 +387,9 @@ ep_status_t ep_moe_pack_weights_ex(const void *weights, const void *scales, int3
  * expert products, SwiGLU and combine without receive rows (a decoding
  * step's form of ep_layout_dispatch, ep_moe_gmm1, ep_moe_gmm2, ep_combine).
  *   x             device bf16 [T, H], 16-byte aligned; not quantised
- *   num_tokens    T >= 0, T * k <= 2048 (more pairs: EP_ERR_UNSUPPORTED, use
- *                 the calls above)
+ *   num_tokens    T >= 0, T * k <= 2048 (more pairs: EP_ERR_UNSUPPORTED; split
+ *                 the tokens over several calls, the rows are independent, or
+ *                 with MXFP8 weights use the calls above)
  *   hidden, inter H and I, positive multiples of 64
  *   topk_idx      device [T, k]; -1 and ids outside [0, E) take no part; an
  *                 id may repeat within a row

@@ -217,3 +217,13 @@ def test_lora_takes_layouts_within_a_launch(ep):
     h.offsets = h.slot = h.row_src = h.status = FAKE
     rc = ep._lib.ep_lora(ctypes.byref(h), FAKE, 512, 512, 16, FAKE, FAKE, None, None, 2 * FAKE, FAKE, FAKE, 64, None)
     assert rc == ep.EP_ERR_BUFFER_TOO_SMALL, ep.ep_last_error()
+
+
+@pytest.mark.parametrize("q,other", [(0, False), (3, True), (4, False)])
+def test_layer_refusal_names_a_way_out(ep, q, other):
+    """Past 2048 pairs: split the tokens; dispatch, GEMMs and combine only where they take such weights."""
+    rc = ep._lib.ep_moe_layer(FAKE, 1025, 256, FAKE, 1, FAKE, 2, 8, 128, q, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40,
+                              FAKE * 2, None)
+    assert rc == ep.EP_ERR_UNSUPPORTED
+    assert "split the tokens" in ep.ep_last_error()
+    assert ("dispatch" in ep.ep_last_error()) == other
