@@ -44,6 +44,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // at least half as long again.
 constexpr int kWaves = 4;
 constexpr int kGroups = 2;                        // 32-row weight groups of a workgroup
+static_assert(kGroups == 2, "hidden and inter are multiples of 64: two groups always divide theirs");
 constexpr int kRing = 2;                          // K steps in flight per wave
 constexpr int kThreads = kWaves * kWave;
 constexpr int kTile = 32;                         // tokens per pass over an expert's weights
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerArgs a, uint16_
     return;
   }
   const int K = a.hidden, ksteps = K / 64, groups = a.inter / 16;
-  const int g0 = min(blk * NG, groups - NG);      // a partial last block repeats groups of the one before
+  const int g0 = blk * NG;
   const size_t gidx = (size_t)expert * groups + g0;
   const int s0 = ksteps * wv / kWaves, s1 = ksteps * (wv + 1) / kWaves;
   int n = 0;
@@ -400,7 +401,7 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerArgs a, const
   const int expert = heads[rank].expert, n = heads[rank].n, used = heads[rank].used;
   if (expert < 0 && !(join && rank == 0 && used == 0)) return;             // uniform
   const int K = a.inter, ksteps = K / 64, groups = a.hidden / 32;
-  const int g0 = min(blk * NG, groups - NG);
+  const int g0 = blk * NG;
   if (expert >= 0) {
     const size_t gidx = (size_t)expert * groups + g0;
     const int s0 = ksteps * wv / kWaves, s1 = ksteps * (wv + 1) / kWaves;
@@ -524,7 +525,7 @@ hipError_t layer_launch(const LayerArgs &a, hipStream_t s) {
   Head *heads = (Head *)(a.ws + ws.heads);
   uint16_t *lists = (uint16_t *)(a.ws + ws.lists);
   const int64_t P = a.T * a.k, used = P < a.E ? P : a.E;
-  const int up_blocks = (a.inter / 16 + NG - 1) / NG, down_blocks = (a.hidden / 32 + NG - 1) / NG;
+  const int up_blocks = a.inter / 16 / NG, down_blocks = a.hidden / 32 / NG;
   const int join = a.T <= kJoinTokens;
   hipLaunchKernelGGL((layer_up_kernel<Q, NG, IdxT>), dim3((unsigned)(used * up_blocks)), dim3(kThreads), 0, s, a, act,
                      heads, lists, done, up_blocks);

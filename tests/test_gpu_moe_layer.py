@@ -195,3 +195,44 @@ def test_layer_no_tokens(ep):
     l.shape = (0, 64, 64, 2, 1)
     l.x, l.ids, l.w = l.x[:0], l.ids[:0], l.w[:0]
     assert l.run().shape == (0, 64)
+
+
+@pytest.mark.parametrize("quant,ncode,bytes_", [("mxfp8", 256, range(10, 247)), ("mxfp4", 16, range(2, 252))])
+def test_layer_every_scale_byte(ep, quant, ncode, bytes_):
+    """Every code under every scale byte whose products all stay in bf16's normal range (smallest e4m3 2^-9, e2m1
+    2^-1; largest 448 and 6), through the down product, where the other activations are zero: its value exactly."""
+    H, I = 256, 64
+    bytes_ = list(bytes_)
+    E = len(bytes_)
+    flat = np.arange(H) % ncode
+    if quant == "mxfp8":
+        flat[(flat & 0x7F) == 0x7F] = 0
+    codes = np.zeros((E, H, I), np.uint8)
+    codes[:, :, 37] = flat
+    sc = np.broadcast_to(np.array(bytes_, np.uint8)[:, None, None], (E, H, I // 32)).copy()
+    w2 = codes if quant == "mxfp8" else (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+    # activation 37 is silu(64) / 64 = 1 (to 2^-60 of it): gate 1.0 and up 1.0 under the scales 2^6 and 2^-6
+    one = 0x38 if quant == "mxfp8" else 0x02
+    w1 = np.zeros((E, 2 * I, H if quant == "mxfp8" else H // 2), np.uint8)
+    w1[:, 37, 0] = w1[:, I + 37, 0] = one
+    s1 = np.full((E, 2 * I, H // 32), 127, np.uint8)
+    s1[:, 37], s1[:, I + 37] = 127 + 6, 127 - 6
+    x = torch.zeros(E, H)
+    x[:, 0] = 1.0
+    p1 = ep.pack_moe_weights(to_dev(w1), to_dev(s1), True, quant=quant)
+    p2 = ep.pack_moe_weights(to_dev(w2), to_dev(sc), False, quant=quant)
+    out = torch.full((E, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(ep.ep_moe_layer_workspace_bytes(E, 1, E, H, I), dtype=torch.uint8, device=DEV)
+    ep.ep_moe_layer(x.bfloat16().to(DEV), torch.arange(E, device=DEV).view(E, 1), torch.ones(E, 1, device=DEV), E, I,
+                    quant, *p1, *p2, ws, out)
+    want = OY.weight_values(w2, sc, quant)[:, :, 37]
+    assert np.array_equal(out.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("quant", ["none", "mxfp8", "mxfp4"])
+def test_layer_wide(ep, quant):
+    """The widest reduction axes of the measured sizes on few experts, and the odd group counts 64-wide blocks allow."""
+    print(f"\n[case] layer wide {quant}", flush=True)
+    for i, case in enumerate([(3, 7168, 192, 3, 2), (9, 320, 2112, 4, 2), (34, 1024, 4160, 2, 1)]):
+        l = Layer(ep, 300 + i, *case, quant)
+        l.check(l.run())
