@@ -286,3 +286,14 @@ def test_lora_largest_floats(ep):
     assert float(d["down"].max()) > 3.397e38 and bool(torch.isfinite(d["down"]).all())
     # u = b dy is one product 2^-126 2^-126 a token, 0 in float32: grad_x = a u lacks up to 3 2^128 2^-252 < 2^-122
     _check_nonfinite(l, d, 2.0 ** -122)
+
+
+@pytest.mark.parametrize("T,fin,fout,r,N", [(9000, 64, 96, 128, 2), (5000, 96, 64, 72, 2), (7001, 32, 160, 104, 5),
+                                            (5200, 64, 64, 96, 3)])
+def test_lora_several_pieces_at_high_ranks(ep, T, fin, fout, r, N):
+    """Above 64 ranks an adapter's gradient is built from pieces of 32 r tokens: one adapter of several, others idle."""
+    print(f"\n[case] lora pieces {(T, fin, fout, r, N)}", flush=True)
+    l = Lora(ep, 330 + r, T, fin, fout, r, N, none=0.1, skew=True)
+    d = l.buffers()
+    l.run(d, l.handle())
+    l.check(d)

@@ -236,3 +236,26 @@ def test_layer_wide(ep, quant):
     for i, case in enumerate([(3, 7168, 192, 3, 2), (9, 320, 2112, 4, 2), (34, 1024, 4160, 2, 1)]):
         l = Layer(ep, 300 + i, *case, quant)
         l.check(l.run())
+
+
+@pytest.mark.parametrize("quant", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("part", ["up", "down"])
+def test_layer_nan_weights(ep, quant, part):
+    """An e4m3 NaN code and an e8m0 NaN scale (0xFF) make NaN of the rows they stand in and of no other."""
+    l = Layer(ep, 320, 3, 128, 128, 4, 2, quant)
+    l.ids[:] = [[0, 1], [1, 2], [2, 3]]
+    w, s = l.w2 if part == "down" else l.w1
+    s[0, 3, 1] = 0xFF                                         # expert 0, row 3 (a gate row in the up product)
+    if quant == "mxfp8":
+        w[2, 40, 70] = 0xFF                                   # expert 2, row 40
+    dev = lambda p: (to_dev(p[0]), to_dev(p[1]))              # noqa: E731
+    l.p1, l.p2 = (ep.pack_moe_weights(*dev(p), up, quant=quant) for p, up in ((l.w1, True), (l.w2, False)))
+    got = np.isnan(l.run().float().cpu().numpy())
+    want = np.zeros(got.shape, bool)
+    if part == "down":
+        want[0, 3] = True
+        want[1:, 40] = quant == "mxfp8"
+    else:                                                     # a NaN activation reaches every output of its tokens
+        want[0] = True
+        want[1:] = quant == "mxfp8"
+    assert np.array_equal(got, want)

@@ -253,3 +253,16 @@ def test_more_tokens_than_a_launch_holds(ep, T, E, groups):
     dz = torch.full((T, E), float("nan"), dtype=torch.bfloat16, device=DEV)
     ep.ep_router_backward(z, idx, w, dz, renormalize=True, scale=2.0)
     assert not dz.any()                                       # one choice, renormalised: its weight is constant
+
+
+@pytest.mark.parametrize("T,E,groups,keep,top,score,biased", [
+    (4099, 238, 2, 1, 2, "softmax", True), (4096, 60, 5, 2, 1, "sigmoid", False), (2051, 500, 4, 3, 2, "softmax", False),
+    (3001, 120, 24, 11, 2, "sigmoid", True), (1030, 511, 7, 5, 2, "sigmoid", True),
+])
+def test_prefill_off_whole_lanes(ep, T, E, groups, keep, top, score, biased):
+    """Group shapes that do not fall on whole lanes, at the sizes of a prompt, some experts masked out."""
+    z = _logits(T, T, E, torch.float32, 0.05)
+    kw = dict(score=score, num_groups=groups, topk_groups=keep, group_top=top)
+    if biased:
+        kw["bias"] = torch.from_numpy(np.random.default_rng(E).normal(size=E) * 0.1).float()
+    _check(ep, z, 8, torch.int32, **kw)
