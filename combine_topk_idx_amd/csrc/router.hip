@@ -163,9 +163,13 @@ __device__ __forceinline__ double key_in(double packed) {
 }
 static_assert((kMaxExperts & (kMaxExperts - 1)) == 0, "the expert is a bit field");
 
-// e^x for x <= 700 or so, to 2^-46 of it: 2^n times the Taylor series of e^r,
-// |r| <= ln 2 / 2, whose 12th term is below 2^-47; 0 below e^-745.  The
-// coefficients are held in scalar registers (as literals each costs two
+// e^x for x <= 700 or so: 2^n times the Taylor series of e^r, |r| <= ln 2 / 2,
+// whose 12th term is below 2^-46.6; 0 below e^-745.  Off by at most 2^-46 for
+// |x| <= 150, and, as n times the rounding of ln 2 grows, by 2^-44.8 for |x| <=
+// 700 (against 60-digit values).  A score below e^-134 is lost beside any bias
+// but 0, so keys hold their 43 bits by the first bound; sums of two scores
+// without a bias are told apart from a difference of 2^-43.8 on by the second.
+// The coefficients are held in scalar registers (as literals each costs two
 // moves a use, a quarter of the kernel's instructions).
 __device__ __forceinline__ double scalar(double c) {
   asm("" : "+s"(c));

@@ -64,6 +64,8 @@
 extern "C" {
 #endif
 
+/* Raised when a call that was there changes; added calls leave it as it is (a
+ * program that must run with older libraries asks for those by symbol). */
 #define EP_ABI_VERSION 4
 
 typedef enum {
