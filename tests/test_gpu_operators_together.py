@@ -108,3 +108,54 @@ def test_layer_against_the_separate_calls(ep):
     ep.ep_combine(h, yb, "none", H, s.idx, s.w, out)
     rel = (out.float() - s.out.float()).norm(dim=1) / s.out.float().norm(dim=1)
     assert float(rel.max()) < 0.125
+
+
+def test_small_calls_in_graphs(ep):
+    """The forms for a few tokens captured: the layer whose second launch sums the pairs, the adapters' down product
+    in several shares; two graphs over workspaces of their own, replayed in turn with eager work between."""
+    steps = [Step(ep, T=3, H=2048, I=128, E=24, k=4, r=8, N=3), Step(ep, T=8, H=1152, I=192, E=12, k=2, r=40, N=2)]
+    other = Step(ep, T=40, H=512, I=256, E=8, k=2)
+    refs, graphs = [], []
+    for s in steps:
+        s()
+        torch.cuda.synchronize()
+        refs.append([t.clone() for t in s.results()])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s()
+        graphs.append(g)
+    for rep in range(4):
+        for s in steps:
+            for t in s.results():
+                t.fill_(3)
+            for w in (s.ws, s.ows, s.lws):
+                w.fill_(0xA5 - rep)
+        for g in graphs:
+            g.replay()
+            other()
+        torch.cuda.synchronize()
+        for s, ref in zip(steps, refs):
+            for i, (t, r) in enumerate(zip(s.results(), ref)):
+                assert torch.equal(t, r), f"replay {rep}, {s.dims}, result {i}"
+
+
+def test_one_workspace_for_calls_of_every_size(ep):
+    """Layer calls of few and of more tokens, and of other shapes, one after the other over one workspace that
+    nobody clears: each call's rows are its own."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    H, I, E, k = 1024, 256, 16, 4
+    w1, s1 = W.make_mx_weights(5, E, 2 * I, H)
+    w2, s2 = W.make_mx_weights(6, E, H, I)
+    p = ep.pack_moe_weights(to_dev(w1), to_dev(s1), True) + ep.pack_moe_weights(to_dev(w2), to_dev(s2), False)
+    u8 = lambda T: torch.zeros(ep.ep_moe_layer_workspace_bytes(T, k, E, H, I), dtype=torch.uint8, device=DEV)   # noqa: E731
+    shared = u8(64)
+    for rep in range(3):
+        for T in (6, 40, 1, 64, 8, 9, 3):
+            x = torch.randn(T, H, generator=g, device=DEV).bfloat16()
+            idx = torch.randint(-1, E, (T, k), generator=g, device=DEV)
+            w = torch.rand(T, k, generator=g, device=DEV)
+            outs = [torch.full((T, H), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+            for ws, out in zip((shared, u8(T)), outs):
+                ep.ep_moe_layer(x, idx, w, E, I, "mxfp8", *p, ws, out)
+            assert torch.equal(*outs), (rep, T)
+            assert bool(outs[0].float().abs().sum() > 0)
