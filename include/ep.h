@@ -428,7 +428,8 @@ ep_status_t ep_moe_layer(const void *x, int64_t num_tokens, int32_t hidden, cons
  *   s when renormalize is set
  * Without a bias the keys are the logits themselves (both scores rise with
  * them).  Keys with a bias and sums of two scores are compared as float64, to
- * 43 significant bits.  An expert whose logit
+ * 43 significant bits; scores below e^-690 (a softmax's: below e^-700 of the
+ * row's largest) count as equal ones there.  An expert whose logit
  * or key is -inf or NaN is never chosen (+inf counts as the largest finite
  * logit); a row that has fewer than k experts left gets -1 with weight 0 in its last places.
  *   logits       device [T, E] of dtype, aligned to it
