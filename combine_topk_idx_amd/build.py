@@ -31,6 +31,7 @@ CONSUMER_SRC = os.path.join(ROOT, "tests", "c_abi", "ep_consumer.c")
 CONSUMER = os.path.join(ROOT, "tests", "c_abi", "ep_consumer")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 SOURCES = ["layout.hip", "dispatch.hip", "combine.hip", "moe.hip", "moe_layer.hip", "router.hip", "lora.hip",
+           "ffn.hip", "gmm_b128.hip",
            "static_ws.hip", "ep_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

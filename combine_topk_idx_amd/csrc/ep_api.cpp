@@ -14,6 +14,7 @@
 
 #include "common.hpp"
 #include "dispatch.hpp"
+#include "ffn.hpp"
 #include "lora.hpp"
 #include "moe.hpp"
 #include "moe_layer.hpp"
@@ -725,6 +726,153 @@ ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, co
   const ep::LoraGradArgs p{*handle, grad_out, x, in_features, out_features, rank, a, b, scale, down, grad_base, grad_x,
                            grad_a, grad_b, (char *)workspace};
   const hipError_t e = ep::launch_lora_backward(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+namespace {
+
+// what ep_ffn and ep_ffn_backward have in common
+ep_status_t check_ffn(const char *fn, const ep_handle_t *handle, const int64_t *recv_count, const void *x_buf,
+                      size_t x_buf_bytes, int32_t hidden, int32_t inter, int act, const void *w1, const void *w2,
+                      int ck_quant, const void *ck, size_t ck_bytes, const void *workspace, size_t workspace_bytes,
+                      int backward) {
+  const ep_status_t st = check_handle(handle, fn);
+  if (st != EP_OK) return st;
+  if (hidden <= 0 || hidden % 64 != 0 || inter <= 0 || inter % 64 != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: hidden and inter must be positive multiples of 64 (got %d, %d)", fn, hidden,
+                inter);
+  if (hidden > kMaxHidden || inter > kMaxHidden)
+    return fail(EP_ERR_UNSUPPORTED, "%s: hidden / inter above %d", fn, kMaxHidden);
+  if (act != EP_ACT_SILU && act != EP_ACT_GELU)
+    return fail(EP_ERR_INVALID_ARG, "%s: act must be EP_ACT_SILU or EP_ACT_GELU (got %d)", fn, act);
+  if (ck_quant != EP_QUANT_NONE && ck_quant != EP_QUANT_FP8_B128)
+    return fail(EP_ERR_INVALID_ARG, "%s: checkpoint_quant must be EP_QUANT_NONE or EP_QUANT_FP8_B128", fn);
+  if (ck_quant == EP_QUANT_FP8_B128 && inter % 128 != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: an 8-bit checkpoint needs inter %% 128 == 0 (got %d)", fn, inter);
+  if (!recv_count && (handle->row_align != 1 || handle->expert_capacity != 0))
+    return fail(EP_ERR_INVALID_ARG, "%s: padded expert blocks need recv_count", fn);
+  if (recv_count && !aligned(recv_count, 8)) return fail(EP_ERR_INVALID_ARG, "%s: recv_count misaligned", fn);
+  if (!w1 || !w2 || !aligned(w1, 16) || !aligned(w2, 16))
+    return fail(EP_ERR_INVALID_ARG, "%s: w1 / w2 NULL or not 16-byte aligned", fn);
+  if (!workspace || !aligned(workspace, 256))
+    return fail(EP_ERR_INVALID_ARG, "%s: workspace is NULL or not 256-byte aligned", fn);
+  const size_t need_ws = ep::ffn_ws(handle->max_rows, inter, backward).total;
+  if (workspace_bytes < need_ws)
+    return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: workspace needs %zu bytes (got %zu)", fn, need_ws, workspace_bytes);
+  if (ck) {
+    if (!aligned(ck, 16)) return fail(EP_ERR_INVALID_ARG, "%s: checkpoint not 16-byte aligned", fn);
+    const size_t need = buffer_bytes(handle->max_rows, 2 * inter, ck_quant, nullptr);
+    if (ck_bytes < need)
+      return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: checkpoint needs %zu bytes (got %zu)", fn, need, ck_bytes);
+  }
+  if (handle->max_rows == 0) return EP_OK;
+  if (!x_buf || !aligned(x_buf, 16)) return fail(EP_ERR_INVALID_ARG, "%s: x_buf NULL or not 16-byte aligned", fn);
+  const size_t rows = (size_t)handle->max_rows * hidden * 2;
+  if (x_buf_bytes < rows) return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: x_buf needs %zu bytes", fn, rows);
+  if (backward && !ck) return fail(EP_ERR_INVALID_ARG, "%s: checkpoint is NULL", fn);
+  return EP_OK;
+}
+
+}  // namespace
+
+size_t ep_ffn_workspace_bytes(int64_t max_rows, int32_t hidden, int32_t inter, int32_t num_experts,
+                              int32_t backward) {
+  if (max_rows < 0 || max_rows > INT32_MAX || hidden <= 0 || hidden % 64 != 0 || hidden > kMaxHidden || inter <= 0 ||
+      inter % 64 != 0 || inter > kMaxHidden || num_experts <= 0 || num_experts > ep::kMaxExperts)
+    return 0;
+  return ep::ffn_ws(max_rows, inter, backward != 0).total;
+}
+
+ep_status_t ep_ffn(const ep_handle_t *handle, const int64_t *recv_count, const void *x_buf, size_t x_buf_bytes,
+                   int32_t hidden, int32_t inter, ep_act_t act, const void *w1, const void *w2,
+                   ep_quant_t checkpoint_quant, void *checkpoint, size_t checkpoint_bytes, void *workspace,
+                   size_t workspace_bytes, void *out_buf, size_t out_buf_bytes, void *stream) {
+  const char *fn = "ep_ffn";
+  const ep_status_t st = check_ffn(fn, handle, recv_count, x_buf, x_buf_bytes, hidden, inter, act, w1, w2,
+                                   checkpoint_quant, checkpoint, checkpoint_bytes, workspace, workspace_bytes, 0);
+  if (st != EP_OK) return st;
+  if (handle->max_rows > 0) {
+    if (!out_buf || !aligned(out_buf, 16))
+      return fail(EP_ERR_INVALID_ARG, "%s: out_buf NULL or not 16-byte aligned", fn);
+    const size_t rows = (size_t)handle->max_rows * hidden * 2;
+    if (out_buf_bytes < rows) return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: out_buf needs %zu bytes", fn, rows);
+    if (overlap(x_buf, rows, out_buf, rows)) return fail(EP_ERR_INVALID_ARG, "%s: out_buf overlaps x_buf", fn);
+    const size_t ck = buffer_bytes(handle->max_rows, 2 * inter, checkpoint_quant, nullptr);
+    if (overlap(checkpoint, ck, x_buf, rows) || overlap(checkpoint, ck, out_buf, rows))
+      return fail(EP_ERR_INVALID_ARG, "%s: checkpoint overlaps x_buf or out_buf", fn);
+  }
+  const ep::FfnArgs p{*handle, recv_count, hidden, inter, (int32_t)act, x_buf, w1, w2, (int32_t)checkpoint_quant,
+                      checkpoint, (char *)workspace, out_buf};
+  const hipError_t e = ep::launch_ffn(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+ep_status_t ep_ffn_backward(const ep_handle_t *handle, const int64_t *recv_count, const void *grad_out,
+                            size_t grad_out_bytes, const void *x_buf, size_t x_buf_bytes, int32_t hidden,
+                            int32_t inter, ep_act_t act, const void *w1, const void *w2,
+                            ep_quant_t checkpoint_quant, const void *checkpoint, size_t checkpoint_bytes,
+                            void *workspace, size_t workspace_bytes, void *grad_x, size_t grad_x_bytes,
+                            void *grad_w1, void *grad_w2, void *stream) {
+  const char *fn = "ep_ffn_backward";
+  const ep_status_t st = check_ffn(fn, handle, recv_count, x_buf, x_buf_bytes, hidden, inter, act, w1, w2,
+                                   checkpoint_quant, checkpoint, checkpoint_bytes, workspace, workspace_bytes, 1);
+  if (st != EP_OK) return st;
+  if (handle->max_rows > 0) {
+    if (!grad_out || !aligned(grad_out, 16) || !grad_x || !aligned(grad_x, 16))
+      return fail(EP_ERR_INVALID_ARG, "%s: grad_out / grad_x NULL or not 16-byte aligned", fn);
+    const size_t rows = (size_t)handle->max_rows * hidden * 2;
+    if (grad_out_bytes < rows || grad_x_bytes < rows)
+      return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: grad_out / grad_x need %zu bytes", fn, rows);
+    if (overlap(x_buf, rows, grad_x, rows) || overlap(grad_out, rows, grad_x, rows))
+      return fail(EP_ERR_INVALID_ARG, "%s: grad_x overlaps x_buf or grad_out", fn);
+  }
+  if (!grad_w1 || !aligned(grad_w1, 16) || !grad_w2 || !aligned(grad_w2, 16))
+    return fail(EP_ERR_INVALID_ARG, "%s: grad_w1 / grad_w2 NULL or not 16-byte aligned", fn);
+  const ep::FfnGradArgs p{{*handle, recv_count, hidden, inter, (int32_t)act, x_buf, w1, w2, (int32_t)checkpoint_quant,
+                           (void *)checkpoint, (char *)workspace, nullptr},
+                          grad_out, grad_x, grad_w1, grad_w2};
+  const hipError_t e = ep::launch_ffn_backward(p, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return EP_OK;
+}
+
+ep_status_t ep_moe_gmm_b128(const ep_handle_t *handle, const int64_t *recv_count, const void *a_buf,
+                            size_t a_buf_bytes, ep_quant_t a_quant, int32_t k, int32_t n, const void *w,
+                            const float *w_scales, int32_t transposed, ep_act_t act, ep_quant_t out_quant,
+                            void *out_buf, size_t out_buf_bytes, void *stream) {
+  const char *fn = "ep_moe_gmm_b128";
+  const ep_status_t st = check_handle(handle, fn);
+  if (st != EP_OK) return st;
+  if (!ep::is_b128(a_quant)) return fail(EP_ERR_INVALID_ARG, "%s: a_quant must be a per-128 e4m3 mode", fn);
+  if (act != EP_ACT_NONE && act != EP_ACT_SILU && act != EP_ACT_GELU)
+    return fail(EP_ERR_INVALID_ARG, "%s: unknown act %d", fn, (int)act);
+  const bool gated = act != EP_ACT_NONE;
+  if (k <= 0 || k % 128 != 0 || n <= 0 || n % (gated ? 256 : 128) != 0)
+    return fail(EP_ERR_INVALID_ARG, "%s: need k %% 128 == 0 and n %% %d == 0 (got %d, %d)", fn, gated ? 256 : 128, k, n);
+  if (k > kMaxHidden || n > kMaxHidden) return fail(EP_ERR_UNSUPPORTED, "%s: k / n above %d", fn, kMaxHidden);
+  if (transposed != 0 && transposed != 1) return fail(EP_ERR_INVALID_ARG, "%s: transposed must be 0 or 1", fn);
+  if (transposed && gated) return fail(EP_ERR_INVALID_ARG, "%s: the transposed product takes no act", fn);
+  if (out_quant != EP_QUANT_NONE && !(gated && ep::is_b128(out_quant)))
+    return fail(EP_ERR_INVALID_ARG, "%s: out_quant must be EP_QUANT_NONE%s", fn, gated ? " or a per-128 mode" : "");
+  if (!recv_count && (handle->row_align != 1 || handle->expert_capacity != 0))
+    return fail(EP_ERR_INVALID_ARG, "%s: padded expert blocks need recv_count", fn);
+  if (recv_count && !aligned(recv_count, 8)) return fail(EP_ERR_INVALID_ARG, "%s: recv_count misaligned", fn);
+  if (!w || !w_scales || !aligned(w, 16) || !aligned(w_scales, 4))
+    return fail(EP_ERR_INVALID_ARG, "%s: w / w_scales NULL or misaligned", fn);
+  if (handle->max_rows > 0) {
+    if (!a_buf || !aligned(a_buf, 16) || !out_buf || !aligned(out_buf, 16))
+      return fail(EP_ERR_INVALID_ARG, "%s: a_buf / out_buf NULL or not 16-byte aligned", fn);
+    const size_t need_a = buffer_bytes(handle->max_rows, k, a_quant, nullptr);
+    const size_t need_o = buffer_bytes(handle->max_rows, gated ? n / 2 : n, out_quant, nullptr);
+    if (a_buf_bytes < need_a || out_buf_bytes < need_o)
+      return fail(EP_ERR_BUFFER_TOO_SMALL, "%s: a_buf needs %zu bytes, out_buf %zu", fn, need_a, need_o);
+    if (overlap(a_buf, need_a, out_buf, need_o)) return fail(EP_ERR_INVALID_ARG, "%s: out_buf overlaps a_buf", fn);
+  }
+  const ep::GmmB128Args p{*handle, recv_count, (const char *)a_buf, (int32_t)a_quant, k, n, w, w_scales, transposed,
+                          (int32_t)act, (int32_t)out_quant, (char *)out_buf};
+  const hipError_t e = ep::launch_gmm_b128(p, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, fn);
   return EP_OK;
 }

@@ -1,0 +1,433 @@
+// Grouped matrix-product core of the feed-forward block (ffn.hip) and the
+// block-scaled product (gmm_b128.hip) on gfx950.
+//
+// A workgroup computes one BN x BM tile of out[row][col] = sum_k R[row][k]
+// C[col][k]: "R" are the rows of an expert's block, "C" the operand whose
+// index runs along an output row.  C is the matrix instructions' first
+// operand, so a lane's accumulators are consecutive output columns of one
+// row (vector stores, one row scale a lane).
+//
+// Operand tiles cover 128 bytes of k (64 bf16 or 128 e4m3) and come in two
+// forms: k contiguous in memory ([index][k], LDS rows of 128 bytes), or k
+// strided ([k][index], LDS rows of one k), which gfx950's transposing LDS
+// reads turn into fragments.  Tiles go from memory to LDS without passing
+// through registers, 16 bytes a lane; a lane's LDS place is fixed by the
+// instruction, so the 16-byte chunks of a row are permuted by choosing which
+// chunk each lane fetches, such that the fragment reads of a wave spread over
+// all LDS banks.  Rows and columns past the end of an operand are out of the
+// range of the buffer descriptor and arrive as zeros.
+#pragma once
+
+#include "common.hpp"
+#include "formats.hpp"
+
+namespace ep {
+
+// Workgroups of a launch of at most that many units (moe.hip): no more than
+// CUs -- the stages fill a CU's LDS -- and a multiple of the XCD count.
+int64_t persistent_grid(int64_t units_upper);
+
+namespace gemm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr int kXcds = 8;
+constexpr int kKBytes = 128;              // bytes of k in a stage
+
+// ---------------------------------------------------------------------------
+// which tile a workgroup computes
+// ---------------------------------------------------------------------------
+
+struct Groups {                           // the experts' rows, in LDS
+  int first[kMaxExperts + 1];             // first row tile of each expert; [E] = all
+  int rows[kMaxExperts];
+  int order[kMaxExperts];                 // experts by descending row count (products over the rows)
+};
+
+// Rows of expert e: recv_count when given, never more than its block.
+__device__ __forceinline__ int expert_rows(const int *__restrict__ offsets, const int64_t *__restrict__ recv_count,
+                                           int e) {
+  const int block = offsets[e + 1] - offsets[e];
+  return recv_count ? (int)min((int64_t)block, max(recv_count[e], (int64_t)0)) : max(block, 0);
+}
+
+// Fills g.rows and the exclusive scan of the experts' tiles of `bm` rows.
+template <int THREADS>
+__device__ __forceinline__ void scan_rows(Groups &g, int E, const int *__restrict__ offsets,
+                                          const int64_t *__restrict__ recv_count, int bm) {
+  constexpr int kPer = (kMaxExperts + THREADS - 1) / THREADS, kWaves = THREADS / kWave;
+  __shared__ int wsum[kWaves];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wv = tid / kWave;
+  int tiles[kPer], sum = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int e = tid * kPer + q;
+    const int n = e < E ? expert_rows(offsets, recv_count, e) : 0;
+    tiles[q] = (n + bm - 1) / bm;
+    sum += tiles[q];
+    if (e < E) g.rows[e] = n;
+  }
+  int x = sum;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == kWave - 1) wsum[wv] = x;
+  __syncthreads();
+  int before = x - sum, all = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    before += i < wv ? wsum[i] : 0;
+    all += wsum[i];
+  }
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int e = tid * kPer + q;
+    if (e < E) g.first[e] = before;
+    before += tiles[q];
+  }
+  if (tid == 0) g.first[E] = all;
+  __syncthreads();
+}
+
+// Fills g.rows and g.order (a product over an expert's rows takes time in
+// their number: the longest first).
+template <int THREADS>
+__device__ __forceinline__ void order_rows(Groups &g, int E, const int *__restrict__ offsets,
+                                           const int64_t *__restrict__ recv_count) {
+  for (int e = threadIdx.x; e < E; e += THREADS) g.rows[e] = expert_rows(offsets, recv_count, e);
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    const int n = g.rows[e];
+    int at = 0;
+    for (int i = 0; i < E; ++i) at += g.rows[i] > n || (g.rows[i] == n && i < e);
+    g.order[at] = e;
+  }
+  __syncthreads();
+}
+
+// Workgroup b runs on XCD b % 8 (the hardware deals them out in turn); in
+// each round an XCD takes consecutive units, which share operands in its L2.
+__device__ __forceinline__ int64_t unit_of_round(int64_t round) {
+  const int slots = (int)gridDim.x / kXcds;
+  return (round * kXcds + blockIdx.x % kXcds) * slots + blockIdx.x / kXcds;
+}
+
+// Units of one group of nr x nc tiles, up to kGroupRows row tiles deep: the
+// units in flight on an XCD form a compact rectangle.
+constexpr int kGroupRows = 8;
+__device__ __forceinline__ void tile_of_unit(int64_t local, int nr, int nc, int &tr, int &tc) {
+  const int64_t per = (int64_t)kGroupRows * nc;
+  const int g = (int)(local / per);
+  const int rem = (int)(local - g * per);
+  const int depth = min(kGroupRows, nr - g * kGroupRows);
+  tc = rem / depth;
+  tr = g * kGroupRows + rem - tc * depth;
+}
+
+// The rows and column tile of a unit (expert-major, uniform).
+struct RowTile {
+  int e, rows, tc;
+  int64_t row0;
+};
+__device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *__restrict__ offsets, int64_t unit,
+                                            int nc, int bm) {
+  const int item = (int)(unit / nc);
+  int lo = 0, hi = E;                                        // the last expert whose first tile is <= item
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (g.first[mid] <= item) lo = mid; else hi = mid;
+  }
+  RowTile u;
+  u.e = __builtin_amdgcn_readfirstlane(lo);
+  const int rows = __builtin_amdgcn_readfirstlane(g.rows[u.e]);
+  int tr;
+  tile_of_unit(unit - (int64_t)g.first[u.e] * nc, (rows + bm - 1) / bm, nc, tr, u.tc);
+  tr = __builtin_amdgcn_readfirstlane(tr);
+  u.tc = __builtin_amdgcn_readfirstlane(u.tc);
+  u.row0 = (int64_t)offsets[u.e] + (int64_t)tr * bm;
+  u.rows = min(bm, rows - tr * bm);
+  return u;
+}
+
+// ---------------------------------------------------------------------------
+// staging
+// ---------------------------------------------------------------------------
+
+struct Source {                           // uniform over a wave
+  const char *base;                       // the tile's first element at k = 0
+  int64_t pitch;                          // bytes between rows of the matrix in memory
+  int valid;                              // indexes (rows of the tile) inside the operand
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes, 0x00020000);
+}
+
+// Loads the wave's share of a tile of ROWS indexes: pieces of 1 KB.
+//   SPLIT   the first half of the indexes comes from one source, the second
+//           half from another (gate and up rows): the caller gives each wave
+//           its own
+template <int ROWS, bool STRIDED, int EB, int WAVES, bool SPLIT>
+struct Loader {
+  static constexpr int kTile = ROWS * kKBytes;
+  static constexpr int kPieces = kTile / 1024;
+  // a tile of fewer pieces than waves: some waves fetch the same piece, so
+  // that every wave has the same number of loads in flight
+  static constexpr int kLoads = kPieces >= WAVES ? kPieces / WAVES : 1;
+  static constexpr int kPitch = ROWS * EB;                // LDS bytes of one k (strided)
+  static constexpr int kSteps = kKBytes / EB;             // k of a stage
+  int voff[kLoads];
+  int lds0;
+
+  // chunk permutation of one k's row (strided form)
+  static __device__ __forceinline__ int strided_key(int k) {
+    if constexpr (EB == 2) return kPitch >= 256 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
+    else return kPitch >= 256 ? (k & 7) << 1 : ((k >> 1) & 3) << 1;
+  }
+
+  __device__ __forceinline__ void init(int wave, int lane, const Source &s) {
+    const int p0 = kPieces >= WAVES ? wave * kLoads : wave % kPieces;
+    lds0 = p0 * 1024;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int at = (p0 + j) * 1024 + lane * 16;         // the lane's place in the tile
+      if constexpr (STRIDED) {
+        const int k = at / kPitch, chunk = (at % kPitch) / 16;
+        const int col = (chunk ^ strided_key(k)) * (16 / EB);
+        // past the operand's columns: past the descriptor's range
+        voff[j] = col < s.valid ? (int)(k * s.pitch) + col * EB : 0x7fffff00;
+      } else {
+        const int row = at / kKBytes, chunk = (at % kKBytes) / 16;
+        const int local = SPLIT ? row % (ROWS / 2) : row;
+        voff[j] = local * (int)s.pitch + (chunk ^ ((row >> 1) & 7)) * 16;
+      }
+    }
+  }
+
+  // stage t of k; `steps_left`: k from this stage on (strided form)
+  __device__ __forceinline__ void load(lds_u8 *tile, const Source &s, int t, int64_t k_left) const {
+    __amdgpu_buffer_rsrc_t r;
+    int soff = 0;
+    if constexpr (STRIDED) {
+      const int64_t rows = k_left < kSteps ? k_left : kSteps;
+      r = rsrc(s.base + (int64_t)t * kSteps * s.pitch, (uint32_t)(rows * s.pitch));
+    } else {
+      r = rsrc(s.base, (uint32_t)(s.valid * s.pitch));
+      soff = t * kKBytes;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(tile + lds0 + j * 1024), 16,
+                                               voff[j], soff, 0, 0);
+  }
+};
+
+// Fragment reads.  bf16 (32x32x16): lane l holds index l % 32, k = 8 (l / 32)
+// + 0..7 of step s.  e4m3 (32x32x64): lane l holds k = 16 (l / 32) + 0..15 and
+// the same + 32 of step s.
+template <int ROWS, bool STRIDED, int EB, int FRAGS>
+struct Reader {
+  static constexpr int kPitch = ROWS * EB;
+  static constexpr int kAddrs = STRIDED ? FRAGS : (EB == 2 ? 4 : 4);
+  int addr[kAddrs];
+
+  // row[f]: first tile index of fragment f is row0 + f * stride
+  __device__ __forceinline__ void init(int lane, int row0, int stride) {
+    const int half = lane >> 5;
+    if constexpr (STRIDED) {
+      const int j = lane & 15, g = lane >> 4;
+#pragma unroll
+      for (int f = 0; f < FRAGS; ++f) {
+        if constexpr (EB == 2) {
+          const int k = 8 * half + (j >> 2);
+          const int chunk = (row0 + f * stride) / 8 + 2 * (g & 1) + ((j & 3) >> 1);
+          addr[f] = k * kPitch + (chunk ^ Loader<ROWS, true, EB, 4, false>::strided_key(k)) * 16 + (j & 1) * 8;
+        } else {
+          const int k = 16 * half + (j >> 1);
+          const int chunk = (row0 + f * stride) / 16 + (g & 1);
+          addr[f] = k * kPitch + (chunk ^ Loader<ROWS, true, EB, 4, false>::strided_key(k)) * 16 + (j & 1) * 8;
+        }
+      }
+    } else {
+      const int r = row0 + (lane & 31);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) addr[s] = r * kKBytes + ((2 * s + half) ^ ((r >> 1) & 7)) * 16;
+    }
+  }
+
+  // bf16 fragment f of k step s (0..3)
+  template <int STRIDE>
+  __device__ __forceinline__ bf16x8 bf16(const lds_u8 *tile, int f, int s) const {
+    if constexpr (STRIDED) {
+      const lds_u8 *p = tile + addr[f] + s * 16 * kPitch;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
+      const s16x4 b =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p + 4 * kPitch));
+      const s16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(bf16x8, v);
+    } else {
+      return *(const __attribute__((address_space(3))) bf16x8 *)(tile + addr[s] + f * STRIDE * kKBytes);
+    }
+  }
+
+  // e4m3 fragment f of k step s (0..1)
+  template <int STRIDE>
+  __device__ __forceinline__ v8i fp8(const lds_u8 *tile, int f, int s) const {
+    if constexpr (STRIDED) {
+      const lds_u8 *p = tile + addr[f] + s * 64 * kPitch;
+      v2i q[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        q[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) v2i *)(p + (32 * (t >> 1) + 8 * (t & 1)) * kPitch));
+      return v8i{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
+    } else {
+      const u32x4 a = *(const __attribute__((address_space(3))) u32x4 *)(tile + addr[2 * s] + f * STRIDE * kKBytes);
+      const u32x4 b = *(const __attribute__((address_space(3))) u32x4 *)(tile + addr[2 * s + 1] + f * STRIDE * kKBytes);
+      return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    }
+  }
+};
+
+// Waits until at most N of the wave's loads are in flight; its LDS reads are
+// done; then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Tile shape: WN x WM waves of CF x RF fragments of 32 x 32, STAGES tiles of k
+// in LDS.
+template <int CF_, int RF_, int WN_, int WM_, int STAGES_>
+struct Shape {
+  static constexpr int CF = CF_, RF = RF_, WN = WN_, WM = WM_, kStages = STAGES_;
+  static constexpr int kWaves = WN * WM, kThreads = kWaves * kWave;
+  static constexpr int BN = 32 * CF * WN, BM = 32 * RF * WM;
+  static constexpr int kStage = (BN + BM) * kKBytes;
+  static constexpr int kLds = kStage * kStages;
+};
+
+// ---------------------------------------------------------------------------
+// epilogue helpers
+// ---------------------------------------------------------------------------
+
+// Accumulator 4b + i of lane l: column 8b + 4 (l / 32) + i of the fragment,
+// row l % 32.  Exchanging halves of lanes l and l + 32 gives each lane eight
+// consecutive columns: 16p + 8 (l / 32) + 0..7 for p = 0, 1.
+__device__ __forceinline__ void swap_halves(uint32_t &x, uint32_t &y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  x = r[0];
+  y = r[1];
+}
+
+// Stores a fragment of 16 values a lane as bf16: dst = the row's first
+// column of the fragment; columns at or past `cols` are left out (cols is a
+// multiple of 8).
+template <class F>
+__device__ __forceinline__ void store_bf16(char *dst, int half, int cols, F value) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    uint32_t x0 = pack_bf16x2(value(8 * p), value(8 * p + 1)), x1 = pack_bf16x2(value(8 * p + 2), value(8 * p + 3));
+    uint32_t y0 = pack_bf16x2(value(8 * p + 4), value(8 * p + 5)), y1 = pack_bf16x2(value(8 * p + 6), value(8 * p + 7));
+    swap_halves(x0, y0);
+    swap_halves(x1, y1);
+    const int n = 16 * p + 8 * half;
+    if (n < cols) *(u32x4 *)(dst + n * 2) = u32x4{x0, x1, y0, y1};
+  }
+}
+
+// Bits of the largest magnitude of a lane's 16 values and of its row's other
+// 16 (as integers: a value that is not a number counts as the largest).
+__device__ __forceinline__ uint32_t row_amax(const v16f &v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return max(m, (uint32_t)__shfl_xor((int)m, 32));
+}
+
+// Multiplier and scale of a block of 128 from the bits of its largest
+// magnitude: the rules of the per-128 receive formats.  A block that holds an
+// infinity or a NaN gets a scale that is not finite.
+struct Block128 {
+  float m, scale;
+  uint32_t byte;                          // the scale's e8m0 form
+  bool zero;
+};
+__device__ __forceinline__ Block128 block128(int quant, uint32_t amax_bits) {
+  const float amax = __uint_as_float(amax_bits);
+  const float s0 = amax / 448.0f;
+  Block128 b;
+  if (quant == EP_QUANT_FP8_B128) {
+    b.m = 448.0f / amax;
+    b.zero = amax_bits == 0 || __builtin_isinf(b.m);
+    b.scale = b.zero ? 0.0f : s0;
+    b.byte = 0;
+  } else {
+    const uint32_t bits = __float_as_uint(s0);
+    const bool finite = bits < 0x7f800000u;
+    const int e = bits && finite ? ceil_log2_bits(bits) : 0;
+    b.zero = bits == 0 || e < -127;
+    const int ec = b.zero ? 0 : e;
+    b.m = finite ? __uint_as_float((uint32_t)(127 - ec) << 23) : __uint_as_float(0x7fc00000u);
+    b.byte = b.zero ? 0u : finite ? (uint32_t)(ec + 127) : 0xffu;
+    b.scale = b.zero ? 0.0f : e8m0_decode(b.byte);
+  }
+  return b;
+}
+
+// e4m3 codes of a fragment: dst = the row's first column of the fragment.
+__device__ __forceinline__ void store_codes(char *dst, int half, bool ok, const v16f &v, const Block128 &b) {
+  uint32_t q[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[4 * c + i] * b.m;
+      z[i] = x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x;            // NaN stays
+    }
+    q[c] = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
+    q[c] = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], q[c], true);
+    if (b.zero) q[c] = 0;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    swap_halves(q[2 * p], q[2 * p + 1]);
+    if (ok) *(u32x2 *)(dst + 16 * p + 8 * half) = u32x2{q[2 * p], q[2 * p + 1]};
+  }
+}
+
+// The gate's activation.
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678f); }
+
+// `kind` is uniform: ep_act_t.
+__device__ __forceinline__ float act(int kind, float z) {
+  return z * (kind == EP_ACT_SILU ? sigmoid(z) : normal_cdf(z));
+}
+
+// the activation and its derivative
+__device__ __forceinline__ void act_grad(int kind, float z, float &f, float &df) {
+  if (kind == EP_ACT_SILU) {
+    const float p = sigmoid(z);
+    f = z * p;
+    df = p + f * (1.0f - p);
+  } else {
+    const float p = normal_cdf(z);
+    f = z * p;
+    df = p + z * 0.39894228f * expf(-0.5f * z * z);
+  }
+}
+
+}  // namespace gemm
+}  // namespace ep

@@ -8,7 +8,8 @@ The functions ``ep_workspace_bytes``, ``ep_workspace_bytes_ex``,
 ``ep_moe_gmm2``, ``ep_moe_packed_bytes_ex``, ``ep_moe_pack_weights_ex``,
 ``ep_moe_layer_workspace_bytes``, ``ep_moe_layer``, ``ep_router``,
 ``ep_router_backward``, ``ep_lora_workspace_bytes``, ``ep_lora``,
-``ep_lora_backward``, ``ep_read_status``,
+``ep_lora_backward``, ``ep_ffn_workspace_bytes``, ``ep_ffn``,
+``ep_ffn_backward``, ``ep_moe_gmm_b128``, ``ep_read_status``,
 ``ep_last_error`` and ``ep_abi_version`` have the names and arguments of the C ABI in
 ``include/ep.h``; torch tensors stand in for device pointers and torch's
 current stream is used unless one is passed.  Every computation runs in the
@@ -43,6 +44,7 @@ QUANT = {"none": 0, "int8_token": 1, "fp8_b128": 2, "mxfp8": 3, "mxfp4": 4, "fp8
          "fp8_b128_ue8m0": 6}
 EP_RECV_INTERLEAVED = 0x100
 SCORE = {"softmax": 0, "sigmoid": 1}
+ACT = {"none": -1, "silu": 0, "gelu": 1}
 _FLOAT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 EP_STATUS_ID_OUT_OF_RANGE = 1
 EP_STATUS_CAPACITY_OVERFLOW = 2
@@ -53,6 +55,7 @@ SYMBOLS = ("ep_workspace_bytes", "ep_workspace_bytes_ex", "ep_layout_rows", "ep_
            "ep_combine_backward", "ep_moe_packed_bytes", "ep_moe_pack_weights", "ep_moe_gmm1", "ep_moe_gmm2",
            "ep_moe_packed_bytes_ex", "ep_moe_pack_weights_ex", "ep_moe_layer_workspace_bytes", "ep_moe_layer",
            "ep_router", "ep_router_backward", "ep_lora_workspace_bytes", "ep_lora", "ep_lora_backward",
+           "ep_ffn_workspace_bytes", "ep_ffn", "ep_ffn_backward", "ep_moe_gmm_b128",
            "ep_read_status", "ep_last_error", "ep_abi_version")
 STATIC_WORKSPACE_BYTES = 4 << 20   # the static workspace of ep_layout_dispatch_noalloc
 
@@ -133,6 +136,15 @@ _lib.ep_lora.restype = _int
 _lib.ep_lora_backward.argtypes = [_hp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                   _vp]
 _lib.ep_lora_backward.restype = _int
+_lib.ep_ffn_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
+_lib.ep_ffn_workspace_bytes.restype = _sz
+_lib.ep_ffn.argtypes = [_hp, _vp, _vp, _sz, _i32, _i32, _int, _vp, _vp, _int, _vp, _sz, _vp, _sz, _vp, _sz, _vp]
+_lib.ep_ffn.restype = _int
+_lib.ep_ffn_backward.argtypes = [_hp, _vp, _vp, _sz, _vp, _sz, _i32, _i32, _int, _vp, _vp, _int, _vp, _sz, _vp, _sz,
+                                 _vp, _sz, _vp, _vp, _vp]
+_lib.ep_ffn_backward.restype = _int
+_lib.ep_moe_gmm_b128.argtypes = [_hp, _vp, _vp, _sz, _int, _i32, _i32, _vp, _vp, _i32, _int, _int, _vp, _sz, _vp]
+_lib.ep_moe_gmm_b128.restype = _int
 _lib.ep_read_status.argtypes = [ctypes.POINTER(ep_handle_t), ctypes.POINTER(ctypes.c_uint32), _vp]
 _lib.ep_read_status.restype = ctypes.c_int
 _lib.ep_last_error.argtypes = []
@@ -637,6 +649,91 @@ def ep_lora_backward(handle: ep_handle_t, grad_out, x, a, b, down, grad_x, grad_
     _check(_lib.ep_lora_backward(ctypes.byref(handle), _ptr(grad_out), _ptr(x), fin, fout, rank, _ptr(a), _ptr(b),
                                  _ptr(scale), _ptr(down), _ptr(grad_base), _ptr(grad_x), _ptr(grad_a), _ptr(grad_b),
                                  _ptr(workspace), _nbytes(workspace), stream))
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACT:
+            raise EpError(EP_ERR_INVALID_ARG, f"unknown act {act!r}")
+        return ACT[act]
+    return int(act)
+
+
+def ep_ffn_workspace_bytes(max_rows: int, hidden: int, inter: int, num_experts: int, backward: bool = False) -> int:
+    return _lib.ep_ffn_workspace_bytes(max_rows, hidden, inter, num_experts, int(bool(backward)))
+
+
+def _ffn_shapes(handle, w1, w2):
+    if not (isinstance(w1, torch.Tensor) and isinstance(w2, torch.Tensor) and w1.dim() == 3 and w2.dim() == 3):
+        raise EpError(EP_ERR_INVALID_ARG, "w1 and w2 must be [num_experts, 2 inter, hidden] and "
+                                          "[num_experts, hidden, inter] tensors")
+    E, hidden, inter = w2.shape
+    if E != handle.num_experts:
+        raise EpError(EP_ERR_INVALID_ARG, f"w2 holds {E} experts, the layout {handle.num_experts}")
+    return E, hidden, inter
+
+
+def ep_ffn(handle: ep_handle_t, x, w1, w2, workspace, out, *, act="silu", recv_count=None, checkpoint=None,
+           checkpoint_quant="none", stream=None) -> None:
+    """out[r] = W2[e] (act(g) * u), [g; u] = W1[e] x[r], for the rows of each
+    expert's block.  x, out: bf16 [max_rows, hidden] (receive buffers of
+    quant "none"); w1 [E, 2 inter, hidden], w2 [E, hidden, inter] bf16.
+    checkpoint: a receive-format buffer (uint8) of width 2 inter and quant
+    "none" or "fp8_b128", filled for ep_ffn_backward."""
+    E, hidden, inter = _ffn_shapes(handle, w1, w2)
+    bf, rows = torch.bfloat16, handle.max_rows
+    stream = _check_here(
+        stream, (x, "x", bf, None, rows * hidden), (w1, "w1", bf, (E, 2 * inter, hidden), None), (w2, "w2", bf, None, None),
+        (workspace, "workspace", None, None, None), (out, "out", bf, None, rows * hidden),
+        (checkpoint, "checkpoint", None, None, None), (recv_count, "recv_count", torch.int64, None, E))
+    _check(_lib.ep_ffn(ctypes.byref(handle), _ptr(recv_count), _ptr(x), _nbytes(x), hidden, inter, _act(act), _ptr(w1),
+                       _ptr(w2), _quant(checkpoint_quant), _ptr(checkpoint),
+                       0 if checkpoint is None else _nbytes(checkpoint), _ptr(workspace), _nbytes(workspace),
+                       _ptr(out), _nbytes(out), stream))
+
+
+def ep_ffn_backward(handle: ep_handle_t, grad_out, x, w1, w2, checkpoint, workspace, grad_x, grad_w1, grad_w2, *,
+                    act="silu", checkpoint_quant="none", recv_count=None, stream=None) -> None:
+    """Gradients of ep_ffn from grad_out, the gradient of its output rows
+    (ep_combine_backward, quant "none"): grad_x (rows), grad_w1 and grad_w2
+    (the weights' shapes), all bf16."""
+    E, hidden, inter = _ffn_shapes(handle, w1, w2)
+    bf, rows = torch.bfloat16, handle.max_rows
+    stream = _check_here(
+        stream, (grad_out, "grad_out", bf, None, rows * hidden), (x, "x", bf, None, rows * hidden),
+        (w1, "w1", bf, (E, 2 * inter, hidden), None), (w2, "w2", bf, None, None),
+        (checkpoint, "checkpoint", None, None, None), (workspace, "workspace", None, None, None),
+        (grad_x, "grad_x", bf, None, rows * hidden), (grad_w1, "grad_w1", bf, (E, 2 * inter, hidden), None),
+        (grad_w2, "grad_w2", bf, (E, hidden, inter), None), (recv_count, "recv_count", torch.int64, None, E))
+    _check(_lib.ep_ffn_backward(ctypes.byref(handle), _ptr(recv_count), _ptr(grad_out), _nbytes(grad_out), _ptr(x),
+                                _nbytes(x), hidden, inter, _act(act), _ptr(w1), _ptr(w2), _quant(checkpoint_quant),
+                                _ptr(checkpoint), 0 if checkpoint is None else _nbytes(checkpoint), _ptr(workspace),
+                                _nbytes(workspace), _ptr(grad_x), _nbytes(grad_x), _ptr(grad_w1), _ptr(grad_w2),
+                                stream))
+
+
+def ep_moe_gmm_b128(handle: ep_handle_t, a_buf, a_quant, k: int, n: int, w, w_scales, out, *, act="none",
+                    transposed: bool = False, out_quant="none", recv_count=None, stream=None) -> None:
+    """Products of per-128 e4m3 receive rows (a_buf, width k) with e4m3 weights
+    that have a float32 scale per 128 x 128 block.  w: uint8 or float8_e4m3fn
+    [E, n, k] (transposed: [E, k, n]), w_scales the same by 128.  act "none":
+    out bf16 [max_rows, n]; "silu" / "gelu": rows [0, n/2) of w are the gate's
+    and [n/2, n) the up's, out is a receive buffer of width n/2 in out_quant
+    ("none" or a per-128 mode)."""
+    E = handle.num_experts
+    if isinstance(w, torch.Tensor) and w.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise EpError(EP_ERR_INVALID_ARG, f"w must be uint8 or float8_e4m3fn (got {w.dtype})")
+    shape = (k, n) if transposed else (n, k)
+    width = n // 2 if _act(act) != ACT["none"] else n
+    stream = _check_here(
+        stream, (a_buf, "a_buf", None, None, None), (w, "w", None, (E, *shape), None),
+        (w_scales, "w_scales", torch.float32, (E, shape[0] // 128, shape[1] // 128), None),
+        (out, "out", torch.bfloat16 if _quant(out_quant) == 0 else None, None,
+         handle.max_rows * width if _quant(out_quant) == 0 else None),
+        (recv_count, "recv_count", torch.int64, None, E))
+    _check(_lib.ep_moe_gmm_b128(ctypes.byref(handle), _ptr(recv_count), _ptr(a_buf), _nbytes(a_buf), _quant(a_quant), k,
+                                n, _ptr(w), _ptr(w_scales), int(bool(transposed)), _act(act), _quant(out_quant),
+                                _ptr(out), _nbytes(out), stream))
 
 
 def ep_read_status(handle: ep_handle_t, stream=None) -> int:

@@ -507,6 +507,83 @@ ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, co
                              const float *down, const void *grad_base, void *grad_x, float *grad_a, float *grad_b,
                              void *workspace, size_t workspace_bytes, void *stream);
 
+/* Gated feed-forward block over expert rows in bf16, with its backward pass
+ * (a training step's form of the expert MLP; also inference above the
+ * few-token layer's limit).  For each row r of expert e's block:
+ *   g = W1[e][0..I-1] x_r,  u = W1[e][I..2I-1] x_r,  a = act(g) * u
+ *   out_r = bf16( W2[e] bf16(a) )
+ * with float32 sums; act(z) = z / (1 + exp(-z)) or z Phi(z) (the normal
+ * distribution's).  The call fills the checkpoint that ep_ffn_backward takes:
+ * a receive-format buffer (region form, rows = max_rows) of width 2I holding
+ * row r's g, then its u, as bf16 (EP_QUANT_NONE) or as e4m3 codes with a
+ * float32 scale per 128 (EP_QUANT_FP8_B128, quantised from the float32 sums by
+ * dispatch's rule).  With x dispatched anew in the backward pass, 8-bit
+ * checkpoints keep 2I + I/16 bytes a row.
+ *   handle          host; any of the row arrangements
+ *   recv_count      device int64 [E] as the layout wrote it; the rows of block e
+ *                   are its first recv_count[e].  NULL: the whole block, for
+ *                   compact layouts only
+ *   x_buf           device bf16 [max_rows, H] (ep_dispatch, EP_QUANT_NONE)
+ *   hidden, inter   H and I, positive multiples of 64, up to 65536; I a
+ *                   multiple of 128 with an 8-bit checkpoint
+ *   w1, w2          device bf16 [E, 2I, H] and [E, H, I], 16-byte aligned
+ *   checkpoint      device, 16-byte aligned, >= ep_buffer_bytes(max_rows, 2I,
+ *                   checkpoint_quant); NULL: none is kept
+ *   workspace       device, 256-byte aligned, >= ep_ffn_workspace_bytes(
+ *                   max_rows, ...); in use as for ep_moe_layer
+ *   out_buf         device bf16 [max_rows, H]; may not overlap x_buf.  Rows
+ *                   that hold no pair are left as they were (x's are not read) */
+typedef enum { EP_ACT_NONE = -1, EP_ACT_SILU = 0, EP_ACT_GELU = 1 } ep_act_t;
+size_t ep_ffn_workspace_bytes(int64_t max_rows, int32_t hidden, int32_t inter, int32_t num_experts,
+                              int32_t backward);
+ep_status_t ep_ffn(const ep_handle_t *handle, const int64_t *recv_count, const void *x_buf, size_t x_buf_bytes,
+                   int32_t hidden, int32_t inter, ep_act_t act, const void *w1, const void *w2,
+                   ep_quant_t checkpoint_quant, void *checkpoint, size_t checkpoint_bytes, void *workspace,
+                   size_t workspace_bytes, void *out_buf, size_t out_buf_bytes, void *stream);
+
+/* Gradients of ep_ffn from the gradient of its output rows
+ * (ep_combine_backward, EP_QUANT_NONE).  With g, u as the checkpoint holds them:
+ *   da = W2[e]^T grad_r,  dg = da u act'(g),  du = da act(g),  a = act(g) u
+ *   grad_x_r  = bf16( W1[e]^T [dg; du] )
+ *   grad_w1[e] = bf16( sum over its rows of [dg; du] x_r^T )
+ *   grad_w2[e] = bf16( sum over its rows of grad_r a^T )
+ * with float32 sums over dg, du and a rounded to bf16.
+ *   grad_out, grad_x  device bf16 [max_rows, H]; grad_x may not overlap
+ *                     grad_out or x_buf
+ *   grad_w1, grad_w2  device bf16, the weights' shapes, written in whole
+ *                     (zeros for an expert without rows)
+ *   workspace         >= ep_ffn_workspace_bytes(..., backward = 1) */
+ep_status_t ep_ffn_backward(const ep_handle_t *handle, const int64_t *recv_count, const void *grad_out,
+                            size_t grad_out_bytes, const void *x_buf, size_t x_buf_bytes, int32_t hidden,
+                            int32_t inter, ep_act_t act, const void *w1, const void *w2,
+                            ep_quant_t checkpoint_quant, const void *checkpoint, size_t checkpoint_bytes,
+                            void *workspace, size_t workspace_bytes, void *grad_x, size_t grad_x_bytes,
+                            void *grad_w1, void *grad_w2, void *stream);
+
+/* Grouped product of per-128 e4m3 rows (ep_dispatch or ep_combine_backward in
+ * one of the three per-128 modes) and e4m3 weights with a float32 scale for
+ * each block of 128 x 128.  For row r of expert e's block:
+ *   transposed = 0: y_r[n] = sum over k of W[e][n][k] a_r[k], weights [E, N, K],
+ *                   scales [E, N/128, K/128]
+ *   transposed = 1: y_r[n] = sum over k of W[e][k][n] a_r[k], weights [E, K, N],
+ *                   scales [E, K/128, N/128]: the gradient of the rows through
+ *                   the same weights and scales (act must be EP_ACT_NONE)
+ *   act EP_ACT_NONE: out_buf is bf16 [max_rows, N]
+ *   else            gate and up rows: N = 2I, out = act(y[0..I-1]) * y[I..2I-1],
+ *                   out_buf a receive-format buffer of width I in out_quant
+ *                   (EP_QUANT_NONE or a per-128 mode; quantised from float32)
+ * Codes are multiplied by the matrix cores in blocks of 64 products, which
+ * they add with less than float32 precision (about 3e-4 of the block's sum of
+ * |products|); blocks of 128 are scaled and added in float32.
+ *   k, n        positive multiples of 128 (n of 256 with an activation), up to 65536
+ *   w           device, 16-byte aligned, codes as they come (not packed)
+ *   w_scales    device float32
+ * handle, recv_count and the rows that hold no pair as for ep_ffn. */
+ep_status_t ep_moe_gmm_b128(const ep_handle_t *handle, const int64_t *recv_count, const void *a_buf,
+                            size_t a_buf_bytes, ep_quant_t a_quant, int32_t k, int32_t n, const void *w,
+                            const float *w_scales, int32_t transposed, ep_act_t act, ep_quant_t out_quant,
+                            void *out_buf, size_t out_buf_bytes, void *stream);
+
 /* Waits for `stream` and copies the status word of `handle` (EP_STATUS_*
  * bits) to host *flags. */
 ep_status_t ep_read_status(const ep_handle_t *handle, uint32_t *flags, void *stream);

@@ -38,12 +38,14 @@ Modules:
 * ``router``   -- the router's ids and weights, and their gradient.
 * ``layer``    -- the few-token expert layer and the low-rank adapters, with
   rounding bounds.
+* ``ffn``      -- the gated feed-forward block of expert rows with its
+  gradients, and the block-scaled product, with rounding bounds.
 * ``validate`` -- the argument rules the C ABI enforces before any launch.
 
 Parity status of every function is listed in each module's header.
 """
 
-from . import codecs, quant, layout, dispatch, combine, backward, validate, moe, router, layer  # noqa: F401
+from . import codecs, quant, layout, dispatch, combine, backward, validate, moe, router, layer, ffn  # noqa: F401
 from .layout import Layout  # noqa: F401
 
 QUANT_MODES = ("none", "int8_token", "fp8_b128", "mxfp8", "mxfp4", "fp8_b128_pow2", "fp8_b128_ue8m0")
