@@ -167,8 +167,30 @@ struct Source {                           // uniform over a wave
   int valid;                              // indexes (rows of the tile) inside the operand
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes, 0x00020000);
+// A buffer descriptor: base, range in bytes (reads past it give zeros).
+__device__ __forceinline__ u32x4 descriptor(const char *base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)base;
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+
+// 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.  Written as
+// assembly because the compiler, which cannot tell the stages apart, would
+// wait for every such load before the next LDS read: wait_stage() does the
+// waiting.  (The loads have no destination registers; nothing else in these
+// kernels uses m0.)
+// `first`: of a group with one descriptor, which a vector instruction may have
+// written just before (five wait states).
+__device__ __forceinline__ void load_lds16(uint32_t lds, int voff, u32x4 desc, int soff, bool first) {
+  if (first)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(desc), "s"(soff)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(desc), "s"(soff)
+                 : "memory");
 }
 
 // Loads the wave's share of a tile of ROWS indexes: pieces of 1 KB.
@@ -214,19 +236,18 @@ struct Loader {
 
   // stage t of k; `steps_left`: k from this stage on (strided form)
   __device__ __forceinline__ void load(lds_u8 *tile, const Source &s, int t, int64_t k_left) const {
-    __amdgpu_buffer_rsrc_t r;
+    u32x4 r;
     int soff = 0;
     if constexpr (STRIDED) {
       const int64_t rows = k_left < kSteps ? k_left : kSteps;
-      r = rsrc(s.base + (int64_t)t * kSteps * s.pitch, (uint32_t)(rows * s.pitch));
+      r = descriptor(s.base + (int64_t)t * kSteps * s.pitch, (uint32_t)(rows * s.pitch));
     } else {
-      r = rsrc(s.base, (uint32_t)(s.valid * s.pitch));
+      r = descriptor(s.base, (uint32_t)(s.valid * s.pitch));
       soff = t * kKBytes;
     }
+    const uint32_t to = (uint32_t)(uintptr_t)tile + lds0;
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(tile + lds0 + j * 1024), 16,
-                                               voff[j], soff, 0, 0);
+    for (int j = 0; j < kLoads; ++j) load_lds16(to + j * 1024, voff[j], r, soff, j == 0);
   }
 };
 
