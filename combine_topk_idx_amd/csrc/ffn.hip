@@ -46,8 +46,8 @@ __device__ __forceinline__ void product(Acc &acc, const Source &c, const Source 
   Reader<S::BN, CSTR, 2, S::CF> rc;
   Reader<S::BM, RSTR, 2, S::RF> rr;
   const int wn = wave % S::WN, wm = wave / S::WN;
-  rc.init(lane, SPLIT ? wn * 32 : wn * S::CF * 32, kCStride);
-  rr.init(lane, wm * S::RF * 32, 32);
+  rc.init(lane, SPLIT ? wn * 32 : wn * S::CF * 32, [](int f) { return f * kCStride; });
+  rr.init(lane, wm * S::RF * 32, [](int f) { return f * 32; });
 #pragma unroll
   for (int i = 0; i < S::CF; ++i)
 #pragma unroll
@@ -67,9 +67,9 @@ __device__ __forceinline__ void product(Acc &acc, const Source &c, const Source 
     for (int s = 0; s < 4; ++s) {
       bf16x8 fc[S::CF], fr[S::RF];
 #pragma unroll
-      for (int i = 0; i < S::CF; ++i) fc[i] = rc.template bf16<kCStride>(tc, i, s);
+      for (int i = 0; i < S::CF; ++i) fc[i] = rc.bf16(tc, i, i * kCStride, s);
 #pragma unroll
-      for (int j = 0; j < S::RF; ++j) fr[j] = rr.template bf16<32>(tr, j, s);
+      for (int j = 0; j < S::RF; ++j) fr[j] = rr.bf16(tr, j, j * 32, s);
 #pragma unroll
       for (int i = 0; i < S::CF; ++i)
 #pragma unroll

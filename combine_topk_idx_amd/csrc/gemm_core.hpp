@@ -34,6 +34,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
@@ -193,6 +194,21 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, int voff, u32x4 desc, i
                  : "memory");
 }
 
+// One dword, or one byte extended to a dword, a lane: lane l's goes to lds + 4 l.
+template <bool BYTE>
+__device__ __forceinline__ void load_lds4(uint32_t lds, int voff, u32x4 desc, int soff) {
+  if (BYTE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_ubyte %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(desc), "s"(soff)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(desc), "s"(soff)
+                 : "memory");
+}
+
 // Loads the wave's share of a tile of ROWS indexes: pieces of 1 KB.
 //   SPLIT   the first half of the indexes comes from one source, the second
 //           half from another (gate and up rows): the caller gives each wave
@@ -209,10 +225,11 @@ struct Loader {
   int voff[kLoads];
   int lds0;
 
-  // chunk permutation of one k's row (strided form)
+  // chunk permutation of one k's row (strided form): a fragment read of bf16
+  // covers 64 bytes of 4 k in 32 lanes, one of e4m3 16 bytes of 16 k
+  static_assert(!STRIDED || kPitch >= 256, "rows of one k span all banks");
   static __device__ __forceinline__ int strided_key(int k) {
-    if constexpr (EB == 2) return kPitch >= 256 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
-    else return kPitch >= 256 ? (k & 7) << 1 : ((k >> 1) & 3) << 1;
+    return EB == 2 ? (k & 3) << 2 : (k & 7) << 1 | ((k >> 4) & 1);
   }
 
   __device__ __forceinline__ void init(int wave, int lane, const Source &s) {
@@ -251,42 +268,46 @@ struct Loader {
   }
 };
 
-// Fragment reads.  bf16 (32x32x16): lane l holds index l % 32, k = 8 (l / 32)
-// + 0..7 of step s.  e4m3 (32x32x64): lane l holds k = 16 (l / 32) + 0..15 and
-// the same + 32 of step s.
+// Fragment reads.
+//   bf16 (32x32x16): lane l holds index l % 32, k = 8 (l / 32) + 0..7 of step s
+//   e4m3 (16x16x128): lane l holds index l % 16, k = 16 (l / 16) + 0..15 and
+//   the same + 64
+// (both operands alike: the order of k inside an instruction is free).
 template <int ROWS, bool STRIDED, int EB, int FRAGS>
 struct Reader {
   static constexpr int kPitch = ROWS * EB;
-  static constexpr int kAddrs = STRIDED ? FRAGS : (EB == 2 ? 4 : 4);
+  static constexpr int kIndexes = EB == 2 ? 32 : 16;      // of a fragment
+  static constexpr int kAddrs = STRIDED ? FRAGS : (EB == 2 ? 4 : 2);
+  typedef Loader<ROWS, STRIDED, EB, 4, false> L;
   int addr[kAddrs];
 
-  // row[f]: first tile index of fragment f is row0 + f * stride
-  __device__ __forceinline__ void init(int lane, int row0, int stride) {
-    const int half = lane >> 5;
+  // fragment f begins at tile index row0 + index_of(f)
+  template <class F>
+  __device__ __forceinline__ void init(int lane, int row0, F index_of) {
     if constexpr (STRIDED) {
       const int j = lane & 15, g = lane >> 4;
 #pragma unroll
       for (int f = 0; f < FRAGS; ++f) {
+        const int at = row0 + index_of(f);
         if constexpr (EB == 2) {
-          const int k = 8 * half + (j >> 2);
-          const int chunk = (row0 + f * stride) / 8 + 2 * (g & 1) + ((j & 3) >> 1);
-          addr[f] = k * kPitch + (chunk ^ Loader<ROWS, true, EB, 4, false>::strided_key(k)) * 16 + (j & 1) * 8;
+          const int k = 8 * (g >> 1) + (j >> 2);
+          const int chunk = at / 8 + 2 * (g & 1) + ((j & 3) >> 1);
+          addr[f] = k * kPitch + (chunk ^ L::strided_key(k)) * 16 + (j & 1) * 8;
         } else {
-          const int k = 16 * half + (j >> 1);
-          const int chunk = (row0 + f * stride) / 16 + (g & 1);
-          addr[f] = k * kPitch + (chunk ^ Loader<ROWS, true, EB, 4, false>::strided_key(k)) * 16 + (j & 1) * 8;
+          const int k = 16 * g + (j >> 1);
+          addr[f] = k * kPitch + (at / 16 ^ L::strided_key(k)) * 16 + (j & 1) * 8;
         }
       }
     } else {
-      const int r = row0 + (lane & 31);
+      const int r = row0 + (lane & (kIndexes - 1)), key = (r >> 1) & 7;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) addr[s] = r * kKBytes + ((2 * s + half) ^ ((r >> 1) & 7)) * 16;
+      for (int s = 0; s < kAddrs; ++s)
+        addr[s] = r * kKBytes + ((EB == 2 ? 2 * s + (lane >> 5) : 4 * s + (lane >> 4)) ^ key) * 16;
     }
   }
 
-  // bf16 fragment f of k step s (0..3)
-  template <int STRIDE>
-  __device__ __forceinline__ bf16x8 bf16(const lds_u8 *tile, int f, int s) const {
+  // bf16 fragment f of k step s (0..3); index: index_of(f)
+  __device__ __forceinline__ bf16x8 bf16(const lds_u8 *tile, int f, int index, int s) const {
     if constexpr (STRIDED) {
       const lds_u8 *p = tile + addr[f] + s * 16 * kPitch;
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
@@ -295,36 +316,42 @@ struct Reader {
       const s16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
       return __builtin_bit_cast(bf16x8, v);
     } else {
-      return *(const __attribute__((address_space(3))) bf16x8 *)(tile + addr[s] + f * STRIDE * kKBytes);
+      return *(const __attribute__((address_space(3))) bf16x8 *)(tile + addr[s] + index * kKBytes);
     }
   }
 
-  // e4m3 fragment f of k step s (0..1)
-  template <int STRIDE>
-  __device__ __forceinline__ v8i fp8(const lds_u8 *tile, int f, int s) const {
+  // e4m3 fragment f
+  __device__ __forceinline__ v8i fp8(const lds_u8 *tile, int f, int index) const {
     if constexpr (STRIDED) {
-      const lds_u8 *p = tile + addr[f] + s * 64 * kPitch;
+      const lds_u8 *p = tile + addr[f];
       v2i q[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         q[t] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) v2i *)(p + (32 * (t >> 1) + 8 * (t & 1)) * kPitch));
+            (__attribute__((address_space(3))) v2i *)(p + (64 * (t >> 1) + 8 * (t & 1)) * kPitch));
       return v8i{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
     } else {
-      const u32x4 a = *(const __attribute__((address_space(3))) u32x4 *)(tile + addr[2 * s] + f * STRIDE * kKBytes);
-      const u32x4 b = *(const __attribute__((address_space(3))) u32x4 *)(tile + addr[2 * s + 1] + f * STRIDE * kKBytes);
+      const u32x4 a = *(const __attribute__((address_space(3))) u32x4 *)(tile + addr[0] + index * kKBytes);
+      const u32x4 b = *(const __attribute__((address_space(3))) u32x4 *)(tile + addr[1] + index * kKBytes);
       return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
     }
   }
 };
 
 // Waits until at most N of the wave's loads are in flight; its LDS reads are
-// done; then for the other waves.
+// done; then (wait_stage) for the other waves.
 template <int N>
-__device__ __forceinline__ void wait_stage() {
+__device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_waves() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+  wait_loads<N>();
+  wait_waves();
 }
 
 // Tile shape: WN x WM waves of CF x RF fragments of 32 x 32, STAGES tiles of k
@@ -367,12 +394,41 @@ __device__ __forceinline__ void store_bf16(char *dst, int half, int cols, F valu
   }
 }
 
+// The same for a pair of 16-column fragments of 16 x 16 (accumulator i of
+// lane l: column 4 (l / 16) + i, row l % 16): rows of 16 lanes exchanged, lane
+// l has columns pair_column(l) + 0..7 of the pair's 32.
+__device__ __forceinline__ int pair_column(int lane) { return ((lane >> 4) & 1) * 16 + (lane >> 5) * 8; }
+__device__ __forceinline__ void swap_rows(uint32_t &x, uint32_t &y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  x = r[0];
+  y = r[1];
+}
+__device__ __forceinline__ void store_bf16_pair(char *dst, int lane, int cols, const v4f &a, const v4f &b) {
+  uint32_t x0 = pack_bf16x2(a[0], a[1]), x1 = pack_bf16x2(a[2], a[3]);
+  uint32_t y0 = pack_bf16x2(b[0], b[1]), y1 = pack_bf16x2(b[2], b[3]);
+  swap_rows(x0, y0);
+  swap_rows(x1, y1);
+  const int n = pair_column(lane);
+  if (n < cols) *(u32x4 *)(dst + n * 2) = u32x4{x0, x1, y0, y1};
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
 // Bits of the largest magnitude of a lane's 16 values and of its row's other
 // 16 (as integers: a value that is not a number counts as the largest).
 __device__ __forceinline__ uint32_t row_amax(const v16f &v) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 16; ++i) m = max(m, magnitude(v[i]));
+  return max(m, (uint32_t)__shfl_xor((int)m, 32));
+}
+
+// The same of a pair of 16 x 16 fragments.
+__device__ __forceinline__ uint32_t row_amax(const v4f &a, const v4f &b) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(magnitude(a[i]), magnitude(b[i])));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
   return max(m, (uint32_t)__shfl_xor((int)m, 32));
 }
 
@@ -406,26 +462,36 @@ __device__ __forceinline__ Block128 block128(int quant, uint32_t amax_bits) {
   return b;
 }
 
-// e4m3 codes of a fragment: dst = the row's first column of the fragment.
+// Four e4m3 codes.
+__device__ __forceinline__ uint32_t codes4(const float (&v)[4], const Block128 &b) {
+  float z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = v[i] * b.m;
+    z[i] = x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x;              // NaN stays
+  }
+  uint32_t q = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
+  q = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], q, true);
+  return b.zero ? 0 : q;
+}
+
+// e4m3 codes of a fragment (of a pair of 16 x 16 fragments): dst = the row's
+// first column.
 __device__ __forceinline__ void store_codes(char *dst, int half, bool ok, const v16f &v, const Block128 &b) {
   uint32_t q[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float z[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = v[4 * c + i] * b.m;
-      z[i] = x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x;            // NaN stays
-    }
-    q[c] = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], 0, false);
-    q[c] = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], q[c], true);
-    if (b.zero) q[c] = 0;
-  }
+  for (int c = 0; c < 4; ++c) q[c] = codes4({v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]}, b);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     swap_halves(q[2 * p], q[2 * p + 1]);
     if (ok) *(u32x2 *)(dst + 16 * p + 8 * half) = u32x2{q[2 * p], q[2 * p + 1]};
   }
+}
+__device__ __forceinline__ void store_codes_pair(char *dst, int lane, bool ok, const v4f &x, const v4f &y,
+                                                 const Block128 &b) {
+  uint32_t p = codes4({x[0], x[1], x[2], x[3]}, b), q = codes4({y[0], y[1], y[2], y[3]}, b);
+  swap_rows(p, q);
+  if (ok) *(u32x2 *)(dst + pair_column(lane)) = u32x2{p, q};
 }
 
 // The gate's activation.

@@ -22,121 +22,128 @@ struct GmmArgs {
   const char *c;           // weights [E, n, k], or [E, k, n]
   const float *c_scales;   // by 128 x 128 block, in the weights' order
   int k, n;                // n: output columns (gated: of gate and up each)
-  int bytes;               // row scales are e8m0 bytes
   int act, out_quant;      // of a gated product
   char *out;               // bf16 rows or e4m3 codes
   char *out_scales;
 };
 
-// Row scales: a group of four blocks for every row of the tile, transposed
-// in LDS ([block][row]), two groups in turn.
-template <int BM>
-struct RowScales {
-  float v[4];
-  // thread t < BM holds row t
-  __device__ __forceinline__ void load(const GmmArgs &p, int64_t row0, int rows, int group) {
-    const int kb = p.k / 128, t = threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = group * 4 + i;
-      v[i] = 0.0f;
-      if (t < rows && b < kb) {
-        const int64_t at = (row0 + t) * kb + b;
-        v[i] = p.bytes ? e8m0_decode(((const uint8_t *)p.r_scales)[at]) : ((const float *)p.r_scales)[at];
-      }
-    }
-  }
-  __device__ __forceinline__ void put(float *lds, int group) const {
-    if ((int)threadIdx.x < BM) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lds[((group & 1) * 4 + i) * BM + threadIdx.x] = v[i];
-    }
-  }
+// The row scales of a stage lie behind the stages: one dword a row (a float32,
+// or a byte extended), fetched by the first waves together with the stage.
+template <class S>
+struct ScaleArea {
+  static constexpr int kRows = S::BM < kWave ? kWave : S::BM;
+  static constexpr int kWaves = kRows / kWave;               // waves that fetch 64 rows each
+  static constexpr int kBytes = kRows * 4;
 };
 
-template <class S, bool CSTR, bool SPLIT, class Acc>
+// What the compiler may read through the scalar cache: uniform, and written
+// by no kernel that runs beside this one.
+typedef const __attribute__((address_space(4))) float *const_floats;
+
+template <class S, bool CSTR, bool SPLIT, bool BYTES, class Acc>
 __device__ __forceinline__ void product(Acc &acc, const GmmArgs &p, const Source &c, const Source &r,
-                                        int64_t row0, int e, int n0, float *sa, lds_u8 *lds, int wave, int lane) {
+                                        int64_t row0, int e, int n0, lds_u8 *lds, int wave, int lane) {
   typedef Loader<S::BN, CSTR, 1, S::kWaves, SPLIT> LC;
   typedef Loader<S::BM, false, 1, S::kWaves, false> LR;
   constexpr int kLoads = LC::kLoads + LR::kLoads, N = S::kStages;
-  constexpr int kCStride = SPLIT ? S::BN / 2 : 32;
+  constexpr int CF = 2 * S::CF, RF = 2 * S::RF;              // of 16 x 16
   LC lc;
   LR lr;
   lc.init(wave, lane, c);
   lr.init(wave, lane, r);
-  Reader<S::BN, CSTR, 1, S::CF> rc;
-  Reader<S::BM, false, 1, S::RF> rr;
+  Reader<S::BN, CSTR, 1, CF> rc;
+  Reader<S::BM, false, 1, RF> rr;
   const int wn = wave % S::WN, wm = wave / S::WN;
-  rc.init(lane, SPLIT ? wn * 32 : wn * S::CF * 32, kCStride);
-  rr.init(lane, wm * S::RF * 32, 32);
+  // gated: the wave's first fragments are gate rows, the others the same up rows
+  auto c_index = [](int f) { return SPLIT ? f / S::CF * (S::BN / 2) + f % S::CF * 16 : f * 16; };
+  rc.init(lane, SPLIT ? wn * S::CF * 16 : wn * CF * 16, c_index);
+  rr.init(lane, wm * RF * 16, [](int f) { return f * 16; });
 #pragma unroll
-  for (int i = 0; i < S::CF; ++i)
+  for (int i = 0; i < CF; ++i)
 #pragma unroll
-    for (int j = 0; j < S::RF; ++j) acc[i][j] = v16f{};
+    for (int j = 0; j < RF; ++j) acc[i][j] = v4f{};
   const int steps = p.k / 128, kb = p.k / 128;
   // weight scales of the wave's columns (64 or fewer, gated: of one gate and
   // one up block)
   const int nb_all = SPLIT ? 2 * p.n / 128 : p.n / 128;
   const int nb = min(n0 / 128 + (SPLIT ? 0 : wn * S::CF * 32 / 128), nb_all - 1);
-  const float *sw = p.c_scales + (int64_t)e * nb_all * kb + (CSTR ? nb : (int64_t)nb * kb);
+  const const_floats sw = (const_floats)(p.c_scales + (int64_t)e * nb_all * kb + (CSTR ? nb : (int64_t)nb * kb));
   const int64_t sw_step = CSTR ? nb_all : 1, sw_up = SPLIT ? (int64_t)(p.n / 128) * kb : 0;
+  typedef ScaleArea<S> A;
+  constexpr int kScale = BYTES ? 1 : 4;                      // bytes of a row scale in memory
+  const uint32_t area = (uint32_t)(uintptr_t)lds + S::kLds;
+  const u32x4 scales = descriptor(p.r_scales + row0 * kb * kScale, (uint32_t)(r.valid * kb * kScale));
+  const int soff_row = (wave * kWave + lane) * kb * kScale;   // rows past the tile's are past the range
   auto fetch = [&](int t) {
     lds_u8 *at = lds + (t % N) * S::kStage;
     lc.load(at, c, t, p.k - (int64_t)t * 128);
     lr.load(at + S::BN * kKBytes, r, t, p.k - (int64_t)t * 128);
+    if (wave < A::kWaves) load_lds4<BYTES>(area + (t % N) * A::kBytes + wave * kWave * 4, soff_row, scales, t * kScale);
   };
-  RowScales<S::BM> scales;
-  scales.load(p, row0, r.valid, 0);
   for (int t = 0; t < N - 1 && t < steps; ++t) fetch(t);
-  scales.put(sa, 0);
   float w0 = sw[0], w1 = SPLIT ? sw[sw_up] : 0.0f;
   for (int t = 0; t < steps; ++t) {
-    if (t + N - 2 < steps) wait_stage<kLoads * (N - 2)>();
-    else wait_stage<0>();
+    if (t + N - 2 >= steps) wait_loads<0>();
+    else if (wave < A::kWaves) wait_loads<(kLoads + 1) * (N - 2)>();
+    else wait_loads<kLoads * (N - 2)>();
+    wait_waves();
     if (t + N - 1 < steps) fetch(t + N - 1);
-    if ((t & 3) == 0) scales.load(p, row0, r.valid, t / 4 + 1);
     const int next = min(t + 1, steps - 1);
     const float w0n = sw[next * sw_step], w1n = SPLIT ? sw[next * sw_step + sw_up] : 0.0f;
     const lds_u8 *tc = lds + (t % N) * S::kStage, *tr = tc + S::BN * kKBytes;
-    const float *srow = sa + (((t >> 2) & 1) * 4 + (t & 3)) * S::BM + wm * S::RF * 32 + (lane & 31);
-    v8i fc[S::CF][2];
+    const lds_u8 *srow = lds + S::kLds + (t % N) * A::kBytes + (wm * RF * 16 + (lane & 15)) * 4;
+    auto row_scale = [&](int j) {
+      const uint32_t v = *(const __attribute__((address_space(3))) uint32_t *)(srow + j * 64);
+      return BYTES ? e8m0_decode(v) : __uint_as_float(v);
+    };
+    v8i fc[CF];
 #pragma unroll
-    for (int i = 0; i < S::CF; ++i)
+    for (int i = 0; i < CF; ++i) fc[i] = rc.fp8(tc, i, c_index(i));
+    // one row fragment ahead; a fragment's products are scaled and added
+    // while the matrix cores work on the next one's
+    v8i fr = rr.fp8(tr, 0, 0);
+    float sr = row_scale(0), sp = 0.0f;
+    v4f q[CF];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) fc[i][s] = rc.template fp8<kCStride>(tc, i, s);
-#pragma unroll
-    for (int j = 0; j < S::RF; ++j) {
-      const v8i f0 = rr.template fp8<32>(tr, j, 0), f1 = rr.template fp8<32>(tr, j, 1);
-      const float sr = srow[j * 32];
-#pragma unroll
-      for (int i = 0; i < S::CF; ++i) {
-        v16f q = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fc[i][0], f0, v16f{}, 0, 0, 0, 0x7f7f7f7f, 0,
-                                                                 0x7f7f7f7f);
-        q = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fc[i][1], f1, q, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-        const float by = sr * (SPLIT && i ? w1 : w0);
-#pragma unroll
-        for (int x = 0; x < 16; ++x) acc[i][j][x] = __builtin_fmaf(q[x], by, acc[i][j][x]);
+    for (int j = 0; j <= RF; ++j) {
+      v8i fn;
+      float sn = 0.0f;
+      if (j + 1 < RF) {
+        fn = rr.fp8(tr, j + 1, (j + 1) * 16);
+        sn = row_scale(j + 1);
       }
+#pragma unroll
+      for (int i = 0; i < CF; ++i) {
+        const v4f was = q[i];
+        if (j < RF) q[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fc[i], fr, v4f{}, 0, 0, 0, 0, 0, 0);
+        if (j > 0) {
+          const float by = sp * (SPLIT && i >= S::CF ? w1 : w0);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[i][j - 1][x] = __builtin_fmaf(was[x], by, acc[i][j - 1][x]);
+          acc[i][j - 1] = pin(acc[i][j - 1]);                // here, not after the loop's branches
+        }
+      }
+      fr = fn;
+      sp = sr;
+      sr = sn;
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if ((t & 3) == 3) scales.put(sa, t / 4 + 1);
     w0 = w0n;
     w1 = w1n;
   }
 }
 
 // GATED: gate and up rows in, n columns act(gate) * up out
-template <class S, bool CSTR, bool GATED>
+template <class S, bool CSTR, bool GATED, bool BYTES>
 __global__ __launch_bounds__(S::kThreads) void gmm_kernel(GmmArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
   constexpr bool kSplit = GATED;
   constexpr int kCols = kSplit ? S::BN / 2 : S::BN;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
-  __shared__ float sa[8 * S::BM];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + S::kStages * ScaleArea<S>::kBytes];
   __shared__ Groups g;
   lds_u8 *lds = (lds_u8 *)smem;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  const int half = lane >> 5, wn = wave % S::WN, wm = wave / S::WN;
+  const int wn = wave % S::WN, wm = wave / S::WN;
   scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
   const int nc = (p.n + kCols - 1) / kCols;
   const int64_t units = (int64_t)g.first[p.E] * nc;
@@ -155,47 +162,50 @@ __global__ __launch_bounds__(S::kThreads) void gmm_kernel(GmmArgs p) {
     } else {
       c = Source{p.c + ((int64_t)u.e * p.n + n0) * p.k, p.k, min(kCols, p.n - n0)};
     }
-    v16f acc[S::CF][S::RF];
-    product<S, CSTR, kSplit>(acc, p, c, r, u.row0, u.e, n0, sa, lds, wave, lane);
+    constexpr int CF = 2 * S::CF, RF = 2 * S::RF;
+    v4f acc[CF][RF];
+    product<S, CSTR, kSplit, BYTES>(acc, p, c, r, u.row0, u.e, n0, lds, wave, lane);
     __syncthreads();
     if constexpr (!kSplit) {
 #pragma unroll
-      for (int i = 0; i < S::CF; ++i) {
-        const int n = n0 + (wn * S::CF + i) * 32, cols = p.n - n;
+      for (int i = 0; i < CF; i += 2) {
+        const int n = n0 + (wn * CF + i) * 16, cols = p.n - n;
 #pragma unroll
-        for (int j = 0; j < S::RF; ++j) {
-          const int at = (wm * S::RF + j) * 32 + (lane & 31);
-          store_bf16(p.out + ((u.row0 + at) * p.n + n) * 2, half, at < u.rows ? cols : 0,
-                     [&](int q) { return acc[i][j][q]; });
+        for (int j = 0; j < RF; ++j) {
+          const int at = (wm * RF + j) * 16 + (lane & 15);
+          store_bf16_pair(p.out + ((u.row0 + at) * p.n + n) * 2, lane, at < u.rows ? cols : 0, acc[i][j], acc[i + 1][j]);
         }
       }
     } else {
+      static_assert(!kSplit || S::CF == 2, "a wave holds 32 gate and the same 32 up columns");
       const int n = n0 + wn * 32;                            // n is a multiple of 128: the tile lies inside
       uint32_t *top = (uint32_t *)smem;                      // [WN][BM] bits of the largest magnitudes
 #pragma unroll
-      for (int j = 0; j < S::RF; ++j) {
+      for (int j = 0; j < RF; ++j) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) acc[0][j][q] = act(p.act, acc[0][j][q]) * acc[S::CF - 1][j][q];
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = act(p.act, acc[i][j][q]) * acc[CF / 2 + i][j][q];
         if (p.out_quant != EP_QUANT_NONE) {
-          const uint32_t m = row_amax(acc[0][j]);
-          if (half == 0) top[wn * S::BM + (wm * S::RF + j) * 32 + lane] = m;
+          const uint32_t m = row_amax(acc[0][j], acc[1][j]);
+          if (lane < 16) top[wn * S::BM + (wm * RF + j) * 16 + lane] = m;
         }
       }
       if (p.out_quant != EP_QUANT_NONE) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < S::RF; ++j) {
-        const int at = (wm * S::RF + j) * 32 + (lane & 31);
+      for (int j = 0; j < RF; ++j) {
+        const int at = (wm * RF + j) * 16 + (lane & 15);
         const int64_t row = u.row0 + at;
         const bool ok = at < u.rows;
         if (p.out_quant == EP_QUANT_NONE) {
-          store_bf16(p.out + (row * p.n + n) * 2, half, ok ? 32 : 0, [&](int q) { return acc[0][j][q]; });
+          store_bf16_pair(p.out + (row * p.n + n) * 2, lane, ok ? 32 : 0, acc[0][j], acc[1][j]);
         } else {
           uint32_t m = 0;
 #pragma unroll
           for (int w = 0; w < S::WN; ++w) m = max(m, top[w * S::BM + at]);
           const Block128 b = block128(p.out_quant, m);
-          store_codes(p.out + row * p.n + n, half, ok, acc[0][j], b);
-          if (ok && wn == 0 && half == 0) {
+          store_codes_pair(p.out + row * p.n + n, lane, ok, acc[0][j], acc[1][j], b);
+          if (ok && wn == 0 && lane < 16) {
             const int64_t to = row * (p.n / 128) + n0 / 128;
             if (p.out_quant == EP_QUANT_FP8_B128_UE8M0) ((uint8_t *)p.out_scales)[to] = (uint8_t)b.byte;
             else ((float *)p.out_scales)[to] = b.scale;
@@ -213,22 +223,28 @@ typedef Shape<2, 2, 4, 2, 3> Medium;
 typedef Shape<2, 1, 4, 2, 3> Small;
 typedef Shape<2, 1, 4, 1, 4> Tiny;
 
-template <class S, bool CSTR, bool GATED>
+template <class S, bool CSTR, bool GATED, bool BYTES>
 hipError_t launch(const GmmArgs &p, int64_t pairs, hipStream_t s) {
   const int cols = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = (pairs + S::BM - 1) / S::BM + (p.E < pairs ? p.E : pairs);
   const int64_t units = tiles * ((p.n + cols - 1) / cols);
-  hipLaunchKernelGGL((gmm_kernel<S, CSTR, GATED>), dim3((unsigned)persistent_grid(units)), dim3(S::kThreads), 0, s, p);
+  hipLaunchKernelGGL((gmm_kernel<S, CSTR, GATED, BYTES>), dim3((unsigned)persistent_grid(units)), dim3(S::kThreads), 0, s, p);
   return hipGetLastError();
 }
 
-template <bool CSTR, bool GATED>
+template <bool CSTR, bool GATED, bool BYTES>
 hipError_t by_shape(const GmmArgs &p, int64_t pairs, hipStream_t s) {
   const int64_t mean = pairs / p.E;
-  if (mean <= 32) return launch<Tiny, CSTR, GATED>(p, pairs, s);
-  if (mean <= 64) return launch<Small, CSTR, GATED>(p, pairs, s);
-  if (mean <= 192) return launch<Medium, CSTR, GATED>(p, pairs, s);
-  return launch<Large, CSTR, GATED>(p, pairs, s);
+  if (mean <= 32) return launch<Tiny, CSTR, GATED, BYTES>(p, pairs, s);
+  if (mean <= 64) return launch<Small, CSTR, GATED, BYTES>(p, pairs, s);
+  if (mean <= 192) return launch<Medium, CSTR, GATED, BYTES>(p, pairs, s);
+  return launch<Large, CSTR, GATED, BYTES>(p, pairs, s);
+}
+
+template <bool BYTES>
+hipError_t by_form(const GmmArgs &p, const GmmB128Args &a, int64_t pairs, hipStream_t s) {
+  if (a.transposed) return by_shape<true, false, BYTES>(p, pairs, s);
+  return a.act == EP_ACT_NONE ? by_shape<false, false, BYTES>(p, pairs, s) : by_shape<false, true, BYTES>(p, pairs, s);
 }
 
 }  // namespace
@@ -238,10 +254,9 @@ hipError_t launch_gmm_b128(const GmmB128Args &a, hipStream_t s) {
   if (pairs == 0) return hipSuccess;
   const int n = a.act != EP_ACT_NONE ? a.n / 2 : a.n;
   GmmArgs p{a.h.offsets, a.recv_count, a.h.num_experts, a.a, a.a + recv_geom(a.h.max_rows, a.k, a.a_quant).scale_off,
-            (const char *)a.w, a.w_scales, a.k, n, a.a_quant == EP_QUANT_FP8_B128_UE8M0, a.act, a.out_quant, a.out, nullptr};
+            (const char *)a.w, a.w_scales, a.k, n, a.act, a.out_quant, a.out, nullptr};
   if (a.out_quant != EP_QUANT_NONE) p.out_scales = a.out + recv_geom(a.h.max_rows, n, a.out_quant).scale_off;
-  if (a.transposed) return by_shape<true, false>(p, pairs, s);
-  return a.act == EP_ACT_NONE ? by_shape<false, false>(p, pairs, s) : by_shape<false, true>(p, pairs, s);
+  return a.a_quant == EP_QUANT_FP8_B128_UE8M0 ? by_form<true>(p, a, pairs, s) : by_form<false>(p, a, pairs, s);
 }
 
 }  // namespace ep
