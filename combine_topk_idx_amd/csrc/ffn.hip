@@ -57,24 +57,46 @@ __device__ __forceinline__ void product(Acc &acc, const Source &c, const Source 
     lc.load(at, c, t, k_all - (int64_t)t * 64);
     lr.load(at + S::BN * kKBytes, r, t, k_all - (int64_t)t * 64);
   };
-  for (int t = 0; t < N - 1 && t < steps; ++t) fetch(t);
-  for (int t = 0; t < steps; ++t) {
+  // Fragments are read one k step of 16 ahead, across the stages' borders: the
+  // waves meet before the last step's matrix instructions, which then cover
+  // the first reads of the next stage.
+  bf16x8 fc[2][S::CF], fr[2][S::RF];
+  auto read = [&](int t, int s, int to) {
+    const lds_u8 *tc = lds + (t % N) * S::kStage, *tr = tc + S::BN * kKBytes;
+#pragma unroll
+    for (int i = 0; i < S::CF; ++i) fc[to][i] = rc.bf16(tc, i, i * kCStride, s);
+#pragma unroll
+    for (int j = 0; j < S::RF; ++j) fr[to][j] = rr.bf16(tr, j, j * 32, s);
+  };
+  auto multiply = [&](int from) {
+#pragma unroll
+    for (int j = 0; j < S::RF; ++j)
+#pragma unroll
+      for (int i = 0; i < S::CF; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[from][i], fr[from][j], acc[i][j], 0, 0, 0);
+  };
+  // stage t is there and no wave reads stage t - 1 any more
+  auto meet = [&](int t) {
     if (t + N - 2 < steps) wait_stage<kLoads * (N - 2)>();
     else wait_stage<0>();
     if (t + N - 1 < steps) fetch(t + N - 1);
-    const lds_u8 *tc = lds + (t % N) * S::kStage, *tr = tc + S::BN * kKBytes;
+  };
+  if (steps == 0) return;
+  for (int t = 0; t < N - 1 && t < steps; ++t) fetch(t);
+  meet(0);
+  read(0, 0, 0);
+  for (int t = 0; t < steps; ++t) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      bf16x8 fc[S::CF], fr[S::RF];
-#pragma unroll
-      for (int i = 0; i < S::CF; ++i) fc[i] = rc.bf16(tc, i, i * kCStride, s);
-#pragma unroll
-      for (int j = 0; j < S::RF; ++j) fr[j] = rr.bf16(tr, j, j * 32, s);
-#pragma unroll
-      for (int i = 0; i < S::CF; ++i)
-#pragma unroll
-        for (int j = 0; j < S::RF; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[i], fr[j], acc[i][j], 0, 0, 0);
+      if (s < 3) {
+        read(t, s + 1, (s + 1) & 1);
+      } else if (t + 1 < steps) {
+        meet(t + 1);
+        read(t + 1, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(s & 1);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
