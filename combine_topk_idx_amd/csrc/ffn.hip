@@ -101,6 +101,57 @@ __device__ __forceinline__ void product(Acc &acc, const Source &c, const Source 
   }
 }
 
+// The same on the 256 x 256 tile; c_hi: the up rows of a split operand.
+template <bool CSTR, bool RSTR, bool SPLIT, class Acc>
+__device__ __forceinline__ void product256(Acc &acc, const Source &c, const Source &c_hi, const Source &r, int steps,
+                                           int64_t k_all, lds_u8 *lds, int wave, int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
+  if (steps == 0) return;
+  Pipe256<CSTR, RSTR, 2, SPLIT> p;
+  p.init(c, c_hi, r, k_all, lds, wave, lane);
+  p.template begin<0>(steps, [](int) {});
+  bf16x8 fc[2][4], fr[2][4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    fr[0][s] = p.read_r(0, 0, s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(0, i, s);
+  }
+  auto step = [&](int t, auto last) {
+    constexpr bool kLast = decltype(last)::value;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q == 1) p.template meet1<0, kLast>(t, steps);
+      if (q == 3) p.template meet3<0, kLast>(t, steps);
+      const bool more = q < 3 || !kLast || t + 1 < steps;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[i][s], fr[q & 1][s], acc[i][q], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+          fr[(q + 1) & 1][s] = p.read_r(q < 3 ? t : t + 1, (q + 1) & 3, s);
+          if (q == 3) {
+            // this step's column fragments have been used for the last time
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(t + 1, i, s);
+          }
+        }
+        if (s < 2) p.template fetch<kLast>(t, q, s, steps);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+  int t = 0;
+  for (; t + 2 < steps; ++t) step(t, Flag<false>());
+  for (; t < steps; ++t) step(t, Flag<true>());
+}
+
 // Four values of the checkpoint.
 [[maybe_unused]] __device__ __forceinline__ void load4_bf16(const char *p, float (&v)[4]) {
   const u32x2 q = *(const u32x2 *)p;
@@ -134,7 +185,7 @@ __global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
     const Source r{p.r + row0 * p.k * 2, (int64_t)p.k * 2, rows};
     Source c;
     if constexpr (kSplit) {
-      const int from = (wave >= S::kWaves / 2 ? p.n : 0) + n0;
+      const int from = (!S::kDeep && wave >= S::kWaves / 2 ? p.n : 0) + n0;
       c = Source{p.c + ((int64_t)e * 2 * p.n + from) * p.k * 2, (int64_t)p.k * 2, min(kCols, p.n - n0)};
     } else if constexpr (kCStr) {
       c = Source{p.c + ((int64_t)e * p.k * p.n + n0) * 2, (int64_t)p.n * 2, p.n - n0};
@@ -142,7 +193,12 @@ __global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
       c = Source{p.c + ((int64_t)e * p.n + n0) * p.k * 2, (int64_t)p.k * 2, min(kCols, p.n - n0)};
     }
     v16f acc[S::CF][S::RF];
-    product<S, kCStr, false, kSplit>(acc, c, r, p.k / 64, p.k, lds, wave, lane);
+    if constexpr (S::kDeep) {
+      const Source c_hi{c.base + (int64_t)p.n * p.k * 2, c.pitch, c.valid};
+      product256<kCStr, false, kSplit>(acc, c, c_hi, r, p.k / 64, p.k, lds, wave, lane);
+    } else {
+      product<S, kCStr, false, kSplit>(acc, c, r, p.k / 64, p.k, lds, wave, lane);
+    }
     __syncthreads();                                         // the stages are free
     if constexpr (MODE == kUp) {
       static_assert(MODE != kUp || S::CF == 2, "one gate and one up fragment a wave");
@@ -285,7 +341,7 @@ __global__ __launch_bounds__(S::kThreads) void weights_kernel(WeightArgs p) {
     const Source r{p.r + (row0 * p.nr + r0) * 2, (int64_t)p.nr * 2, p.nr - r0};
     const Source c{p.c + (row0 * p.nc + c0) * 2, (int64_t)p.nc * 2, p.nc - c0};
     v16f acc[S::CF][S::RF];
-    product<S, true, true, false>(acc, c, r, (rows + 63) / 64, rows, lds, wave, lane);
+    product256<true, true, false>(acc, c, c, r, (rows + 63) / 64, rows, lds, wave, lane);
 #pragma unroll
     for (int i = 0; i < S::CF; ++i) {
       const int n = c0 + (wn * S::CF + i) * 32, cols = p.nc - n;

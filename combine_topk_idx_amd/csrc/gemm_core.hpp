@@ -38,6 +38,11 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
 constexpr int kXcds = 8;
 constexpr int kKBytes = 128;              // bytes of k in a stage
 
@@ -363,6 +368,174 @@ struct Shape {
   static constexpr int BN = 32 * CF * WN, BM = 32 * RF * WM;
   static constexpr int kStage = (BN + BM) * kKBytes;
   static constexpr int kLds = kStage * kStages;
+  static constexpr bool kDeep = BN == 256 && BM == 256;  // runs on Pipe256
+};
+
+// ---------------------------------------------------------------------------
+// the 256 x 256 tile
+// ---------------------------------------------------------------------------
+//
+// Eight waves (4 along the columns, 2 along the rows) of 64 columns x 128 rows,
+// two stages of 64 KB.  A stage is worked through in quarters of 32 of a
+// wave's rows (8 matrix instructions of bf16, 8 of e4m3); the column
+// fragments of the whole stage stay in registers.  A part of a stage is
+// fetched again (for two stages on) as soon as every wave has read it, a
+// quarter of the bytes in every quarter:
+//   quarter    fetched                         the waves meet first, so that
+//   0          row quarters 2, 3 of stage t+1
+//   1          row quarters 0, 1 of stage t+2  (row quarters 2, 3 of t are there)
+//   2          first half of C of stage t+2
+//   3          second half of C of stage t+2   (C, row quarters 0, 1 of t+1 are there)
+// which leaves every load at least four quarters (2048 matrix-core cycles)
+// and never queues more than two a wave: issued in one burst, the 64 loads of
+// a stage held every wave's next instruction back for about 1000 cycles.
+// Fragments are read a quarter ahead, between the matrix instructions.
+// In LDS the rows of quarters 0, 1 (of both row halves) come first.
+struct Tile256 {
+  static constexpr int BN = 256, BM = 256, kThreads = 512, WN = 4, WM = 2;
+  static constexpr int kStage = 512 * kKBytes, kLds = 2 * kStage;
+  static constexpr int kR = 256 * kKBytes;               // the row part of a stage
+};
+
+template <bool CSTR, bool RSTR, int EB, bool SPLIT>
+struct Pipe256 {
+  static constexpr int kSteps = kKBytes / EB;             // k of a stage
+  static_assert(EB == 2 || !RSTR, "e4m3 rows are k contiguous");
+  // e4m3 fragments are 16 wide, two to a quarter
+  static constexpr int kCFrags = EB == 2 ? 2 : 4, kWide = EB == 2 ? 32 : 16;
+  typedef Reader<256, CSTR, EB, kCFrags> RC;
+  typedef Reader<RSTR ? 128 : 256, RSTR, EB, 2> RR;
+  Source c[2], r[2];                                      // halves of C; row quarters 0, 1 and 2, 3
+  int64_t k_all;
+  lds_u8 *lds;
+  uint32_t to;                                            // the wave's place in a half
+  int vc[2], vr[RSTR ? 2 : 1][2];
+  RC rc;
+  RR rr;
+
+  static __device__ __forceinline__ int c_index(int f) {
+    if constexpr (EB == 2) return f * (SPLIT ? 128 : 32);
+    else return SPLIT ? f / 2 * 128 + f % 2 * 16 : f * 16;
+  }
+
+  // c_hi: the second half's source of a split operand (else unused)
+  __device__ __forceinline__ void init(const Source &cs, const Source &c_hi, const Source &rs, int64_t k, lds_u8 *l,
+                                       int wave, int lane) {
+    k_all = k;
+    lds = l;
+    to = (uint32_t)(uintptr_t)l + wave * 2048;
+    c[0] = cs;
+    if constexpr (SPLIT) c[1] = c_hi;
+    else if constexpr (CSTR) c[1] = Source{cs.base + kSteps / 2 * cs.pitch, cs.pitch, cs.valid};
+    else c[1] = Source{cs.base + 128 * cs.pitch, cs.pitch, max(cs.valid - 128, 0)};
+    r[0] = rs;
+    r[1] = Source{rs.base + (RSTR ? 64 * EB : 64 * rs.pitch), rs.pitch, max(rs.valid - 64, 0)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = (wave * 2 + j) * 1024 + lane * 16;     // in a half
+      if constexpr (CSTR) {
+        const int row = at / (256 * EB), chunk = at % (256 * EB) / 16;
+        const int col = (chunk ^ RC::L::strided_key(row)) * (16 / EB);
+        vc[j] = col < cs.valid ? (int)(row * cs.pitch) + col * EB : 0x7fffff00;
+      } else {
+        const int row = at / kKBytes, chunk = at % kKBytes / 16;
+        vc[j] = row * (int)cs.pitch + (chunk ^ ((row >> 1) & 7)) * 16;
+      }
+      if constexpr (RSTR) {
+        const int row = at / 256, chunk = at % 256 / 16;
+        const int local = (chunk ^ RR::L::strided_key(row)) * (16 / EB);
+        const int col = (local >> 6) * 128 + (local & 63);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) vr[h][j] = col < rs.valid - h * 64 ? (int)(row * rs.pitch) + col * EB : 0x7fffff00;
+      } else {
+        const int local = at / kKBytes, chunk = at % kKBytes / 16;
+        const int row = (local >> 6) * 128 + (local & 63);
+        vr[0][j] = row * (int)rs.pitch + (chunk ^ ((local >> 1) & 7)) * 16;
+      }
+    }
+    const int wn = wave % 4, wm = wave / 4;
+    rc.init(lane, SPLIT ? wn * 32 : wn * 64, [](int f) { return c_index(f); });
+    rr.init(lane, wm * 64, [](int f) { return f * kWide; });
+  }
+
+  template <bool STR>
+  __device__ __forceinline__ void load(const Source &s, int t, int k0, const int (&v)[2], uint32_t at, int j) const {
+    u32x4 d;
+    int soff = 0;
+    if constexpr (STR) {
+      const int64_t left = k_all - (int64_t)t * kSteps - k0;
+      const int64_t rows = left < 0 ? 0 : left < kSteps ? left : kSteps;
+      d = descriptor(s.base + (int64_t)t * kSteps * s.pitch, (uint32_t)(rows * s.pitch));
+    } else {
+      d = descriptor(s.base, (uint32_t)(s.valid * s.pitch));
+      soff = t * kKBytes;
+    }
+    load_lds16(at + j * 1024, v[j], d, soff, true);
+  }
+  // load j (0, 1) of half h of C, of the row quarters 2h, 2h + 1
+  __device__ __forceinline__ void load_c(int t, int h, int j) const {
+    load<CSTR>(c[h], t, CSTR ? h * (kSteps / 2) : 0, vc, to + (t & 1) * Tile256::kStage + h * 16384, j);
+  }
+  __device__ __forceinline__ void load_r(int t, int h, int j) const {
+    load<RSTR>(r[h], t, 0, vr[RSTR ? h : 0], to + (t & 1) * Tile256::kStage + Tile256::kR + h * 16384, j);
+  }
+  __device__ __forceinline__ const lds_u8 *stage_c(int t) const { return lds + (t & 1) * Tile256::kStage; }
+  __device__ __forceinline__ const lds_u8 *stage_r(int t, int q) const {
+    return stage_c(t) + Tile256::kR + (q >> 1) * 16384;
+  }
+  __device__ __forceinline__ bf16x8 read_c(int t, int f, int s) const { return rc.bf16(stage_c(t), f, c_index(f), s); }
+  __device__ __forceinline__ v8i read_c(int t, int f) const { return rc.fp8(stage_c(t), f, c_index(f)); }
+  __device__ __forceinline__ bf16x8 read_r(int t, int q, int s) const {
+    return rr.bf16(stage_r(t, q), q & 1, (q & 1) * 32, s);
+  }
+  __device__ __forceinline__ v8i read_r8(int t, int q, int f) const {
+    return rr.fp8(stage_r(t, q), 0, (q & 1) * 32 + f * 16);
+  }
+
+  // The fetches of quarter q of stage t, j = 0, 1 (`steps` stages in all).
+  // LAST: t may be one of the last two stages.
+  template <bool LAST>
+  __device__ __forceinline__ void fetch(int t, int q, int j, int steps) const {
+    if (q == 0) {
+      if (!LAST || t + 1 < steps) load_r(t + 1, 1, j);
+    } else if (!LAST || t + 2 < steps) {
+      if (q == 1) load_r(t + 2, 0, j);
+      else load_c(t + 2, q - 2, j);
+    }
+  }
+  // Before the loop: stage 0 and, but for its row quarters 2, 3, stage 1;
+  // `extra`: issues EXTRA more loads that go with row quarters 0, 1.
+  template <int EXTRA, class F>
+  __device__ __forceinline__ void begin(int steps, F extra) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (t < steps) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_r(t, 0, j);
+        extra(t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_c(t, j >> 1, j & 1);
+        if (t == 0) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) load_r(0, 1, j);
+        }
+      }
+    }
+    if (steps > 1) wait_stage<8 + EXTRA>();
+    else wait_stage<2>();
+  }
+  // The meetings before quarters 1 and 3: loads that may still be in flight are
+  // those issued after the ones waited for.
+  template <int EXTRA, bool LAST>
+  __device__ __forceinline__ void meet1(int t, int steps) const {
+    if (!LAST || t + 1 < steps) wait_stage<8 + EXTRA>();
+    else wait_stage<0>();
+  }
+  template <int EXTRA, bool LAST>
+  __device__ __forceinline__ void meet3(int t, int steps) const {
+    if (!LAST || t + 2 < steps) wait_stage<6 + EXTRA>();
+    else if (t + 1 < steps) wait_stage<2>();
+  }
 };
 
 // ---------------------------------------------------------------------------
