@@ -101,18 +101,10 @@ __device__ __forceinline__ void product(Acc &acc, const Source &c, const Source 
   }
 }
 
-// The same on the 256 x 256 tile; c_hi: the up rows of a split operand.
-template <bool CSTR, bool RSTR, bool SPLIT, class Acc>
-__device__ __forceinline__ void product256(Acc &acc, const Source &c, const Source &c_hi, const Source &r, int steps,
-                                           int64_t k_all, lds_u8 *lds, int wave, int lane) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
-  if (steps == 0) return;
-  Pipe256<CSTR, RSTR, 2, SPLIT> p;
-  p.init(c, c_hi, r, k_all, lds, wave, lane);
-  p.template begin<0>(steps, [](int) {});
+// The same on the 256 x 256 tile, after p.begin(): its first NQ quarters.
+template <int NQ, bool CSTR, bool RSTR, bool SPLIT, class Acc>
+__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2, SPLIT> &p) {
+  p.template meet0<0>();
   bf16x8 fc[2][4], fr[2][4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -120,36 +112,53 @@ __device__ __forceinline__ void product256(Acc &acc, const Source &c, const Sour
 #pragma unroll
     for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(0, i, s);
   }
+  // LAST: t may be one of the last two stages
   auto step = [&](int t, auto last) {
     constexpr bool kLast = decltype(last)::value;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (q == 1) p.template meet1<0, kLast>(t, steps);
-      if (q == 3) p.template meet3<0, kLast>(t, steps);
-      const bool more = q < 3 || !kLast || t + 1 < steps;
+      if (q == 1) p.template meet1<0, kLast>(t);
+      if (q == 3) p.template meet3<0, kLast>(t);
+      const bool next = !kLast || t + 1 < p.steps;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
+        if (q < NQ) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[i][s], fr[q & 1][s], acc[i][q], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) {
-          fr[(q + 1) & 1][s] = p.read_r(q < 3 ? t : t + 1, (q + 1) & 3, s);
-          if (q == 3) {
-            // this step's column fragments have been used for the last time
-#pragma unroll
-            for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(t + 1, i, s);
-          }
+          for (int i = 0; i < 2; ++i)
+            acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[i][s], fr[q & 1][s], acc[i][q], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (s < 2) p.template fetch<kLast>(t, q, s, steps);
+        if (q + 1 < NQ) fr[(q + 1) & 1][s] = p.read_r(t, q + 1, s);
+        if (q == 3 && next) {
+          // this step's column fragments have been used for the last time
+          fr[0][s] = p.read_r(t + 1, 0, s);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(t + 1, i, s);
+        }
+        if (s < 2) p.template fetch<kLast>(t, q, s);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   int t = 0;
-  for (; t + 2 < steps; ++t) step(t, Flag<false>());
-  for (; t < steps; ++t) step(t, Flag<true>());
+  for (; t + 2 < p.steps; ++t) step(t, Flag<false>());
+  for (; t < p.steps; ++t) step(t, Flag<true>());
+}
+
+// `rows`: valid rows of the tile (each height has a loop of its own: branches
+// between the quarters cost more than the quarters they left out).
+template <bool CSTR, bool RSTR, bool SPLIT, class Acc>
+__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2, SPLIT> &p, int rows) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
+  if (p.steps == 0) return;
+  if (rows > 192) product256<4>(acc, p);
+  else if (rows > 128) product256<3>(acc, p);
+  else if (rows > 64) product256<2>(acc, p);
+  else product256<1>(acc, p);
 }
 
 // Four values of the checkpoint.
@@ -163,101 +172,69 @@ __device__ __forceinline__ void product256(Acc &acc, const Source &c, const Sour
   v[0] = a.x * scale; v[1] = a.y * scale; v[2] = b.x * scale; v[3] = b.y * scale;
 }
 
-template <class S, int MODE>
-__global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
-#ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
-  constexpr bool kSplit = MODE == kUp, kCStr = MODE == kGradX || MODE == kGradAct;
-  constexpr int kCols = kSplit ? S::BN / 2 : S::BN;         // output columns of a tile
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
-  __shared__ Groups g;
-  lds_u8 *lds = (lds_u8 *)smem;
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  const int half = lane >> 5, wn = wave % S::WN, wm = wave / S::WN;
-  scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
-  const int nc = (p.n + kCols - 1) / kCols;
-  const int64_t units = (int64_t)g.first[p.E] * nc;
-  for (int64_t round = 0;; ++round) {
-    const int64_t unit = unit_of_round(round);
-    if (unit >= units) return;                               // uniform; later rounds only have larger units
-    const RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
-    const int64_t row0 = u.row0;
-    const int e = u.e, rows = u.rows, n0 = u.tc * kCols;
-    const Source r{p.r + row0 * p.k * 2, (int64_t)p.k * 2, rows};
-    Source c;
-    if constexpr (kSplit) {
-      const int from = (!S::kDeep && wave >= S::kWaves / 2 ? p.n : 0) + n0;
-      c = Source{p.c + ((int64_t)e * 2 * p.n + from) * p.k * 2, (int64_t)p.k * 2, min(kCols, p.n - n0)};
-    } else if constexpr (kCStr) {
-      c = Source{p.c + ((int64_t)e * p.k * p.n + n0) * 2, (int64_t)p.n * 2, p.n - n0};
-    } else {
-      c = Source{p.c + ((int64_t)e * p.n + n0) * p.k * 2, (int64_t)p.k * 2, min(kCols, p.n - n0)};
+// What becomes of a tile's accumulators.  A wave's fragment (i, j) holds the
+// output columns col(i) + 0..31 and the tile's rows row(j) + 0..31.
+//   cols        output columns of the tile
+//   top         LDS [2][4][rows of a tile]: largest magnitudes (8-bit checkpoint)
+template <int MODE, int RF, int BM, class Acc, class Row>
+__device__ __forceinline__ void epilogue(const RowArgs &p, const RowTile &u, int n0, int wn, int lane, Acc &acc, Row row_of,
+                                         uint32_t *top) {
+  const int half = lane >> 5;
+  if constexpr (MODE == kUp) {
+    const int n = n0 + wn * 32, cols = p.n - n;
+    if (p.ck_form == kCkFp8) {
+#pragma unroll
+      for (int j = 0; j < RF; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t m = row_amax(acc[i][j]);
+          if (half == 0) top[(i * 4 + wn) * BM + row_of(j) + lane] = m;
+        }
+      lds_barrier();
     }
-    v16f acc[S::CF][S::RF];
-    if constexpr (S::kDeep) {
-      const Source c_hi{c.base + (int64_t)p.n * p.k * 2, c.pitch, c.valid};
-      product256<kCStr, false, kSplit>(acc, c, c_hi, r, p.k / 64, p.k, lds, wave, lane);
-    } else {
-      product<S, kCStr, false, kSplit>(acc, c, r, p.k / 64, p.k, lds, wave, lane);
-    }
-    __syncthreads();                                         // the stages are free
-    if constexpr (MODE == kUp) {
-      static_assert(MODE != kUp || S::CF == 2, "one gate and one up fragment a wave");
-      const int n = n0 + wn * 32, cols = p.n - n;
-      uint32_t *top = (uint32_t *)smem;                      // [2][WN][BM] bits of the largest magnitudes
+#pragma unroll
+    for (int j = 0; j < RF; ++j) {
+      const int at = row_of(j) + (lane & 31);
+      const bool ok = at < u.rows && cols > 0;
+      const int64_t row = u.row0 + at;
+      const v16f &gt = acc[0][j], &up = acc[1][j];
+      float a[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i] = act(p.act, gt[i]) * up[i];
+      store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int i) { return a[i]; });
+      if (p.ck_form == kCkBf16) {
+        char *q = p.ck + (row * 2 * p.n + n) * 2;
+        store_bf16(q, half, ok ? cols : 0, [&](int i) { return gt[i]; });
+        store_bf16(q + (int64_t)p.n * 2, half, ok ? cols : 0, [&](int i) { return up[i]; });
+      }
       if (p.ck_form == kCkFp8) {
+        // the whole 128-column block of the checkpoint lies in the tile
 #pragma unroll
-        for (int j = 0; j < S::RF; ++j)
+        for (int i = 0; i < 2; ++i) {
+          uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t m = row_amax(acc[i][j]);
-            if (half == 0) top[(i * S::WN + wn) * S::BM + (wm * S::RF + j) * 32 + lane] = m;
-          }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int j = 0; j < S::RF; ++j) {
-        const int at = (wm * S::RF + j) * 32 + (lane & 31);
-        const bool ok = at < rows && cols > 0;
-        const int64_t row = row0 + at;
-        const v16f &gt = acc[0][j], &up = acc[1][j];
-        float a[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) a[i] = act(p.act, gt[i]) * up[i];
-        store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int i) { return a[i]; });
-        if (p.ck_form == kCkBf16) {
-          char *q = p.ck + (row * 2 * p.n + n) * 2;
-          store_bf16(q, half, ok ? cols : 0, [&](int i) { return gt[i]; });
-          store_bf16(q + (int64_t)p.n * 2, half, ok ? cols : 0, [&](int i) { return up[i]; });
-        }
-        if (p.ck_form == kCkFp8) {
-          // the whole 128-column block of the checkpoint lies in the tile
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int w = 0; w < S::WN; ++w) m = max(m, top[(i * S::WN + w) * S::BM + at]);
-            const Block128 b = block128(EP_QUANT_FP8_B128, m);
-            store_codes(p.ck + row * 2 * p.n + i * p.n + n, half, ok, acc[i][j], b);
-            if (ok && wn == 0 && half == 0) p.ck_scales[row * (2 * p.n / 128) + (i * p.n + n0) / 128] = b.scale;
-          }
+          for (int w = 0; w < 4; ++w) m = max(m, top[(i * 4 + w) * BM + at]);
+          const Block128 b = block128(EP_QUANT_FP8_B128, m);
+          store_codes(p.ck + row * 2 * p.n + i * p.n + n, half, ok, acc[i][j], b);
+          if (ok && wn == 0 && half == 0) p.ck_scales[row * (2 * p.n / 128) + (i * p.n + n0) / 128] = b.scale;
         }
       }
-    } else if constexpr (MODE == kGradAct) {
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < S::CF; ++i) {
-        const int n = n0 + (wn * S::CF + i) * 32, cols = p.n - n;
+    for (int i = 0; i < 2; ++i) {
+      const int n = n0 + (wn * 2 + i) * 32, cols = p.n - n;
 #pragma unroll
-        for (int j = 0; j < S::RF; ++j) {
-          const int at = (wm * S::RF + j) * 32 + (lane & 31);
-          const bool ok = at < rows && cols > 0;
-          const int64_t row = row0 + at;
+      for (int j = 0; j < RF; ++j) {
+        const int at = row_of(j) + (lane & 31);
+        const bool ok = at < u.rows && cols > 0;
+        const int64_t row = u.row0 + at;
+        if constexpr (MODE == kGradAct) {
           float dg[16], du[16], a[16];
           float sg = 0.0f, su = 0.0f;
-          if (p.ck_form == kCkFp8) {
-            if (ok) {
-              sg = p.ck_scales[row * (2 * p.n / 128) + n / 128];
-              su = p.ck_scales[row * (2 * p.n / 128) + (p.n + n) / 128];
-            }
+          if (p.ck_form == kCkFp8 && ok) {
+            sg = p.ck_scales[row * (2 * p.n / 128) + n / 128];
+            su = p.ck_scales[row * (2 * p.n / 128) + (p.n + n) / 128];
           }
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
@@ -286,21 +263,95 @@ __global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
           store_bf16(d, half, ok ? cols : 0, [&](int q) { return dg[q]; });
           store_bf16(d + (int64_t)p.n * 2, half, ok ? cols : 0, [&](int q) { return du[q]; });
           store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int q) { return a[q]; });
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < S::CF; ++i) {
-        const int n = n0 + (wn * S::CF + i) * 32, cols = p.n - n;
-#pragma unroll
-        for (int j = 0; j < S::RF; ++j) {
-          const int at = (wm * S::RF + j) * 32 + (lane & 31);
-          store_bf16(p.out + ((row0 + at) * p.n + n) * 2, half, at < rows ? cols : 0,
-                     [&](int q) { return acc[i][j][q]; });
+        } else {
+          store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int q) { return acc[i][j][q]; });
         }
       }
     }
+  }
+}
+
+// The tile's part of the weights; `up`: of the up rows.
+template <int MODE>
+__device__ __forceinline__ Source weights_of(const RowArgs &p, int e, int n0, bool up, int cols) {
+  if constexpr (MODE == kUp)
+    return Source{p.c + ((int64_t)e * 2 * p.n + (up ? p.n : 0) + n0) * p.k * 2, (int64_t)p.k * 2, min(cols, p.n - n0)};
+  else if constexpr (MODE == kDown)
+    return Source{p.c + ((int64_t)e * p.n + n0) * p.k * 2, (int64_t)p.k * 2, min(cols, p.n - n0)};
+  else
+    return Source{p.c + ((int64_t)e * p.k * p.n + n0) * 2, (int64_t)p.n * 2, p.n - n0};
+}
+
+template <class S, int MODE>
+__global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
+  constexpr bool kSplit = MODE == kUp, kCStr = MODE == kGradX || MODE == kGradAct;
+  constexpr int kCols = kSplit ? S::BN / 2 : S::BN;         // output columns of a tile
+  static_assert(S::CF == 2 && S::WN == 4, "the epilogue's columns");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
+  __shared__ Groups g;
+  lds_u8 *lds = (lds_u8 *)smem;
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
+  const int wn = wave % S::WN, wm = wave / S::WN;
+  scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
+  const int nc = (p.n + kCols - 1) / kCols;
+  const int units = g.first[p.E] * nc;
+  for (int round = 0;; ++round) {
+    const int unit = unit_of_round(round);
+    if (unit >= units) return;                               // uniform; later rounds only have larger units
+    const RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
+    const int n0 = u.tc * kCols;
+    const Source r{p.r + u.row0 * p.k * 2, (int64_t)p.k * 2, u.rows};
+    const Source c = weights_of<MODE>(p, u.e, n0, kSplit && wave >= S::kWaves / 2, kCols);
+    v16f acc[S::CF][S::RF];
+    product<S, kCStr, false, kSplit>(acc, c, r, p.k / 64, p.k, lds, wave, lane);
+    __syncthreads();                                         // the stages are free
+    epilogue<MODE, S::RF, S::BM>(p, u, n0, wn, lane, acc, [&](int j) { return (wm * S::RF + j) * 32; },
+                                 (uint32_t *)smem);
     __syncthreads();                                         // before the next unit's stages
+  }
+#endif
+}
+
+// The same on 256 x 256 tiles: the next unit's first stages are fetched before
+// the epilogue of a unit.
+template <int MODE>
+__global__ __launch_bounds__(Tile256::kThreads) void rows256_kernel(RowArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef Tile256 S;
+  constexpr bool kSplit = MODE == kUp, kCStr = MODE == kGradX || MODE == kGradAct;
+  constexpr int kCols = kSplit ? S::BN / 2 : S::BN;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
+  __shared__ uint32_t top[MODE == kUp ? 2 * 4 * S::BM : 1];
+  __shared__ Groups g;
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
+  const int nc = (p.n + kCols - 1) / kCols;
+  scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
+  const Plan256 plan = plan_units(uniform(g.first[p.E]), nc);
+  const int units = plan.units;
+  Pipe256<kCStr, false, 2, kSplit> pipe;
+  RowTile u;
+  int n0;
+  auto start = [&](int unit) {
+    u = row_tile256(g, plan, p.E, p.offsets, unit, nc);
+    n0 = u.tc * kCols;
+    pipe.init(weights_of<MODE>(p, u.e, n0, false, kCols), weights_of<MODE>(p, u.e, n0, true, kCols),
+              Source{p.r + u.row0 * p.k * 2, (int64_t)p.k * 2, u.rows}, p.k, (lds_u8 *)smem, wave, lane);
+    pipe.begin([](int) {});
+  };
+  int unit = unit_of_round(0);
+  if (unit >= units) return;
+  start(unit);
+  for (int round = 1;; ++round) {
+    v16f acc[2][4];
+    product256(acc, pipe, u.rows);
+    lds_barrier();                                           // the stages are free
+    const RowTile done = u;
+    const int done_n0 = n0;
+    unit = unit_of_round(round);
+    if (unit < units) start(unit);
+    epilogue<MODE, 4, S::BM>(p, done, done_n0, S::wn(wave), lane, acc, [&](int j) { return S::row(wave, j, 0); }, top);
+    if (unit >= units) return;
   }
 #endif
 }
@@ -309,56 +360,83 @@ struct WeightArgs {
   const int *offsets;
   const int64_t *recv_count;
   int E;
-  const char *r, *c;       // [rows, nr] and [rows, nc] bf16
-  int nr, nc;
-  char *out;               // [E, nr, nc] bf16
+  struct {
+    const char *r, *c;     // [rows, nr] and [rows, nc] bf16
+    int nr, nc;
+    char *out;             // [E, nr, nc] bf16
+  } of[2];
 };
 
-// out[e] = R_e^T C_e over the rows of expert e (zeros without rows).
-template <class S>
-__global__ __launch_bounds__(S::kThreads) void weights_kernel(WeightArgs p) {
-#ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
+// out[e] = R_e^T C_e over the rows of expert e (zeros without rows), for both
+// weights in one launch: fewer units left over, and the last units, where
+// they would fill less than half of a round, are cut into 2 or 4 pieces.
+__global__ __launch_bounds__(Tile256::kThreads) void weights256_kernel(WeightArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef Tile256 S;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
   __shared__ Groups g;
-  lds_u8 *lds = (lds_u8 *)smem;
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  const int half = lane >> 5, wn = wave % S::WN, wm = wave / S::WN;
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
+  const int half = lane >> 5, wn = S::wn(wave);
   order_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count);
-  const int tr_all = (p.nr + S::BM - 1) / S::BM, tc_all = (p.nc + S::BN - 1) / S::BN;
-  const int64_t per = (int64_t)tr_all * tc_all, units = per * p.E;
-  for (int64_t round = 0;; ++round) {
-    const int64_t unit = unit_of_round(round);
-    if (unit >= units) return;
-    const int place = (int)(unit / per);
-    const int e = __builtin_amdgcn_readfirstlane(g.order[place]);
-    const int rows = __builtin_amdgcn_readfirstlane(g.rows[e]);
+  auto tiles = [](int n) { return (n + 255) / 256; };
+  const int per0 = tiles(p.of[0].nr) * tiles(p.of[0].nc), per = per0 + tiles(p.of[1].nr) * tiles(p.of[1].nc);
+  const int grid = (int)gridDim.x, all = per * p.E, over = all % grid;
+  const int parts = over * 4 <= grid ? 4 : over * 2 <= grid ? 2 : 1;
+  const int whole = all - over, units = whole + over * parts;
+  Pipe256<true, true, 2, false> pipe;
+  int e, r0, c0, rows_out, which, nr, nc;
+  auto start = [&](int unit) {
+    int piece = 0, height = 256;
+    if (unit >= whole) {
+      piece = (unit - whole) % parts;
+      unit = whole + (unit - whole) / parts;
+      height = 256 / parts;
+    }
+    const int place = unit / per;
+    e = uniform(g.order[place]);
+    const int rows = uniform(g.rows[e]);
+    int local = unit - place * per;
+    which = uniform((int)(local >= per0));
+    if (which) local -= per0;
+    nr = uniform(which ? p.of[1].nr : p.of[0].nr);
+    nc = uniform(which ? p.of[1].nc : p.of[0].nc);
     int tr, tc;
-    tile_of_unit(unit - place * per, tr_all, tc_all, tr, tc);
-    tr = __builtin_amdgcn_readfirstlane(tr);
-    tc = __builtin_amdgcn_readfirstlane(tc);
-    const int r0 = tr * S::BM, c0 = tc * S::BN;
+    tile_of_unit(local, tiles(nr), tiles(nc), tr, tc);
+    r0 = uniform(tr * 256 + piece * height);
+    c0 = uniform(tc * 256);
+    rows_out = uniform(max(min(height, nr - r0), 0));
     const int64_t row0 = p.offsets[e];
-    const Source r{p.r + (row0 * p.nr + r0) * 2, (int64_t)p.nr * 2, p.nr - r0};
-    const Source c{p.c + (row0 * p.nc + c0) * 2, (int64_t)p.nc * 2, p.nc - c0};
-    v16f acc[S::CF][S::RF];
-    product256<true, true, false>(acc, c, c, r, (rows + 63) / 64, rows, lds, wave, lane);
+    const char *rb = which ? p.of[1].r : p.of[0].r, *cb = which ? p.of[1].c : p.of[0].c;
+    const Source c{cb + uniform((row0 * nc + c0) * 2), (int64_t)nc * 2, nc - c0};
+    pipe.init(c, c, Source{rb + uniform((row0 * nr + r0) * 2), (int64_t)nr * 2, rows_out}, rows, (lds_u8 *)smem, wave, lane);
+    pipe.begin([](int) {});
+  };
+  int unit = unit_of_round(0);
+  if (unit >= units) return;
+  start(unit);
+  for (int round = 1;; ++round) {
+    v16f acc[2][4];
+    product256(acc, pipe, rows_out);
+    lds_barrier();
+    const int done_nc = nc, done_c0 = c0, done_rows = rows_out;
+    char *out = (which ? p.of[1].out : p.of[0].out) + ((int64_t)e * nr + r0) * nc * 2;
+    unit = unit_of_round(round);
+    if (unit < units) start(unit);
 #pragma unroll
-    for (int i = 0; i < S::CF; ++i) {
-      const int n = c0 + (wn * S::CF + i) * 32, cols = p.nc - n;
+    for (int i = 0; i < 2; ++i) {
+      const int n = done_c0 + (wn * 2 + i) * 32, cols = done_nc - n;
 #pragma unroll
-      for (int j = 0; j < S::RF; ++j) {
-        const int at = r0 + (wm * S::RF + j) * 32 + (lane & 31);
-        store_bf16(p.out + (((int64_t)e * p.nr + at) * p.nc + n) * 2, half, at < p.nr ? cols : 0,
-                   [&](int q) { return acc[i][j][q]; });
+      for (int j = 0; j < 4; ++j) {
+        const int at = S::row(wave, j, lane & 31);
+        store_bf16(out + ((int64_t)at * done_nc + n) * 2, half, at < done_rows ? cols : 0, [&](int q) { return acc[i][j][q]; });
       }
     }
-    __syncthreads();
+    if (unit >= units) return;
   }
 #endif
 }
 
-typedef Shape<2, 4, 4, 2, 2> Large;      // 256 rows x 256 columns
-typedef Shape<2, 2, 4, 2, 3> Medium;     // 128 rows
+typedef Shape<2, 2, 4, 2, 3> Medium;     // 128 rows x 256 columns
 typedef Shape<2, 1, 4, 2, 3> Small;      // 64 rows
 typedef Shape<2, 1, 4, 1, 4> Tiny;       // 32 rows
 
@@ -366,8 +444,10 @@ template <class S, int MODE>
 hipError_t rows_launch(const RowArgs &p, int64_t pairs, hipStream_t s) {
   const int cols = MODE == kUp ? S::BN / 2 : S::BN;
   const int64_t tiles = (pairs + S::BM - 1) / S::BM + (p.E < pairs ? p.E : pairs);
-  const int64_t units = tiles * ((p.n + cols - 1) / cols);
-  hipLaunchKernelGGL((rows_kernel<S, MODE>), dim3((unsigned)persistent_grid(units)), dim3(S::kThreads), 0, s, p);
+  const int64_t units = tiles * ((p.n + cols - 1) / cols) * (S::BM == 256 ? 4 : 1);   // tiles may be cut
+  const dim3 grid((unsigned)persistent_grid(units)), block(S::kThreads);
+  if constexpr (S::BM == 256) hipLaunchKernelGGL(rows256_kernel<MODE>, grid, block, 0, s, p);
+  else hipLaunchKernelGGL((rows_kernel<S, MODE>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -377,7 +457,7 @@ hipError_t rows_shape(const RowArgs &p, int64_t pairs, hipStream_t s) {
   if (mean <= 32) return rows_launch<Tiny, MODE>(p, pairs, s);
   if (mean <= 64) return rows_launch<Small, MODE>(p, pairs, s);
   if (mean <= 192) return rows_launch<Medium, MODE>(p, pairs, s);
-  return rows_launch<Large, MODE>(p, pairs, s);
+  return rows_launch<Tile256, MODE>(p, pairs, s);
 }
 
 RowArgs row_args(const FfnArgs &f, const void *r, const void *c, int k, int n, void *out) {
@@ -394,11 +474,11 @@ int64_t pairs_of(const ep_handle_t &h) {
   return n < h.max_rows ? n : h.max_rows;
 }
 
-hipError_t weights_launch(const FfnArgs &f, const void *r, int nr, const void *c, int nc, void *out, hipStream_t s) {
-  const WeightArgs p{f.h.offsets, f.recv_count, f.h.num_experts, (const char *)r, (const char *)c, nr, nc, (char *)out};
-  typedef Large S;
-  const int64_t units = (int64_t)((nr + S::BM - 1) / S::BM) * ((nc + S::BN - 1) / S::BN) * p.E;
-  hipLaunchKernelGGL((weights_kernel<S>), dim3((unsigned)persistent_grid(units)), dim3(S::kThreads), 0, s, p);
+hipError_t weights_launch(const WeightArgs &p, hipStream_t s) {
+  typedef Tile256 S;
+  int64_t tiles = 0;
+  for (const auto &o : p.of) tiles += (int64_t)((o.nr + 255) / 256) * ((o.nc + 255) / 256);
+  hipLaunchKernelGGL(weights256_kernel, dim3((unsigned)persistent_grid(tiles * 4 * p.E)), dim3(S::kThreads), 0, s, p);
   return hipGetLastError();
 }
 
@@ -427,8 +507,10 @@ hipError_t launch_ffn_backward(const FfnGradArgs &g, hipStream_t s) {
         hipSuccess)
       return e;
   }
-  if ((e = weights_launch(f, d, 2 * f.inter, f.x, f.hidden, g.grad_w1, s)) != hipSuccess) return e;
-  return weights_launch(f, g.grad_out, f.hidden, a, f.inter, g.grad_w2, s);
+  return weights_launch({f.h.offsets, f.recv_count, f.h.num_experts,
+                         {{d, (const char *)f.x, 2 * f.inter, f.hidden, (char *)g.grad_w1},
+                          {(const char *)g.grad_out, a, f.hidden, f.inter, (char *)g.grad_w2}}},
+                        s);
 }
 
 }  // namespace ep

@@ -46,6 +46,12 @@ struct Flag {
 constexpr int kXcds = 8;
 constexpr int kKBytes = 128;              // bytes of k in a stage
 
+// A value that is the same in every lane, kept in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
+}
+
 // ---------------------------------------------------------------------------
 // which tile a workgroup computes
 // ---------------------------------------------------------------------------
@@ -121,18 +127,16 @@ __device__ __forceinline__ void order_rows(Groups &g, int E, const int *__restri
 
 // Workgroup b runs on XCD b % 8 (the hardware deals them out in turn); in
 // each round an XCD takes consecutive units, which share operands in its L2.
-__device__ __forceinline__ int64_t unit_of_round(int64_t round) {
+__device__ __forceinline__ int unit_of_round(int round) {
   const int slots = (int)gridDim.x / kXcds;
-  return (round * kXcds + blockIdx.x % kXcds) * slots + blockIdx.x / kXcds;
+  return (round * kXcds + (int)blockIdx.x % kXcds) * slots + (int)blockIdx.x / kXcds;
 }
 
-// Units of one group of nr x nc tiles, up to kGroupRows row tiles deep: the
-// units in flight on an XCD form a compact rectangle.
+// Units of nr x nc tiles in groups kGroupRows row tiles deep: the units in
+// flight on an XCD form a compact rectangle.
 constexpr int kGroupRows = 8;
-__device__ __forceinline__ void tile_of_unit(int64_t local, int nr, int nc, int &tr, int &tc) {
-  const int64_t per = (int64_t)kGroupRows * nc;
-  const int g = (int)(local / per);
-  const int rem = (int)(local - g * per);
+__device__ __forceinline__ void tile_of_unit(int local, int nr, int nc, int &tr, int &tc) {
+  const int per = kGroupRows * nc, g = local / per, rem = local - g * per;
   const int depth = min(kGroupRows, nr - g * kGroupRows);
   tc = rem / depth;
   tr = g * kGroupRows + rem - tc * depth;
@@ -143,9 +147,9 @@ struct RowTile {
   int e, rows, tc;
   int64_t row0;
 };
-__device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *__restrict__ offsets, int64_t unit,
+__device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *__restrict__ offsets, int unit,
                                             int nc, int bm) {
-  const int item = (int)(unit / nc);
+  const int item = unit / nc;
   int lo = 0, hi = E;                                        // the last expert whose first tile is <= item
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -155,7 +159,7 @@ __device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *_
   u.e = __builtin_amdgcn_readfirstlane(lo);
   const int rows = __builtin_amdgcn_readfirstlane(g.rows[u.e]);
   int tr;
-  tile_of_unit(unit - (int64_t)g.first[u.e] * nc, (rows + bm - 1) / bm, nc, tr, u.tc);
+  tile_of_unit(unit - g.first[u.e] * nc, (rows + bm - 1) / bm, nc, tr, u.tc);
   tr = __builtin_amdgcn_readfirstlane(tr);
   u.tc = __builtin_amdgcn_readfirstlane(u.tc);
   u.row0 = (int64_t)offsets[u.e] + (int64_t)tr * bm;
@@ -353,6 +357,11 @@ __device__ __forceinline__ void wait_waves() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+// A barrier that orders LDS accesses alone: loads in flight stay there.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wait_waves();
+}
 template <int N>
 __device__ __forceinline__ void wait_stage() {
   wait_loads<N>();
@@ -368,19 +377,18 @@ struct Shape {
   static constexpr int BN = 32 * CF * WN, BM = 32 * RF * WM;
   static constexpr int kStage = (BN + BM) * kKBytes;
   static constexpr int kLds = kStage * kStages;
-  static constexpr bool kDeep = BN == 256 && BM == 256;  // runs on Pipe256
 };
 
 // ---------------------------------------------------------------------------
 // the 256 x 256 tile
 // ---------------------------------------------------------------------------
 //
-// Eight waves (4 along the columns, 2 along the rows) of 64 columns x 128 rows,
-// two stages of 64 KB.  A stage is worked through in quarters of 32 of a
-// wave's rows (8 matrix instructions of bf16, 8 of e4m3); the column
-// fragments of the whole stage stay in registers.  A part of a stage is
-// fetched again (for two stages on) as soon as every wave has read it, a
-// quarter of the bytes in every quarter:
+// Eight waves: 4 along the columns, 2 along the rows, two stages of 64 KB.  A
+// stage is worked through in quarters of 64 rows (32 a wave; 8 matrix
+// instructions of bf16, 8 of e4m3); a wave's column fragments of the whole
+// stage stay in registers.  A part of a stage is fetched again (for two
+// stages on) as soon as every wave has read it, a quarter of the bytes in
+// every quarter:
 //   quarter    fetched                         the waves meet first, so that
 //   0          row quarters 2, 3 of stage t+1
 //   1          row quarters 0, 1 of stage t+2  (row quarters 2, 3 of t are there)
@@ -390,12 +398,72 @@ struct Shape {
 // and never queues more than two a wave: issued in one burst, the 64 loads of
 // a stage held every wave's next instruction back for about 1000 cycles.
 // Fragments are read a quarter ahead, between the matrix instructions.
-// In LDS the rows of quarters 0, 1 (of both row halves) come first.
 struct Tile256 {
   static constexpr int BN = 256, BM = 256, kThreads = 512, WN = 4, WM = 2;
   static constexpr int kStage = 512 * kKBytes, kLds = 2 * kStage;
   static constexpr int kR = 256 * kKBytes;               // the row part of a stage
+  static __device__ __forceinline__ int wn(int wave) { return wave >> 1; }
+  static __device__ __forceinline__ int wm(int wave) { return wave & 1; }
+  // row of the tile of row `i` (0..31) of a wave's quarter q
+  static __device__ __forceinline__ int row(int wave, int q, int i) { return q * 64 + wm(wave) * 32 + i; }
 };
+
+// The units of a launch on 256-row tiles.  Every workgroup takes every
+// gridDim-th unit, so a round of units takes as long as its slowest.  Where
+// the units past whole rounds would fill at most half of the last one, the
+// row tiles they belong to, the launch's last, are cut into 2 or 4 equal
+// pieces (352 units of 4096-long sums on 256 CUs: 232 -> 205 us).
+// Working off the experts' short last tiles together at the end, by height,
+// evens out the rounds too, but reads every expert's weights a second time
+// (measured: no faster).
+struct Plan256 {
+  int whole, parts, units;                // row tiles not cut; pieces of each other one
+};
+__device__ __forceinline__ Plan256 plan_units(int tiles, int nc) {
+  const int grid = (int)gridDim.x, over = tiles * nc % grid;
+  Plan256 p{tiles, 1, tiles * nc};
+  if (over * 2 <= grid) {
+    const int cut = (over + nc - 1) / nc;
+    p.parts = over * 4 <= grid ? 4 : 2;
+    p.whole = tiles - cut;
+    p.units = (p.whole + cut * p.parts) * nc;
+  }
+  return p;
+}
+
+// The rows and column tile of a unit (uniform; rows may be 0).
+__device__ __forceinline__ RowTile row_tile256(const Groups &g, const Plan256 &p, int E,
+                                               const int *__restrict__ offsets, int unit, int nc) {
+  int item = unit / nc, piece = -1;
+  const int col = unit - item * nc;
+  if (item >= p.whole) {
+    const int past = item - p.whole;
+    item = p.whole + past / p.parts;
+    piece = past % p.parts;
+  }
+  int lo = 0, hi = E;                                        // the last expert whose first tile is <= item
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (g.first[mid] <= item) lo = mid; else hi = mid;
+  }
+  RowTile u;
+  u.e = uniform(lo);
+  const int first = uniform(g.first[u.e]), rows = uniform(g.rows[u.e]);
+  int tr = item - first, height = 256, at = 0;
+  u.tc = col;
+  if (piece >= 0) {
+    height = 256 / p.parts;
+    at = piece * height;
+  } else {
+    tile_of_unit(unit - first * nc, min((rows + 255) / 256, p.whole - first), nc, tr, u.tc);
+  }
+  tr = uniform(tr);
+  u.tc = uniform(u.tc);
+  at = uniform(at);
+  u.row0 = (int64_t)offsets[u.e] + (int64_t)tr * 256 + at;
+  u.rows = uniform(max(min(height, rows - tr * 256 - at), 0));
+  return u;
+}
 
 template <bool CSTR, bool RSTR, int EB, bool SPLIT>
 struct Pipe256 {
@@ -407,6 +475,7 @@ struct Pipe256 {
   typedef Reader<RSTR ? 128 : 256, RSTR, EB, 2> RR;
   Source c[2], r[2];                                      // halves of C; row quarters 0, 1 and 2, 3
   int64_t k_all;
+  int steps;
   lds_u8 *lds;
   uint32_t to;                                            // the wave's place in a half
   int vc[2], vr[RSTR ? 2 : 1][2];
@@ -418,10 +487,12 @@ struct Pipe256 {
     else return SPLIT ? f / 2 * 128 + f % 2 * 16 : f * 16;
   }
 
-  // c_hi: the second half's source of a split operand (else unused)
+  // c_hi: the second half's source of a split operand (else unused); k: the
+  // reduction's length
   __device__ __forceinline__ void init(const Source &cs, const Source &c_hi, const Source &rs, int64_t k, lds_u8 *l,
                                        int wave, int lane) {
     k_all = k;
+    steps = (int)((k + kSteps - 1) / kSteps);
     lds = l;
     to = (uint32_t)(uintptr_t)l + wave * 2048;
     c[0] = cs;
@@ -429,7 +500,7 @@ struct Pipe256 {
     else if constexpr (CSTR) c[1] = Source{cs.base + kSteps / 2 * cs.pitch, cs.pitch, cs.valid};
     else c[1] = Source{cs.base + 128 * cs.pitch, cs.pitch, max(cs.valid - 128, 0)};
     r[0] = rs;
-    r[1] = Source{rs.base + (RSTR ? 64 * EB : 64 * rs.pitch), rs.pitch, max(rs.valid - 64, 0)};
+    r[1] = Source{rs.base + (RSTR ? 128 * EB : 128 * rs.pitch), rs.pitch, max(rs.valid - 128, 0)};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int at = (wave * 2 + j) * 1024 + lane * 16;     // in a half
@@ -443,19 +514,18 @@ struct Pipe256 {
       }
       if constexpr (RSTR) {
         const int row = at / 256, chunk = at % 256 / 16;
-        const int local = (chunk ^ RR::L::strided_key(row)) * (16 / EB);
-        const int col = (local >> 6) * 128 + (local & 63);
+        const int col = (chunk ^ RR::L::strided_key(row)) * (16 / EB);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) vr[h][j] = col < rs.valid - h * 64 ? (int)(row * rs.pitch) + col * EB : 0x7fffff00;
+        for (int h = 0; h < 2; ++h)
+          vr[h][j] = col < rs.valid - h * 128 ? (int)(row * rs.pitch) + col * EB : 0x7fffff00;
       } else {
-        const int local = at / kKBytes, chunk = at % kKBytes / 16;
-        const int row = (local >> 6) * 128 + (local & 63);
-        vr[0][j] = row * (int)rs.pitch + (chunk ^ ((local >> 1) & 7)) * 16;
+        const int row = at / kKBytes, chunk = at % kKBytes / 16;
+        vr[0][j] = row * (int)rs.pitch + (chunk ^ ((row >> 1) & 7)) * 16;
       }
     }
-    const int wn = wave % 4, wm = wave / 4;
+    const int wn = Tile256::wn(wave), wm = Tile256::wm(wave);
     rc.init(lane, SPLIT ? wn * 32 : wn * 64, [](int f) { return c_index(f); });
-    rr.init(lane, wm * 64, [](int f) { return f * kWide; });
+    rr.init(lane, wm * 32, [](int f) { return RSTR ? f * 64 : f * kWide; });
   }
 
   template <bool STR>
@@ -486,16 +556,16 @@ struct Pipe256 {
   __device__ __forceinline__ bf16x8 read_c(int t, int f, int s) const { return rc.bf16(stage_c(t), f, c_index(f), s); }
   __device__ __forceinline__ v8i read_c(int t, int f) const { return rc.fp8(stage_c(t), f, c_index(f)); }
   __device__ __forceinline__ bf16x8 read_r(int t, int q, int s) const {
-    return rr.bf16(stage_r(t, q), q & 1, (q & 1) * 32, s);
+    return rr.bf16(stage_r(t, q), q & 1, (q & 1) * 64, s);
   }
   __device__ __forceinline__ v8i read_r8(int t, int q, int f) const {
-    return rr.fp8(stage_r(t, q), 0, (q & 1) * 32 + f * 16);
+    return rr.fp8(stage_r(t, q), 0, (q & 1) * 64 + f * 16);
   }
 
-  // The fetches of quarter q of stage t, j = 0, 1 (`steps` stages in all).
+  // The fetches of quarter q of stage t, j = 0, 1.
   // LAST: t may be one of the last two stages.
   template <bool LAST>
-  __device__ __forceinline__ void fetch(int t, int q, int j, int steps) const {
+  __device__ __forceinline__ void fetch(int t, int q, int j) const {
     if (q == 0) {
       if (!LAST || t + 1 < steps) load_r(t + 1, 1, j);
     } else if (!LAST || t + 2 < steps) {
@@ -505,8 +575,8 @@ struct Pipe256 {
   }
   // Before the loop: stage 0 and, but for its row quarters 2, 3, stage 1;
   // `extra`: issues EXTRA more loads that go with row quarters 0, 1.
-  template <int EXTRA, class F>
-  __device__ __forceinline__ void begin(int steps, F extra) const {
+  template <class F>
+  __device__ __forceinline__ void begin(F extra) const {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (t < steps) {
@@ -521,18 +591,21 @@ struct Pipe256 {
         }
       }
     }
+  }
+  template <int EXTRA>
+  __device__ __forceinline__ void meet0() const {
     if (steps > 1) wait_stage<8 + EXTRA>();
     else wait_stage<2>();
   }
   // The meetings before quarters 1 and 3: loads that may still be in flight are
   // those issued after the ones waited for.
   template <int EXTRA, bool LAST>
-  __device__ __forceinline__ void meet1(int t, int steps) const {
+  __device__ __forceinline__ void meet1(int t) const {
     if (!LAST || t + 1 < steps) wait_stage<8 + EXTRA>();
     else wait_stage<0>();
   }
   template <int EXTRA, bool LAST>
-  __device__ __forceinline__ void meet3(int t, int steps) const {
+  __device__ __forceinline__ void meet3(int t) const {
     if (!LAST || t + 2 < steps) wait_stage<6 + EXTRA>();
     else if (t + 1 < steps) wait_stage<2>();
   }

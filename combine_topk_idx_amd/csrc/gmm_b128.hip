@@ -146,9 +146,9 @@ __global__ __launch_bounds__(S::kThreads) void gmm_kernel(GmmArgs p) {
   const int wn = wave % S::WN, wm = wave / S::WN;
   scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
   const int nc = (p.n + kCols - 1) / kCols;
-  const int64_t units = (int64_t)g.first[p.E] * nc;
-  for (int64_t round = 0;; ++round) {
-    const int64_t unit = unit_of_round(round);
+  const int units = g.first[p.E] * nc;
+  for (int round = 0;; ++round) {
+    const int unit = unit_of_round(round);
     if (unit >= units) return;
     RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
     const int n0 = u.tc * kCols;
