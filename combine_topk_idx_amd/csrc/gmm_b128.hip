@@ -133,16 +133,163 @@ __device__ __forceinline__ void product(Acc &acc, const GmmArgs &p, const Source
   }
 }
 
+// The same on the 256 x 256 tile, after p.begin(): its first NQ quarters.
+// A pair of matrix instructions is scaled and added while the next pair runs.
+//   sw, step, up   the weight scales of the wave's columns by block of k, and of
+//                  the up columns
+template <int NQ, bool CSTR, bool SPLIT, bool BYTES, class Acc, class Fetch>
+__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, false, 1, SPLIT> &p, const lds_u8 *area, int wm,
+                                           int lane, const_floats sw, int64_t step_w, int64_t up, Fetch fetch_scales) {
+  auto row_scale = [&](int t, int q, int f) {
+    const uint32_t v = *(const __attribute__((address_space(3))) uint32_t *)(
+        area + (t & 3) * 1024 + (q * 64 + wm * 32 + f * 16 + (lane & 15)) * 4);
+    return BYTES ? e8m0_decode(v) : __uint_as_float(v);
+  };
+  p.template meet0<1>();
+  v8i fc[4], fr[2][2];
+  float sr[2][2], coef[2][2];
+  v4f part[2][2];
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    fr[0][f] = p.read_r8(0, 0, f);
+    sr[0][f] = row_scale(0, 0, f);
+    part[1][f] = v4f{};
+    coef[1][f] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) fc[i] = p.read_c(0, i);
+  float w[2] = {sw[0], SPLIT ? sw[up] : 0.0f};
+  auto add = [&](int q, int i, int from) {                   // the pair (q, i)
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      v4f &a = acc[i][2 * q + f];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[x] = __builtin_fmaf(part[from][f][x], coef[from][f], a[x]);
+      a = pin(a);                                            // here, not after the loop's branches
+    }
+  };
+  auto step = [&](int t, auto last) {
+    constexpr bool kLast = decltype(last)::value;
+    const int next_t = kLast ? min(t + 1, p.steps - 1) : t + 1;
+    const float wn[2] = {sw[next_t * step_w], SPLIT ? sw[next_t * step_w + up] : 0.0f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q == 1) p.template meet1<1, kLast>(t);
+      if (q == 3) p.template meet3<1, kLast>(t);
+      const bool next = !kLast || t + 1 < p.steps;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (q < NQ) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            part[i & 1][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fc[i], fr[q & 1][f], v4f{}, 0, 0, 0, 0, 0, 0);
+            coef[i & 1][f] = sr[q & 1][f] * w[SPLIT ? i >> 1 : 0];
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (i > 0) add(q, i - 1, (i & 1) ^ 1);
+          else if (q > 0) add(q - 1, 3, 1);
+          else add(NQ - 1, 3, 1);                            // of the stage before (zeros before the first)
+        }
+        if (i < 2) {
+          if (q + 1 < NQ) {
+            fr[(q + 1) & 1][i] = p.read_r8(t, q + 1, i);
+            sr[(q + 1) & 1][i] = row_scale(t, q + 1, i);
+          } else if (q == 3 && next) {
+            fr[0][i] = p.read_r8(t + 1, 0, i);
+            sr[0][i] = row_scale(t + 1, 0, i);
+          }
+          p.template fetch<kLast>(t, q, i);
+        } else if (i == 2 && q == 1 && (!kLast || t + 2 < p.steps)) {
+          fetch_scales(t + 2);
+        }
+        // this stage's column fragment has been used for the last time
+        if (q == 3 && next) fc[i] = p.read_c(t + 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    w[0] = wn[0];
+    w[1] = wn[1];
+  };
+  int t = 0;
+  for (; t + 2 < p.steps; ++t) step(t, Flag<false>());
+  for (; t < p.steps; ++t) step(t, Flag<true>());
+  add(NQ - 1, 3, 1);
+}
+
+// Fragments (i, j) of a wave: columns col + 16 i .. (gated: gate, then up), the
+// tile's rows row_of(j) + 0..15.
+template <bool GATED, int RF, int BM, class Acc, class Row>
+__device__ __forceinline__ void epilogue(const GmmArgs &p, const RowTile &u, int n0, int wn, int lane, Acc &acc, Row row_of,
+                                         uint32_t *top) {
+  if constexpr (!GATED) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const int n = n0 + (wn * 4 + i) * 16, cols = p.n - n;
+#pragma unroll
+      for (int j = 0; j < RF; ++j) {
+        const int at = row_of(j) + (lane & 15);
+        store_bf16_pair(p.out + ((u.row0 + at) * p.n + n) * 2, lane, at < u.rows ? cols : 0, acc[i][j], acc[i + 1][j]);
+      }
+    }
+  } else {
+    const int n = n0 + wn * 32;                              // n is a multiple of 128: the tile lies inside
+#pragma unroll
+    for (int j = 0; j < RF; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = act(p.act, acc[i][j][q]) * acc[2 + i][j][q];
+      if (p.out_quant != EP_QUANT_NONE) {
+        const uint32_t m = row_amax(acc[0][j], acc[1][j]);
+        if (lane < 16) top[wn * BM + row_of(j) + lane] = m;
+      }
+    }
+    if (p.out_quant != EP_QUANT_NONE) lds_barrier();
+#pragma unroll
+    for (int j = 0; j < RF; ++j) {
+      const int at = row_of(j) + (lane & 15);
+      const int64_t row = u.row0 + at;
+      const bool ok = at < u.rows;
+      if (p.out_quant == EP_QUANT_NONE) {
+        store_bf16_pair(p.out + (row * p.n + n) * 2, lane, ok ? 32 : 0, acc[0][j], acc[1][j]);
+      } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max(m, top[w * BM + at]);
+        const Block128 b = block128(p.out_quant, m);
+        store_codes_pair(p.out + row * p.n + n, lane, ok, acc[0][j], acc[1][j], b);
+        if (ok && wn == 0 && lane < 16) {
+          const int64_t to = row * (p.n / 128) + n0 / 128;
+          if (p.out_quant == EP_QUANT_FP8_B128_UE8M0) ((uint8_t *)p.out_scales)[to] = (uint8_t)b.byte;
+          else ((float *)p.out_scales)[to] = b.scale;
+        }
+      }
+    }
+  }
+}
+
+// The tile's part of the weights; `up`: of the up rows.
+template <bool CSTR, bool GATED>
+__device__ __forceinline__ Source weights_of(const GmmArgs &p, int e, int n0, bool up, int cols) {
+  if constexpr (GATED)
+    return Source{p.c + ((int64_t)e * 2 * p.n + (up ? p.n : 0) + n0) * p.k, p.k, min(cols, p.n - n0)};
+  else if constexpr (CSTR)
+    return Source{p.c + (int64_t)e * p.k * p.n + n0, p.n, p.n - n0};
+  else
+    return Source{p.c + ((int64_t)e * p.n + n0) * p.k, p.k, min(cols, p.n - n0)};
+}
+
 // GATED: gate and up rows in, n columns act(gate) * up out
 template <class S, bool CSTR, bool GATED, bool BYTES>
 __global__ __launch_bounds__(S::kThreads) void gmm_kernel(GmmArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
-  constexpr bool kSplit = GATED;
-  constexpr int kCols = kSplit ? S::BN / 2 : S::BN;
+  constexpr int kCols = GATED ? S::BN / 2 : S::BN;
+  static_assert(S::CF == 2 && S::WN == 4, "the epilogue's columns");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + S::kStages * ScaleArea<S>::kBytes];
   __shared__ Groups g;
   lds_u8 *lds = (lds_u8 *)smem;
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
   const int wn = wave % S::WN, wm = wave / S::WN;
   scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
   const int nc = (p.n + kCols - 1) / kCols;
@@ -150,75 +297,83 @@ __global__ __launch_bounds__(S::kThreads) void gmm_kernel(GmmArgs p) {
   for (int round = 0;; ++round) {
     const int unit = unit_of_round(round);
     if (unit >= units) return;
-    RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
+    const RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
     const int n0 = u.tc * kCols;
     const Source r{p.r + u.row0 * p.k, p.k, u.rows};
-    Source c;
-    if constexpr (kSplit) {
-      const int from = (wave >= S::kWaves / 2 ? p.n : 0) + n0;
-      c = Source{p.c + ((int64_t)u.e * 2 * p.n + from) * p.k, p.k, min(kCols, p.n - n0)};
-    } else if constexpr (CSTR) {
-      c = Source{p.c + (int64_t)u.e * p.k * p.n + n0, p.n, p.n - n0};
-    } else {
-      c = Source{p.c + ((int64_t)u.e * p.n + n0) * p.k, p.k, min(kCols, p.n - n0)};
-    }
-    constexpr int CF = 2 * S::CF, RF = 2 * S::RF;
-    v4f acc[CF][RF];
-    product<S, CSTR, kSplit, BYTES>(acc, p, c, r, u.row0, u.e, n0, lds, wave, lane);
+    const Source c = weights_of<CSTR, GATED>(p, u.e, n0, GATED && wave >= S::kWaves / 2, kCols);
+    constexpr int RF = 2 * S::RF;
+    v4f acc[4][RF];
+    product<S, CSTR, GATED, BYTES>(acc, p, c, r, u.row0, u.e, n0, lds, wave, lane);
     __syncthreads();
-    if constexpr (!kSplit) {
-#pragma unroll
-      for (int i = 0; i < CF; i += 2) {
-        const int n = n0 + (wn * CF + i) * 16, cols = p.n - n;
-#pragma unroll
-        for (int j = 0; j < RF; ++j) {
-          const int at = (wm * RF + j) * 16 + (lane & 15);
-          store_bf16_pair(p.out + ((u.row0 + at) * p.n + n) * 2, lane, at < u.rows ? cols : 0, acc[i][j], acc[i + 1][j]);
-        }
-      }
-    } else {
-      static_assert(!kSplit || S::CF == 2, "a wave holds 32 gate and the same 32 up columns");
-      const int n = n0 + wn * 32;                            // n is a multiple of 128: the tile lies inside
-      uint32_t *top = (uint32_t *)smem;                      // [WN][BM] bits of the largest magnitudes
-#pragma unroll
-      for (int j = 0; j < RF; ++j) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] = act(p.act, acc[i][j][q]) * acc[CF / 2 + i][j][q];
-        if (p.out_quant != EP_QUANT_NONE) {
-          const uint32_t m = row_amax(acc[0][j], acc[1][j]);
-          if (lane < 16) top[wn * S::BM + (wm * RF + j) * 16 + lane] = m;
-        }
-      }
-      if (p.out_quant != EP_QUANT_NONE) __syncthreads();
-#pragma unroll
-      for (int j = 0; j < RF; ++j) {
-        const int at = (wm * RF + j) * 16 + (lane & 15);
-        const int64_t row = u.row0 + at;
-        const bool ok = at < u.rows;
-        if (p.out_quant == EP_QUANT_NONE) {
-          store_bf16_pair(p.out + (row * p.n + n) * 2, lane, ok ? 32 : 0, acc[0][j], acc[1][j]);
-        } else {
-          uint32_t m = 0;
-#pragma unroll
-          for (int w = 0; w < S::WN; ++w) m = max(m, top[w * S::BM + at]);
-          const Block128 b = block128(p.out_quant, m);
-          store_codes_pair(p.out + row * p.n + n, lane, ok, acc[0][j], acc[1][j], b);
-          if (ok && wn == 0 && lane < 16) {
-            const int64_t to = row * (p.n / 128) + n0 / 128;
-            if (p.out_quant == EP_QUANT_FP8_B128_UE8M0) ((uint8_t *)p.out_scales)[to] = (uint8_t)b.byte;
-            else ((float *)p.out_scales)[to] = b.scale;
-          }
-        }
-      }
-    }
+    epilogue<GATED, RF, S::BM>(p, u, n0, wn, lane, acc, [&](int j) { return (wm * RF + j) * 16; }, (uint32_t *)smem);
     __syncthreads();
   }
 #endif
 }
 
-typedef Shape<2, 4, 4, 2, 2> Large;
+template <bool CSTR, bool GATED, bool BYTES>
+__global__ __launch_bounds__(Tile256::kThreads) void gmm256_kernel(GmmArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef Tile256 S;
+  constexpr int kCols = GATED ? S::BN / 2 : S::BN, kScale = BYTES ? 1 : 4;
+  // two stages, then four stages' row scales
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + 4 * 1024];
+  __shared__ uint32_t top[GATED ? 4 * S::BM : 1];
+  __shared__ Groups g;
+  lds_u8 *lds = (lds_u8 *)smem;
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
+  const int wn = S::wn(wave), kb = p.k / 128;
+  scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
+  const int nc = (p.n + kCols - 1) / kCols;
+  const Plan256 plan = plan_units(uniform(g.first[p.E]), nc);
+  const int units = plan.units;
+  Pipe256<CSTR, false, 1, GATED> pipe;
+  RowTile u;
+  int n0;
+  u32x4 scales;
+  // waves w and w + 4 fetch the same rows' scales: as many loads in every wave
+  const int scale_row = ((wave & 3) * kWave + lane) * kb * kScale;
+  const uint32_t scale_to = (uint32_t)(uintptr_t)lds + S::kLds + (wave & 3) * kWave * 4;
+  auto fetch_scales = [&](int t) { load_lds4<BYTES>(scale_to + (t & 3) * 1024, scale_row, scales, t * kScale); };
+  auto start = [&](int unit) {
+    u = row_tile256(g, plan, p.E, p.offsets, unit, nc);
+    n0 = u.tc * kCols;
+    scales = descriptor(p.r_scales + u.row0 * kb * kScale, (uint32_t)(u.rows * kb * kScale));
+    pipe.init(weights_of<CSTR, GATED>(p, u.e, n0, false, kCols), weights_of<CSTR, GATED>(p, u.e, n0, true, kCols),
+              Source{p.r + u.row0 * p.k, p.k, u.rows}, p.k, lds, wave, lane);
+    pipe.begin(fetch_scales);
+  };
+  int unit = unit_of_round(0);
+  if (unit >= units) return;
+  start(unit);
+  for (int round = 1;; ++round) {
+    v4f acc[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = v4f{};
+    const int nb_all = GATED ? 2 * p.n / 128 : p.n / 128;
+    const int nb = min(n0 / 128 + (GATED ? 0 : wn * 64 / 128), nb_all - 1);
+    const const_floats sw = (const_floats)(p.c_scales + (int64_t)u.e * nb_all * kb + (CSTR ? nb : (int64_t)nb * kb));
+    const int64_t sw_step = CSTR ? nb_all : 1, sw_up = GATED ? (int64_t)(p.n / 128) * kb : 0;
+    const lds_u8 *area = lds + S::kLds;
+    const int wm = S::wm(wave);
+    if (u.rows > 192) product256<4, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
+    else if (u.rows > 128) product256<3, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
+    else if (u.rows > 64) product256<2, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
+    else product256<1, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
+    lds_barrier();                                           // the stages are free
+    const RowTile done = u;
+    const int done_n0 = n0;
+    unit = unit_of_round(round);
+    if (unit < units) start(unit);
+    epilogue<GATED, 8, S::BM>(p, done, done_n0, wn, lane, acc,
+                              [&](int j) { return S::row(wave, j >> 1, (j & 1) * 16); }, top);
+    if (unit >= units) return;
+  }
+#endif
+}
+
 typedef Shape<2, 2, 4, 2, 3> Medium;
 typedef Shape<2, 1, 4, 2, 3> Small;
 typedef Shape<2, 1, 4, 1, 4> Tiny;
@@ -227,8 +382,10 @@ template <class S, bool CSTR, bool GATED, bool BYTES>
 hipError_t launch(const GmmArgs &p, int64_t pairs, hipStream_t s) {
   const int cols = GATED ? S::BN / 2 : S::BN;
   const int64_t tiles = (pairs + S::BM - 1) / S::BM + (p.E < pairs ? p.E : pairs);
-  const int64_t units = tiles * ((p.n + cols - 1) / cols);
-  hipLaunchKernelGGL((gmm_kernel<S, CSTR, GATED, BYTES>), dim3((unsigned)persistent_grid(units)), dim3(S::kThreads), 0, s, p);
+  const int64_t units = tiles * ((p.n + cols - 1) / cols) * (S::BM == 256 ? 4 : 1);   // tiles may be cut
+  const dim3 grid((unsigned)persistent_grid(units)), block(S::kThreads);
+  if constexpr (S::BM == 256) hipLaunchKernelGGL((gmm256_kernel<CSTR, GATED, BYTES>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((gmm_kernel<S, CSTR, GATED, BYTES>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -238,7 +395,7 @@ hipError_t by_shape(const GmmArgs &p, int64_t pairs, hipStream_t s) {
   if (mean <= 32) return launch<Tiny, CSTR, GATED, BYTES>(p, pairs, s);
   if (mean <= 64) return launch<Small, CSTR, GATED, BYTES>(p, pairs, s);
   if (mean <= 192) return launch<Medium, CSTR, GATED, BYTES>(p, pairs, s);
-  return launch<Large, CSTR, GATED, BYTES>(p, pairs, s);
+  return launch<Tile256, CSTR, GATED, BYTES>(p, pairs, s);
 }
 
 template <bool BYTES>
