@@ -31,71 +31,42 @@ struct RowArgs {
   char *d;                 // kGradAct: [rows, 2I]
 };
 
-// The product over k of a tile: acc[c][r] += C fragment c . R fragment r.
-template <class S, bool CSTR, bool RSTR, bool SPLIT, class Acc>
-__device__ __forceinline__ void product(Acc &acc, const Source &c, const Source &r, int steps,
-                                        int64_t k_all, lds_u8 *lds, int wave, int lane) {
-  typedef Loader<S::BN, CSTR, 2, S::kWaves, SPLIT> LC;
-  typedef Loader<S::BM, RSTR, 2, S::kWaves, false> LR;
-  constexpr int kLoads = LC::kLoads + LR::kLoads, N = S::kStages;
-  constexpr int kCStride = SPLIT ? S::BN / 2 : 32;
-  LC lc;
-  LR lr;
-  lc.init(wave, lane, c);
-  lr.init(wave, lane, r);
-  Reader<S::BN, CSTR, 2, S::CF> rc;
-  Reader<S::BM, RSTR, 2, S::RF> rr;
-  const int wn = wave % S::WN, wm = wave / S::WN;
-  rc.init(lane, SPLIT ? wn * 32 : wn * S::CF * 32, [](int f) { return f * kCStride; });
-  rr.init(lane, wm * S::RF * 32, [](int f) { return f * 32; });
+// The product over k of a tile, after p.begin(): acc[c][r] = C fragment c . R
+// fragment r.  Fragments are read one k step of 16 ahead, across the stages'
+// borders: the waves meet before the last step's matrix instructions, which
+// then cover the first reads of the next stage.
+template <class S, bool CSTR, bool SPLIT, class Acc>
+__device__ __forceinline__ void product(Acc &acc, const PipeN<S, CSTR, 2, SPLIT> &p) {
+  auto none = [](int) {};
 #pragma unroll
   for (int i = 0; i < S::CF; ++i)
 #pragma unroll
     for (int j = 0; j < S::RF; ++j) acc[i][j] = v16f{};
-  auto fetch = [&](int t) {
-    lds_u8 *at = lds + (t % N) * S::kStage;
-    lc.load(at, c, t, k_all - (int64_t)t * 64);
-    lr.load(at + S::BN * kKBytes, r, t, k_all - (int64_t)t * 64);
-  };
-  // Fragments are read one k step of 16 ahead, across the stages' borders: the
-  // waves meet before the last step's matrix instructions, which then cover
-  // the first reads of the next stage.
   bf16x8 fc[2][S::CF], fr[2][S::RF];
   auto read = [&](int t, int s, int to) {
-    const lds_u8 *tc = lds + (t % N) * S::kStage, *tr = tc + S::BN * kKBytes;
+    const lds_u8 *tc = p.stage_c(t), *tr = p.stage_r(t);
 #pragma unroll
-    for (int i = 0; i < S::CF; ++i) fc[to][i] = rc.bf16(tc, i, i * kCStride, s);
+    for (int i = 0; i < S::CF; ++i) fc[to][i] = p.rc.bf16(tc, i, p.c_index(i), s);
 #pragma unroll
-    for (int j = 0; j < S::RF; ++j) fr[to][j] = rr.bf16(tr, j, j * 32, s);
+    for (int j = 0; j < S::RF; ++j) fr[to][j] = p.rr.bf16(tr, j, j * 32, s);
   };
-  auto multiply = [&](int from) {
-#pragma unroll
-    for (int j = 0; j < S::RF; ++j)
-#pragma unroll
-      for (int i = 0; i < S::CF; ++i)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[from][i], fr[from][j], acc[i][j], 0, 0, 0);
-  };
-  // stage t is there and no wave reads stage t - 1 any more
-  auto meet = [&](int t) {
-    if (t + N - 2 < steps) wait_stage<kLoads * (N - 2)>();
-    else wait_stage<0>();
-    if (t + N - 1 < steps) fetch(t + N - 1);
-  };
-  if (steps == 0) return;
-  for (int t = 0; t < N - 1 && t < steps; ++t) fetch(t);
-  meet(0);
+  p.template meet<0>(0, false, none);
   read(0, 0, 0);
-  for (int t = 0; t < steps; ++t) {
+  for (int t = 0; t < p.steps; ++t) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s < 3) {
         read(t, s + 1, (s + 1) & 1);
-      } else if (t + 1 < steps) {
-        meet(t + 1);
+      } else if (t + 1 < p.steps) {
+        p.template meet<0>(t + 1, false, none);
         read(t + 1, 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
-      multiply(s & 1);
+#pragma unroll
+      for (int j = 0; j < S::RF; ++j)
+#pragma unroll
+        for (int i = 0; i < S::CF; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[s & 1][i], fr[s & 1][j], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -161,111 +132,161 @@ __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2
   else product256<1>(acc, p);
 }
 
-// Four values of the checkpoint.
-[[maybe_unused]] __device__ __forceinline__ void load4_bf16(const char *p, float (&v)[4]) {
-  const u32x2 q = *(const u32x2 *)p;
-  v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-}
-[[maybe_unused]] __device__ __forceinline__ void load4_fp8(const char *p, float scale, float (&v)[4]) {
-  const uint32_t q = *(const uint32_t *)p;
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q, true);
-  v[0] = a.x * scale; v[1] = a.y * scale; v[2] = b.x * scale; v[3] = b.y * scale;
+// Eight values of the checkpoint.
+[[maybe_unused]] __device__ __forceinline__ void decode8(u32x4 q, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(q[i]);
+    v[2 * i + 1] = bf16_hi(q[i]);
+  }
 }
 
-// What becomes of a tile's accumulators.  A wave's fragment (i, j) holds the
-// output columns col(i) + 0..31 and the tile's rows row(j) + 0..31.
-//   cols        output columns of the tile
-//   top         LDS [2][4][rows of a tile]: largest magnitudes (8-bit checkpoint)
+// What becomes of a tile's accumulators.  A wave's fragment (i, j) holds 32
+// output columns (of the gate and of the up rows: the same) and the tile's rows
+// row_of(j) + 0..31.
+//   top         LDS [2][4][BM]: largest magnitudes (8-bit checkpoint)
+template <int RF, int BM, int ACT, class Acc, class Row>
+__device__ __forceinline__ void epilogue_up(const RowArgs &p, const RowTile &u, int n0, int wn, int lane, Acc &acc,
+                                            Row row_of, uint32_t *top) {
+  const int half = lane >> 5, n = n0 + wn * 32, cols = p.n - n;
+  if (p.ck_form == kCkFp8) {
+#pragma unroll
+    for (int j = 0; j < RF; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t m = row_amax(acc[i][j]);
+        if (half == 0) top[(i * 4 + wn) * BM + row_of(j) + lane] = m;
+      }
+    lds_barrier();
+  }
+#pragma unroll
+  for (int j = 0; j < RF; ++j) {
+    const int at = row_of(j) + (lane & 31);
+    const bool ok = at < u.rows && cols > 0;
+    const int64_t row = u.row0 + at;
+    const v16f &gt = acc[0][j], &up = acc[1][j];
+    float a[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = act<ACT>(gt[i]) * up[i];
+    store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int i) { return a[i]; });
+    if (p.ck_form == kCkBf16) {
+      char *q = p.ck + (row * 2 * p.n + n) * 2;
+      store_bf16(q, half, ok ? cols : 0, [&](int i) { return gt[i]; });
+      store_bf16(q + (int64_t)p.n * 2, half, ok ? cols : 0, [&](int i) { return up[i]; });
+    }
+    if (p.ck_form == kCkFp8) {
+      // the whole 128-column block of the checkpoint lies in the tile
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max(m, top[(i * 4 + w) * BM + at]);
+        const Block128 b = block128(EP_QUANT_FP8_B128, m);
+        store_codes(p.ck + row * 2 * p.n + i * p.n + n, half, ok, acc[i][j], b);
+        if (ok && wn == 0 && half == 0) p.ck_scales[row * (2 * p.n / 128) + (i * p.n + n0) / 128] = b.scale;
+      }
+    }
+  }
+}
+
+// da in acc: dg, du and a to memory.  The checkpoint of the next fragment is
+// on its way while a fragment is worked on; rows and columns past the tile's
+// read its first ones.
+template <int RF, int ACT, bool FP8, class Acc, class Row>
+__device__ __forceinline__ void epilogue_act(const RowArgs &p, const RowTile &u, int n0, int wn, int lane, Acc &acc,
+                                             Row row_of) {
+  const int half = lane >> 5;
+  struct Piece {
+    u32x4 g[2], u[2];                      // 8 values each: bf16, or e4m3 in the first two words
+    float sg, su;
+  };
+  auto load = [&](int f) {
+    const int i = f / RF, j = f % RF, at = row_of(j) + (lane & 31), n = n0 + (wn * 2 + i) * 32;
+    const int64_t row = u.row0 + (at < u.rows ? at : 0);
+    const int col = (n < p.n ? n : n0) + 8 * half;
+    Piece q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t to = row * 2 * p.n + col + 16 * h;
+      if constexpr (FP8) {
+        const u32x2 a = *(const u32x2 *)(p.ck + to), b = *(const u32x2 *)(p.ck + to + p.n);
+        q.g[h] = u32x4{a.x, a.y, 0, 0};
+        q.u[h] = u32x4{b.x, b.y, 0, 0};
+      } else {
+        q.g[h] = *(const u32x4 *)(p.ck + to * 2);
+        q.u[h] = *(const u32x4 *)(p.ck + (to + p.n) * 2);
+      }
+    }
+    if constexpr (FP8) {
+      const float *s = p.ck_scales + row * (2 * p.n / 128);
+      q.sg = s[col / 128];
+      q.su = s[(p.n + col) / 128];
+    }
+    return q;
+  };
+  Piece next = load(0);
+#pragma unroll
+  for (int f = 0; f < 2 * RF; ++f) {
+    const Piece q = next;
+    if (f + 1 < 2 * RF) next = load(f + 1);
+    const int i = f / RF, j = f % RF, at = row_of(j) + (lane & 31), n = n0 + (wn * 2 + i) * 32;
+    const int64_t row = u.row0 + at;
+    float da[16];
+    columns_of(acc[i][j], da);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float gt[8], up[8], dg[8], du[8], a[8];
+      if constexpr (FP8) {
+        e4m3x8_decode(u32x2{q.g[h].x, q.g[h].y}, gt);
+        e4m3x8_decode(u32x2{q.u[h].x, q.u[h].y}, up);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          gt[x] *= q.sg;
+          up[x] *= q.su;
+        }
+      } else {
+        decode8(q.g[h], gt);
+        decode8(q.u[h], up);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        float v, dv;
+        act_grad<ACT>(gt[x], v, dv);
+        dg[x] = da[8 * h + x] * up[x] * dv;
+        du[x] = da[8 * h + x] * v;
+        a[x] = v * up[x];
+      }
+      const int col = n + 16 * h + 8 * half;
+      if (at < u.rows && col < p.n) {
+        char *d = p.d + (row * 2 * p.n + col) * 2;
+        store8_bf16(d, dg);
+        store8_bf16(d + (int64_t)p.n * 2, du);
+        store8_bf16(p.out + (row * p.n + col) * 2, a);
+      }
+    }
+  }
+}
+
 template <int MODE, int RF, int BM, class Acc, class Row>
 __device__ __forceinline__ void epilogue(const RowArgs &p, const RowTile &u, int n0, int wn, int lane, Acc &acc, Row row_of,
                                          uint32_t *top) {
-  const int half = lane >> 5;
   if constexpr (MODE == kUp) {
-    const int n = n0 + wn * 32, cols = p.n - n;
-    if (p.ck_form == kCkFp8) {
-#pragma unroll
-      for (int j = 0; j < RF; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t m = row_amax(acc[i][j]);
-          if (half == 0) top[(i * 4 + wn) * BM + row_of(j) + lane] = m;
-        }
-      lds_barrier();
-    }
-#pragma unroll
-    for (int j = 0; j < RF; ++j) {
-      const int at = row_of(j) + (lane & 31);
-      const bool ok = at < u.rows && cols > 0;
-      const int64_t row = u.row0 + at;
-      const v16f &gt = acc[0][j], &up = acc[1][j];
-      float a[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] = act(p.act, gt[i]) * up[i];
-      store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int i) { return a[i]; });
-      if (p.ck_form == kCkBf16) {
-        char *q = p.ck + (row * 2 * p.n + n) * 2;
-        store_bf16(q, half, ok ? cols : 0, [&](int i) { return gt[i]; });
-        store_bf16(q + (int64_t)p.n * 2, half, ok ? cols : 0, [&](int i) { return up[i]; });
-      }
-      if (p.ck_form == kCkFp8) {
-        // the whole 128-column block of the checkpoint lies in the tile
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) m = max(m, top[(i * 4 + w) * BM + at]);
-          const Block128 b = block128(EP_QUANT_FP8_B128, m);
-          store_codes(p.ck + row * 2 * p.n + i * p.n + n, half, ok, acc[i][j], b);
-          if (ok && wn == 0 && half == 0) p.ck_scales[row * (2 * p.n / 128) + (i * p.n + n0) / 128] = b.scale;
-        }
-      }
-    }
+    with_act(p.act, [&](auto a) { epilogue_up<RF, BM, decltype(a)::value>(p, u, n0, wn, lane, acc, row_of, top); });
+  } else if constexpr (MODE == kGradAct) {
+    if (u.rows <= 0) return;
+    with_act(p.act, [&](auto a) {
+      if (p.ck_form == kCkFp8) epilogue_act<RF, decltype(a)::value, true>(p, u, n0, wn, lane, acc, row_of);
+      else epilogue_act<RF, decltype(a)::value, false>(p, u, n0, wn, lane, acc, row_of);
+    });
   } else {
+    const int half = lane >> 5;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = n0 + (wn * 2 + i) * 32, cols = p.n - n;
 #pragma unroll
       for (int j = 0; j < RF; ++j) {
         const int at = row_of(j) + (lane & 31);
-        const bool ok = at < u.rows && cols > 0;
-        const int64_t row = u.row0 + at;
-        if constexpr (MODE == kGradAct) {
-          float dg[16], du[16], a[16];
-          float sg = 0.0f, su = 0.0f;
-          if (p.ck_form == kCkFp8 && ok) {
-            sg = p.ck_scales[row * (2 * p.n / 128) + n / 128];
-            su = p.ck_scales[row * (2 * p.n / 128) + (p.n + n) / 128];
-          }
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float gt[4] = {}, up[4] = {};
-            const int m = n + 8 * b + 4 * half;
-            if (ok) {
-              if (p.ck_form == kCkFp8) {
-                load4_fp8(p.ck + row * 2 * p.n + m, sg, gt);
-                load4_fp8(p.ck + row * 2 * p.n + p.n + m, su, up);
-              } else {
-                load4_bf16(p.ck + (row * 2 * p.n + m) * 2, gt);
-                load4_bf16(p.ck + (row * 2 * p.n + p.n + m) * 2, up);
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float da = acc[i][j][4 * b + q];
-              float f, df;
-              act_grad(p.act, gt[q], f, df);
-              dg[4 * b + q] = da * up[q] * df;
-              du[4 * b + q] = da * f;
-              a[4 * b + q] = f * up[q];
-            }
-          }
-          char *d = p.d + (row * 2 * p.n + n) * 2;
-          store_bf16(d, half, ok ? cols : 0, [&](int q) { return dg[q]; });
-          store_bf16(d + (int64_t)p.n * 2, half, ok ? cols : 0, [&](int q) { return du[q]; });
-          store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int q) { return a[q]; });
-        } else {
-          store_bf16(p.out + (row * p.n + n) * 2, half, ok ? cols : 0, [&](int q) { return acc[i][j][q]; });
-        }
+        store_bf16(p.out + ((u.row0 + at) * p.n + n) * 2, half, at < u.rows ? cols : 0, [&](int q) { return acc[i][j][q]; });
       }
     }
   }
@@ -282,6 +303,7 @@ __device__ __forceinline__ Source weights_of(const RowArgs &p, int e, int n0, bo
     return Source{p.c + ((int64_t)e * p.k * p.n + n0) * 2, (int64_t)p.n * 2, p.n - n0};
 }
 
+// The next unit's first stages are fetched before the epilogue of a unit.
 template <class S, int MODE>
 __global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
@@ -289,26 +311,36 @@ __global__ __launch_bounds__(S::kThreads) void rows_kernel(RowArgs p) {
   constexpr int kCols = kSplit ? S::BN / 2 : S::BN;         // output columns of a tile
   static_assert(S::CF == 2 && S::WN == 4, "the epilogue's columns");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
+  __shared__ uint32_t top[MODE == kUp ? 2 * 4 * S::BM : 1];
   __shared__ Groups g;
-  lds_u8 *lds = (lds_u8 *)smem;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
   const int wn = wave % S::WN, wm = wave / S::WN;
   scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
   const int nc = (p.n + kCols - 1) / kCols;
-  const int units = g.first[p.E] * nc;
-  for (int round = 0;; ++round) {
-    const int unit = unit_of_round(round);
-    if (unit >= units) return;                               // uniform; later rounds only have larger units
-    const RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
-    const int n0 = u.tc * kCols;
-    const Source r{p.r + u.row0 * p.k * 2, (int64_t)p.k * 2, u.rows};
-    const Source c = weights_of<MODE>(p, u.e, n0, kSplit && wave >= S::kWaves / 2, kCols);
+  const int units = uniform(g.first[p.E]) * nc;
+  PipeN<S, kCStr, 2, kSplit> pipe;
+  RowTile u;
+  int n0;
+  auto start = [&](int unit) {
+    u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
+    n0 = u.tc * kCols;
+    pipe.init(weights_of<MODE>(p, u.e, n0, kSplit && wave >= S::kWaves / 2, kCols),
+              Source{p.r + u.row0 * p.k * 2, (int64_t)p.k * 2, u.rows}, p.k, (lds_u8 *)smem, wave, lane);
+    pipe.begin([](int) {});
+  };
+  int unit = unit_of_round(0);
+  if (unit >= units) return;                                 // uniform; later rounds only have larger units
+  start(unit);
+  for (int round = 1;; ++round) {
     v16f acc[S::CF][S::RF];
-    product<S, kCStr, false, kSplit>(acc, c, r, p.k / 64, p.k, lds, wave, lane);
-    __syncthreads();                                         // the stages are free
-    epilogue<MODE, S::RF, S::BM>(p, u, n0, wn, lane, acc, [&](int j) { return (wm * S::RF + j) * 32; },
-                                 (uint32_t *)smem);
-    __syncthreads();                                         // before the next unit's stages
+    product(acc, pipe);
+    lds_barrier();                                           // the stages are free
+    const RowTile done = u;
+    const int done_n0 = n0;
+    unit = unit_of_round(round);
+    if (unit < units) start(unit);
+    epilogue<MODE, S::RF, S::BM>(p, done, done_n0, wn, lane, acc, [&](int j) { return (wm * S::RF + j) * 32; }, top);
+    if (unit >= units) return;
   }
 #endif
 }
@@ -436,28 +468,31 @@ __global__ __launch_bounds__(Tile256::kThreads) void weights256_kernel(WeightArg
 #endif
 }
 
-typedef Shape<2, 2, 4, 2, 3> Medium;     // 128 rows x 256 columns
-typedef Shape<2, 1, 4, 2, 3> Small;      // 64 rows
-typedef Shape<2, 1, 4, 1, 4> Tiny;       // 32 rows
-
-template <class S, int MODE>
-hipError_t rows_launch(const RowArgs &p, int64_t pairs, hipStream_t s) {
-  const int cols = MODE == kUp ? S::BN / 2 : S::BN;
-  const int64_t tiles = (pairs + S::BM - 1) / S::BM + (p.E < pairs ? p.E : pairs);
-  const int64_t units = tiles * ((p.n + cols - 1) / cols) * (S::BM == 256 ? 4 : 1);   // tiles may be cut
-  const dim3 grid((unsigned)persistent_grid(units)), block(S::kThreads);
-  if constexpr (S::BM == 256) hipLaunchKernelGGL(rows256_kernel<MODE>, grid, block, 0, s, p);
-  else hipLaunchKernelGGL((rows_kernel<S, MODE>), grid, block, 0, s, p);
-  return hipGetLastError();
-}
+template <int BM>
+struct ShapeOf;
+template <>
+struct ShapeOf<32> : Shape<2, 1, 4, 1, 4> {};
+template <>
+struct ShapeOf<64> : Shape<2, 1, 4, 2, 3> {};
+template <>
+struct ShapeOf<128> : Shape<2, 2, 4, 2, 3> {};
+template <>
+struct ShapeOf<256> : Tile256 {};
 
 template <int MODE>
-hipError_t rows_shape(const RowArgs &p, int64_t pairs, hipStream_t s) {
-  const int64_t mean = pairs / p.E;
-  if (mean <= 32) return rows_launch<Tiny, MODE>(p, pairs, s);
-  if (mean <= 64) return rows_launch<Small, MODE>(p, pairs, s);
-  if (mean <= 192) return rows_launch<Medium, MODE>(p, pairs, s);
-  return rows_launch<Tile256, MODE>(p, pairs, s);
+hipError_t rows_launch(const RowArgs &p, int64_t pairs, hipStream_t s) {
+  const int cols = MODE == kUp ? 128 : 256;
+  const int64_t nc = (p.n + cols - 1) / cols;
+  return with_height(pairs, p.E, nc, [&](auto bm) {
+    constexpr int BM = decltype(bm)::value;
+    typedef ShapeOf<BM> S;
+    const int64_t tiles = (pairs + BM - 1) / BM + (p.E < pairs ? p.E : pairs);
+    // 256-row tiles may be cut in 4
+    const dim3 grid((unsigned)persistent_grid(tiles * nc * (BM == 256 ? 4 : 1))), block(S::kThreads);
+    if constexpr (BM == 256) hipLaunchKernelGGL(rows256_kernel<MODE>, grid, block, 0, s, p);
+    else hipLaunchKernelGGL((rows_kernel<S, MODE>), grid, block, 0, s, p);
+    return hipGetLastError();
+  });
 }
 
 RowArgs row_args(const FfnArgs &f, const void *r, const void *c, int k, int n, void *out) {
@@ -488,9 +523,9 @@ hipError_t launch_ffn(const FfnArgs &f, hipStream_t s) {
   const int64_t pairs = pairs_of(f.h);
   if (pairs == 0) return hipSuccess;
   char *a = f.ws + ffn_ws(f.h.max_rows, f.inter, 0).a;
-  const hipError_t e = rows_shape<kUp>(row_args(f, f.x, f.w1, f.hidden, f.inter, a), pairs, s);
+  const hipError_t e = rows_launch<kUp>(row_args(f, f.x, f.w1, f.hidden, f.inter, a), pairs, s);
   if (e != hipSuccess) return e;
-  return rows_shape<kDown>(row_args(f, a, f.w2, f.inter, f.hidden, f.out), pairs, s);
+  return rows_launch<kDown>(row_args(f, a, f.w2, f.inter, f.hidden, f.out), pairs, s);
 }
 
 hipError_t launch_ffn_backward(const FfnGradArgs &g, hipStream_t s) {
@@ -502,8 +537,8 @@ hipError_t launch_ffn_backward(const FfnGradArgs &g, hipStream_t s) {
   if (pairs > 0) {
     RowArgs p = row_args(f, g.grad_out, f.w2, f.hidden, f.inter, a);
     p.d = d;
-    if ((e = rows_shape<kGradAct>(p, pairs, s)) != hipSuccess) return e;
-    if ((e = rows_shape<kGradX>(row_args(f, d, f.w1, 2 * f.inter, f.hidden, g.grad_x), pairs, s)) !=
+    if ((e = rows_launch<kGradAct>(p, pairs, s)) != hipSuccess) return e;
+    if ((e = rows_launch<kGradX>(row_args(f, d, f.w1, 2 * f.inter, f.hidden, g.grad_x), pairs, s)) !=
         hipSuccess)
       return e;
   }

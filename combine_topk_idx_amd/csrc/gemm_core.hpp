@@ -38,6 +38,10 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
 template <bool B>
 struct Flag {
   static constexpr bool value = B;
@@ -165,6 +169,25 @@ __device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *_
   u.row0 = (int64_t)offsets[u.e] + (int64_t)tr * bm;
   u.rows = min(bm, rows - tr * bm);
   return u;
+}
+
+// Height of a launch's row tiles from its mean rows an expert (256 columns a
+// tile; gated: 128).  Measured on 64 experts of 129 rows (2048 -> 2 x 768, 8-bit
+// checkpoint; 32, 64, 128, 256 rows): gate and up 202, 157, 177, 177 us, dy W2
+// 102, 69, 97, 87 us -- under 2.5 rounds of 128-row tiles the last, nearly empty
+// round costs more than the weights read once more for each 64 rows; a W2 103,
+// 78, 62, 66 us, its gradient 172, 130, 104, 106 us, at 2.8 rounds.  16 experts
+// of 127 rows, 2 column tiles: 17, 21, 30, 27 us, by the CUs that have a unit.
+// Many rows an expert: 256-row tiles (half the bytes a product), whose
+// leftover ones are cut.
+template <class F>
+__host__ inline hipError_t with_height(int64_t pairs, int64_t E, int64_t nc, F launch) {
+  const int64_t used = E < pairs ? E : pairs, mean = pairs / used;
+  auto units = [&](int bm) { return (pairs / bm + (used + 1) / 2) * nc; };
+  if (mean > 192) return launch(Int<256>());
+  if (mean > 32 && units(128) >= 640) return launch(Int<128>());
+  if (mean > 32 && units(64) >= 128) return launch(Int<64>());
+  return launch(Int<32>());
 }
 
 // ---------------------------------------------------------------------------
@@ -377,6 +400,67 @@ struct Shape {
   static constexpr int BN = 32 * CF * WN, BM = 32 * RF * WM;
   static constexpr int kStage = (BN + BM) * kKBytes;
   static constexpr int kLds = kStage * kStages;
+};
+
+// The operands of a tile of Shape S on their way through N = S::kStages stages:
+// stage t + N - 1 is fetched when every wave has read stage t - 1.
+//   EXTRA   more loads a stage that `extra(t)` issues, in the first
+//           `extra_waves` waves
+template <class S, bool CSTR, int EB, bool SPLIT>
+struct PipeN {
+  typedef Loader<S::BN, CSTR, EB, S::kWaves, SPLIT> LC;
+  typedef Loader<S::BM, false, EB, S::kWaves, false> LR;
+  static constexpr int kLoads = LC::kLoads + LR::kLoads, N = S::kStages, kSteps = kKBytes / EB;
+  static constexpr int kCFrags = EB == 2 ? S::CF : 2 * S::CF, kRFrags = EB == 2 ? S::RF : 2 * S::RF;
+  static constexpr int kWide = EB == 2 ? 32 : 16;
+  LC lc;
+  LR lr;
+  Reader<S::BN, CSTR, EB, kCFrags> rc;
+  Reader<S::BM, false, EB, kRFrags> rr;
+  Source c, r;
+  int64_t k_all;
+  int steps;
+  lds_u8 *lds;
+
+  // split: the wave's first half of fragments are gate rows, the others the same up rows
+  static __device__ __forceinline__ int c_index(int f) {
+    return SPLIT ? f / (kCFrags / 2) * (S::BN / 2) + f % (kCFrags / 2) * kWide : f * kWide;
+  }
+  __device__ __forceinline__ void init(const Source &cs, const Source &rs, int64_t k, lds_u8 *l, int wave, int lane) {
+    c = cs;
+    r = rs;
+    k_all = k;
+    steps = (int)((k + kSteps - 1) / kSteps);
+    lds = l;
+    lc.init(wave, lane, c);
+    lr.init(wave, lane, r);
+    const int wn = wave % S::WN, wm = wave / S::WN;
+    rc.init(lane, wn * (SPLIT ? S::CF * 16 : S::CF * 32), [](int f) { return c_index(f); });
+    rr.init(lane, wm * S::RF * 32, [](int f) { return f * kWide; });
+  }
+  __device__ __forceinline__ const lds_u8 *stage_c(int t) const { return lds + (t % N) * S::kStage; }
+  __device__ __forceinline__ const lds_u8 *stage_r(int t) const { return stage_c(t) + S::BN * kKBytes; }
+  template <class F>
+  __device__ __forceinline__ void fetch(int t, F extra) const {
+    lds_u8 *at = lds + (t % N) * S::kStage;
+    lc.load(at, c, t, k_all - (int64_t)t * kSteps);
+    lr.load(at + S::BN * kKBytes, r, t, k_all - (int64_t)t * kSteps);
+    extra(t);
+  }
+  // Before the loop, as soon as the stages are free.
+  template <class F>
+  __device__ __forceinline__ void begin(F extra) const {
+    for (int t = 0; t < N - 1 && t < steps; ++t) fetch(t, extra);
+  }
+  // Stage t is there and no wave reads stage t - 1 any more.
+  template <int EXTRA, class F>
+  __device__ __forceinline__ void meet(int t, bool with_extra, F extra) const {
+    if (t + N - 2 >= steps) wait_loads<0>();
+    else if (EXTRA && with_extra) wait_loads<(kLoads + EXTRA) * (N - 2)>();
+    else wait_loads<kLoads * (N - 2)>();
+    wait_waves();
+    if (t + N - 1 < steps) fetch(t + N - 1, extra);
+  }
 };
 
 // ---------------------------------------------------------------------------
@@ -640,6 +724,22 @@ __device__ __forceinline__ void store_bf16(char *dst, int half, int cols, F valu
   }
 }
 
+// A fragment's values in that order: v[8 p + i] is column 16 p + 8 (l / 32) + i.
+__device__ __forceinline__ void columns_of(const v16f &a, float (&v)[16]) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t x = __float_as_uint(a[8 * p + i]), y = __float_as_uint(a[8 * p + 4 + i]);
+      swap_halves(x, y);
+      v[8 * p + i] = __uint_as_float(x);
+      v[8 * p + 4 + i] = __uint_as_float(y);
+    }
+}
+__device__ __forceinline__ void store8_bf16(char *dst, const float *v) {
+  *(u32x4 *)dst = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
 // The same for a pair of 16-column fragments of 16 x 16 (accumulator i of
 // lane l: column 4 (l / 16) + i, row l % 16): rows of 16 lanes exchanged, lane
 // l has columns pair_column(l) + 0..7 of the pair's 32.
@@ -741,25 +841,46 @@ __device__ __forceinline__ void store_codes_pair(char *dst, int lane, bool ok, c
 }
 
 // The gate's activation.
-__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678f); }
+// e^z as 2^(z log2 e): the product's rounding costs |z| 2^-24 of the value
+__device__ __forceinline__ float fast_exp(float z) { return __builtin_amdgcn_exp2f(z * 1.44269504f); }
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-z)); }
+// The normal distribution by Abramowitz and Stegun 7.1.26 (the error function
+// within 1.5e-7), at a sixth of erfcf's instructions; tail: e^(-z^2 / 2), which
+// the density needs too.
+__device__ __forceinline__ float normal_cdf(float z, float tail) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.23164189f, 1.0f));
+  float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+  q = __builtin_fmaf(t, q, 1.421413741f);
+  q = __builtin_fmaf(t, q, -0.284496736f);
+  q = __builtin_fmaf(t, q, 0.254829592f);
+  q = 0.5f * t * q * tail;
+  return z > 0.0f ? 1.0f - q : q;
+}
 
-// `kind` is uniform: ep_act_t.
-__device__ __forceinline__ float act(int kind, float z) {
-  return z * (kind == EP_ACT_SILU ? sigmoid(z) : normal_cdf(z));
+template <int ACT>
+__device__ __forceinline__ float act(float z) {
+  return z * (ACT == EP_ACT_SILU ? sigmoid(z) : normal_cdf(z, fast_exp(-0.5f * z * z)));
 }
 
 // the activation and its derivative
-__device__ __forceinline__ void act_grad(int kind, float z, float &f, float &df) {
-  if (kind == EP_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ void act_grad(float z, float &f, float &df) {
+  if constexpr (ACT == EP_ACT_SILU) {
     const float p = sigmoid(z);
     f = z * p;
     df = p + f * (1.0f - p);
   } else {
-    const float p = normal_cdf(z);
+    const float tail = fast_exp(-0.5f * z * z), p = normal_cdf(z, tail);
     f = z * p;
-    df = p + z * 0.39894228f * expf(-0.5f * z * z);
+    df = p + z * 0.39894228f * tail;
   }
+}
+
+// Calls f with the activation as a constant: one branch, not one a value.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == EP_ACT_SILU) f(Int<EP_ACT_SILU>());
+  else f(Int<EP_ACT_GELU>());
 }
 
 }  // namespace gemm

@@ -40,68 +40,36 @@ struct ScaleArea {
 // by no kernel that runs beside this one.
 typedef const __attribute__((address_space(4))) float *const_floats;
 
-template <class S, bool CSTR, bool SPLIT, bool BYTES, class Acc>
-__device__ __forceinline__ void product(Acc &acc, const GmmArgs &p, const Source &c, const Source &r,
-                                        int64_t row0, int e, int n0, lds_u8 *lds, int wave, int lane) {
-  typedef Loader<S::BN, CSTR, 1, S::kWaves, SPLIT> LC;
-  typedef Loader<S::BM, false, 1, S::kWaves, false> LR;
-  constexpr int kLoads = LC::kLoads + LR::kLoads, N = S::kStages;
-  constexpr int CF = 2 * S::CF, RF = 2 * S::RF;              // of 16 x 16
-  LC lc;
-  LR lr;
-  lc.init(wave, lane, c);
-  lr.init(wave, lane, r);
-  Reader<S::BN, CSTR, 1, CF> rc;
-  Reader<S::BM, false, 1, RF> rr;
-  const int wn = wave % S::WN, wm = wave / S::WN;
-  // gated: the wave's first fragments are gate rows, the others the same up rows
-  auto c_index = [](int f) { return SPLIT ? f / S::CF * (S::BN / 2) + f % S::CF * 16 : f * 16; };
-  rc.init(lane, SPLIT ? wn * S::CF * 16 : wn * CF * 16, c_index);
-  rr.init(lane, wm * RF * 16, [](int f) { return f * 16; });
+// The product over k of a tile, after p.begin().
+//   sw, step_w, up   the weight scales of the wave's columns by block of k, and
+//                    of the up columns
+template <class S, bool CSTR, bool SPLIT, bool BYTES, class Acc, class Fetch>
+__device__ __forceinline__ void product(Acc &acc, const PipeN<S, CSTR, 1, SPLIT> &p, const lds_u8 *area, int wave, int lane,
+                                        const_floats sw, int64_t step_w, int64_t up, Fetch fetch_scales) {
+  typedef ScaleArea<S> A;
+  constexpr int CF = 2 * S::CF, RF = 2 * S::RF, N = S::kStages;   // of 16 x 16
+  const int wm = wave / S::WN;
 #pragma unroll
   for (int i = 0; i < CF; ++i)
 #pragma unroll
     for (int j = 0; j < RF; ++j) acc[i][j] = v4f{};
-  const int steps = p.k / 128, kb = p.k / 128;
-  // weight scales of the wave's columns (64 or fewer, gated: of one gate and
-  // one up block)
-  const int nb_all = SPLIT ? 2 * p.n / 128 : p.n / 128;
-  const int nb = min(n0 / 128 + (SPLIT ? 0 : wn * S::CF * 32 / 128), nb_all - 1);
-  const const_floats sw = (const_floats)(p.c_scales + (int64_t)e * nb_all * kb + (CSTR ? nb : (int64_t)nb * kb));
-  const int64_t sw_step = CSTR ? nb_all : 1, sw_up = SPLIT ? (int64_t)(p.n / 128) * kb : 0;
-  typedef ScaleArea<S> A;
-  constexpr int kScale = BYTES ? 1 : 4;                      // bytes of a row scale in memory
-  const uint32_t area = (uint32_t)(uintptr_t)lds + S::kLds;
-  const u32x4 scales = descriptor(p.r_scales + row0 * kb * kScale, (uint32_t)(r.valid * kb * kScale));
-  const int soff_row = (wave * kWave + lane) * kb * kScale;   // rows past the tile's are past the range
-  auto fetch = [&](int t) {
-    lds_u8 *at = lds + (t % N) * S::kStage;
-    lc.load(at, c, t, p.k - (int64_t)t * 128);
-    lr.load(at + S::BN * kKBytes, r, t, p.k - (int64_t)t * 128);
-    if (wave < A::kWaves) load_lds4<BYTES>(area + (t % N) * A::kBytes + wave * kWave * 4, soff_row, scales, t * kScale);
-  };
-  for (int t = 0; t < N - 1 && t < steps; ++t) fetch(t);
-  float w0 = sw[0], w1 = SPLIT ? sw[sw_up] : 0.0f;
-  for (int t = 0; t < steps; ++t) {
-    if (t + N - 2 >= steps) wait_loads<0>();
-    else if (wave < A::kWaves) wait_loads<(kLoads + 1) * (N - 2)>();
-    else wait_loads<kLoads * (N - 2)>();
-    wait_waves();
-    if (t + N - 1 < steps) fetch(t + N - 1);
-    const int next = min(t + 1, steps - 1);
-    const float w0n = sw[next * sw_step], w1n = SPLIT ? sw[next * sw_step + sw_up] : 0.0f;
-    const lds_u8 *tc = lds + (t % N) * S::kStage, *tr = tc + S::BN * kKBytes;
-    const lds_u8 *srow = lds + S::kLds + (t % N) * A::kBytes + (wm * RF * 16 + (lane & 15)) * 4;
+  float w0 = sw[0], w1 = SPLIT ? sw[up] : 0.0f;
+  for (int t = 0; t < p.steps; ++t) {
+    p.template meet<1>(t, wave < A::kWaves, fetch_scales);
+    const int next = min(t + 1, p.steps - 1);
+    const float w0n = sw[next * step_w], w1n = SPLIT ? sw[next * step_w + up] : 0.0f;
+    const lds_u8 *tc = p.stage_c(t), *tr = p.stage_r(t);
+    const lds_u8 *srow = area + (t % N) * A::kBytes + (wm * RF * 16 + (lane & 15)) * 4;
     auto row_scale = [&](int j) {
       const uint32_t v = *(const __attribute__((address_space(3))) uint32_t *)(srow + j * 64);
       return BYTES ? e8m0_decode(v) : __uint_as_float(v);
     };
     v8i fc[CF];
 #pragma unroll
-    for (int i = 0; i < CF; ++i) fc[i] = rc.fp8(tc, i, c_index(i));
+    for (int i = 0; i < CF; ++i) fc[i] = p.rc.fp8(tc, i, p.c_index(i));
     // one row fragment ahead; a fragment's products are scaled and added
     // while the matrix cores work on the next one's
-    v8i fr = rr.fp8(tr, 0, 0);
+    v8i fr = p.rr.fp8(tr, 0, 0);
     float sr = row_scale(0), sp = 0.0f;
     v4f q[CF];
 #pragma unroll
@@ -109,7 +77,7 @@ __device__ __forceinline__ void product(Acc &acc, const GmmArgs &p, const Source
       v8i fn;
       float sn = 0.0f;
       if (j + 1 < RF) {
-        fn = rr.fp8(tr, j + 1, (j + 1) * 16);
+        fn = p.rr.fp8(tr, j + 1, (j + 1) * 16);
         sn = row_scale(j + 1);
       }
 #pragma unroll
@@ -135,8 +103,6 @@ __device__ __forceinline__ void product(Acc &acc, const GmmArgs &p, const Source
 
 // The same on the 256 x 256 tile, after p.begin(): its first NQ quarters.
 // A pair of matrix instructions is scaled and added while the next pair runs.
-//   sw, step, up   the weight scales of the wave's columns by block of k, and of
-//                  the up columns
 template <int NQ, bool CSTR, bool SPLIT, bool BYTES, class Acc, class Fetch>
 __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, false, 1, SPLIT> &p, const lds_u8 *area, int wm,
                                            int lane, const_floats sw, int64_t step_w, int64_t up, Fetch fetch_scales) {
@@ -234,12 +200,16 @@ __device__ __forceinline__ void epilogue(const GmmArgs &p, const RowTile &u, int
     }
   } else {
     const int n = n0 + wn * 32;                              // n is a multiple of 128: the tile lies inside
+    with_act(p.act, [&](auto kind) {
+#pragma unroll
+      for (int j = 0; j < RF; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][j][q] = act<decltype(kind)::value>(acc[i][j][q]) * acc[2 + i][j][q];
+    });
 #pragma unroll
     for (int j = 0; j < RF; ++j) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = act(p.act, acc[i][j][q]) * acc[2 + i][j][q];
       if (p.out_quant != EP_QUANT_NONE) {
         const uint32_t m = row_amax(acc[0][j], acc[1][j]);
         if (lane < 16) top[wn * BM + row_of(j) + lane] = m;
@@ -280,33 +250,70 @@ __device__ __forceinline__ Source weights_of(const GmmArgs &p, int e, int n0, bo
     return Source{p.c + ((int64_t)e * p.n + n0) * p.k, p.k, min(cols, p.n - n0)};
 }
 
-// GATED: gate and up rows in, n columns act(gate) * up out
+// The wave's weight scales: by block of k from `at`, `step` apart; the up
+// columns' `up` further.
+struct ColumnScales {
+  const_floats at;
+  int64_t step, up;
+};
+template <bool CSTR, bool GATED>
+__device__ __forceinline__ ColumnScales column_scales(const GmmArgs &p, int e, int n0, int wn) {
+  const int kb = p.k / 128, nb_all = GATED ? 2 * p.n / 128 : p.n / 128;
+  // a wave has 64 columns or fewer, gated: of one gate and one up block
+  const int nb = min(n0 / 128 + (GATED ? 0 : wn * 64 / 128), nb_all - 1);
+  return {(const_floats)(p.c_scales + (int64_t)e * nb_all * kb + (CSTR ? nb : (int64_t)nb * kb)), CSTR ? nb_all : 1,
+          GATED ? (int64_t)(p.n / 128) * kb : 0};
+}
+
+// GATED: gate and up rows in, n columns act(gate) * up out.  The next unit's
+// first stages are fetched before the epilogue of a unit.
 template <class S, bool CSTR, bool GATED, bool BYTES>
 __global__ __launch_bounds__(S::kThreads) void gmm_kernel(GmmArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__     // the core uses device-only types
-  constexpr int kCols = GATED ? S::BN / 2 : S::BN;
+  constexpr int kCols = GATED ? S::BN / 2 : S::BN, kScale = BYTES ? 1 : 4;   // bytes of a row scale in memory
   static_assert(S::CF == 2 && S::WN == 4, "the epilogue's columns");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + S::kStages * ScaleArea<S>::kBytes];
+  typedef ScaleArea<S> A;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + S::kStages * A::kBytes];
+  __shared__ uint32_t top[GATED ? 4 * S::BM : 1];
   __shared__ Groups g;
   lds_u8 *lds = (lds_u8 *)smem;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
-  const int wn = wave % S::WN, wm = wave / S::WN;
+  const int wn = wave % S::WN, wm = wave / S::WN, kb = p.k / 128;
   scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
   const int nc = (p.n + kCols - 1) / kCols;
-  const int units = g.first[p.E] * nc;
-  for (int round = 0;; ++round) {
-    const int unit = unit_of_round(round);
-    if (unit >= units) return;
-    const RowTile u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
-    const int n0 = u.tc * kCols;
-    const Source r{p.r + u.row0 * p.k, p.k, u.rows};
-    const Source c = weights_of<CSTR, GATED>(p, u.e, n0, GATED && wave >= S::kWaves / 2, kCols);
+  const int units = uniform(g.first[p.E]) * nc;
+  PipeN<S, CSTR, 1, GATED> pipe;
+  RowTile u;
+  int n0;
+  u32x4 scales;
+  const int scale_row = (wave * kWave + lane) * kb * kScale;  // rows past the tile's are past the range
+  const uint32_t scale_to = (uint32_t)(uintptr_t)lds + S::kLds + wave * kWave * 4;
+  auto fetch_scales = [&](int t) {
+    if (wave < A::kWaves) load_lds4<BYTES>(scale_to + (t % S::kStages) * A::kBytes, scale_row, scales, t * kScale);
+  };
+  auto start = [&](int unit) {
+    u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
+    n0 = u.tc * kCols;
+    scales = descriptor(p.r_scales + u.row0 * kb * kScale, (uint32_t)(u.rows * kb * kScale));
+    pipe.init(weights_of<CSTR, GATED>(p, u.e, n0, GATED && wave >= S::kWaves / 2, kCols),
+              Source{p.r + u.row0 * p.k, p.k, u.rows}, p.k, lds, wave, lane);
+    pipe.begin(fetch_scales);
+  };
+  int unit = unit_of_round(0);
+  if (unit >= units) return;
+  start(unit);
+  for (int round = 1;; ++round) {
     constexpr int RF = 2 * S::RF;
     v4f acc[4][RF];
-    product<S, CSTR, GATED, BYTES>(acc, p, c, r, u.row0, u.e, n0, lds, wave, lane);
-    __syncthreads();
-    epilogue<GATED, RF, S::BM>(p, u, n0, wn, lane, acc, [&](int j) { return (wm * RF + j) * 16; }, (uint32_t *)smem);
-    __syncthreads();
+    const ColumnScales w = column_scales<CSTR, GATED>(p, u.e, n0, wn);
+    product<S, CSTR, GATED, BYTES>(acc, pipe, lds + S::kLds, wave, lane, w.at, w.step, w.up, fetch_scales);
+    lds_barrier();                                           // the stages are free
+    const RowTile done = u;
+    const int done_n0 = n0;
+    unit = unit_of_round(round);
+    if (unit < units) start(unit);
+    epilogue<GATED, RF, S::BM>(p, done, done_n0, wn, lane, acc, [&](int j) { return (wm * RF + j) * 16; }, top);
+    if (unit >= units) return;
   }
 #endif
 }
@@ -352,16 +359,13 @@ __global__ __launch_bounds__(Tile256::kThreads) void gmm256_kernel(GmmArgs p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[i][j] = v4f{};
-    const int nb_all = GATED ? 2 * p.n / 128 : p.n / 128;
-    const int nb = min(n0 / 128 + (GATED ? 0 : wn * 64 / 128), nb_all - 1);
-    const const_floats sw = (const_floats)(p.c_scales + (int64_t)u.e * nb_all * kb + (CSTR ? nb : (int64_t)nb * kb));
-    const int64_t sw_step = CSTR ? nb_all : 1, sw_up = GATED ? (int64_t)(p.n / 128) * kb : 0;
+    const ColumnScales w = column_scales<CSTR, GATED>(p, u.e, n0, wn);
     const lds_u8 *area = lds + S::kLds;
     const int wm = S::wm(wave);
-    if (u.rows > 192) product256<4, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
-    else if (u.rows > 128) product256<3, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
-    else if (u.rows > 64) product256<2, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
-    else product256<1, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, sw, sw_step, sw_up, fetch_scales);
+    if (u.rows > 192) product256<4, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, w.at, w.step, w.up, fetch_scales);
+    else if (u.rows > 128) product256<3, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, w.at, w.step, w.up, fetch_scales);
+    else if (u.rows > 64) product256<2, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, w.at, w.step, w.up, fetch_scales);
+    else product256<1, CSTR, GATED, BYTES>(acc, pipe, area, wm, lane, w.at, w.step, w.up, fetch_scales);
     lds_barrier();                                           // the stages are free
     const RowTile done = u;
     const int done_n0 = n0;
@@ -374,34 +378,37 @@ __global__ __launch_bounds__(Tile256::kThreads) void gmm256_kernel(GmmArgs p) {
 #endif
 }
 
-typedef Shape<2, 2, 4, 2, 3> Medium;
-typedef Shape<2, 1, 4, 2, 3> Small;
-typedef Shape<2, 1, 4, 1, 4> Tiny;
-
-template <class S, bool CSTR, bool GATED, bool BYTES>
-hipError_t launch(const GmmArgs &p, int64_t pairs, hipStream_t s) {
-  const int cols = GATED ? S::BN / 2 : S::BN;
-  const int64_t tiles = (pairs + S::BM - 1) / S::BM + (p.E < pairs ? p.E : pairs);
-  const int64_t units = tiles * ((p.n + cols - 1) / cols) * (S::BM == 256 ? 4 : 1);   // tiles may be cut
-  const dim3 grid((unsigned)persistent_grid(units)), block(S::kThreads);
-  if constexpr (S::BM == 256) hipLaunchKernelGGL((gmm256_kernel<CSTR, GATED, BYTES>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((gmm_kernel<S, CSTR, GATED, BYTES>), grid, block, 0, s, p);
-  return hipGetLastError();
-}
+template <int BM>
+struct ShapeOf;
+template <>
+struct ShapeOf<32> : Shape<2, 1, 4, 1, 4> {};
+template <>
+struct ShapeOf<64> : Shape<2, 1, 4, 2, 3> {};
+template <>
+struct ShapeOf<128> : Shape<2, 2, 4, 2, 3> {};
+template <>
+struct ShapeOf<256> : Tile256 {};
 
 template <bool CSTR, bool GATED, bool BYTES>
-hipError_t by_shape(const GmmArgs &p, int64_t pairs, hipStream_t s) {
-  const int64_t mean = pairs / p.E;
-  if (mean <= 32) return launch<Tiny, CSTR, GATED, BYTES>(p, pairs, s);
-  if (mean <= 64) return launch<Small, CSTR, GATED, BYTES>(p, pairs, s);
-  if (mean <= 192) return launch<Medium, CSTR, GATED, BYTES>(p, pairs, s);
-  return launch<Tile256, CSTR, GATED, BYTES>(p, pairs, s);
+hipError_t launch(const GmmArgs &p, int64_t pairs, hipStream_t s) {
+  const int cols = GATED ? 128 : 256;
+  const int64_t nc = (p.n + cols - 1) / cols;
+  return with_height(pairs, p.E, nc, [&](auto bm) {
+    constexpr int BM = decltype(bm)::value;
+    typedef ShapeOf<BM> S;
+    const int64_t tiles = (pairs + BM - 1) / BM + (p.E < pairs ? p.E : pairs);
+    // 256-row tiles may be cut in 4
+    const dim3 grid((unsigned)persistent_grid(tiles * nc * (BM == 256 ? 4 : 1))), block(S::kThreads);
+    if constexpr (BM == 256) hipLaunchKernelGGL((gmm256_kernel<CSTR, GATED, BYTES>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((gmm_kernel<S, CSTR, GATED, BYTES>), grid, block, 0, s, p);
+    return hipGetLastError();
+  });
 }
 
 template <bool BYTES>
 hipError_t by_form(const GmmArgs &p, const GmmB128Args &a, int64_t pairs, hipStream_t s) {
-  if (a.transposed) return by_shape<true, false, BYTES>(p, pairs, s);
-  return a.act == EP_ACT_NONE ? by_shape<false, false, BYTES>(p, pairs, s) : by_shape<false, true, BYTES>(p, pairs, s);
+  if (a.transposed) return launch<true, false, BYTES>(p, pairs, s);
+  return a.act == EP_ACT_NONE ? launch<false, false, BYTES>(p, pairs, s) : launch<false, true, BYTES>(p, pairs, s);
 }
 
 }  // namespace
