@@ -73,9 +73,9 @@ __device__ __forceinline__ void product(Acc &acc, const PipeN<S, CSTR, 2, SPLIT>
 }
 
 // The same on the 256 x 256 tile, after p.begin(): its first NQ quarters.
-template <int NQ, bool CSTR, bool RSTR, bool SPLIT, class Acc>
-__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2, SPLIT> &p) {
-  p.template meet0<0>();
+template <int NQ, int STORES, bool CSTR, bool RSTR, bool SPLIT, class Acc>
+__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2, SPLIT> &p, bool after) {
+  p.template meet0<0, STORES>(after);
   bf16x8 fc[2][4], fr[2][4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -83,14 +83,14 @@ __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2
 #pragma unroll
     for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(0, i, s);
   }
-  // LAST: t may be one of the last two stages
-  auto step = [&](int t, auto last) {
-    constexpr bool kLast = decltype(last)::value;
+  // EDGE: t may be the first stage or one of the last two
+  auto step = [&](int t, auto edge) {
+    constexpr bool kEdge = decltype(edge)::value;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (q == 1) p.template meet1<0, kLast>(t);
-      if (q == 3) p.template meet3<0, kLast>(t);
-      const bool next = !kLast || t + 1 < p.steps;
+      if (q == 1) p.template meet1<0, kEdge, STORES>(t, after);
+      if (q == 3) p.template meet3<0, kEdge, STORES>(t, after);
+      const bool next = !kEdge || t + 1 < p.steps;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -107,29 +107,31 @@ __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2
 #pragma unroll
           for (int i = 0; i < 2; ++i) fc[i][s] = p.read_c(t + 1, i, s);
         }
-        if (s < 2) p.template fetch<kLast>(t, q, s);
+        if (s < 2) p.template fetch<kEdge>(t, q, s);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   int t = 0;
+  if (STORES) step(t++, Flag<true>());
   for (; t + 2 < p.steps; ++t) step(t, Flag<false>());
   for (; t < p.steps; ++t) step(t, Flag<true>());
 }
 
 // `rows`: valid rows of the tile (each height has a loop of its own: branches
 // between the quarters cost more than the quarters they left out).
-template <bool CSTR, bool RSTR, bool SPLIT, class Acc>
-__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2, SPLIT> &p, int rows) {
+// STORES, after: of the pipe's meetings.
+template <int STORES, bool CSTR, bool RSTR, bool SPLIT, class Acc>
+__device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, RSTR, 2, SPLIT> &p, int rows, bool after) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = v16f{};
   if (p.steps == 0) return;
-  if (rows > 192) product256<4>(acc, p);
-  else if (rows > 128) product256<3>(acc, p);
-  else if (rows > 64) product256<2>(acc, p);
-  else product256<1>(acc, p);
+  if (rows > 192) product256<4, STORES>(acc, p, after);
+  else if (rows > 128) product256<3, STORES>(acc, p, after);
+  else if (rows > 64) product256<2, STORES>(acc, p, after);
+  else product256<1, STORES>(acc, p, after);
 }
 
 // Eight values of the checkpoint.
@@ -353,7 +355,10 @@ __global__ __launch_bounds__(Tile256::kThreads) void rows256_kernel(RowArgs p) {
   typedef Tile256 S;
   constexpr bool kSplit = MODE == kUp, kCStr = MODE == kGradX || MODE == kGradAct;
   constexpr int kCols = kSplit ? S::BN / 2 : S::BN;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
+  // whole lines out through LDS where the epilogue is a plain store
+  constexpr bool kLines = MODE == kDown || MODE == kGradX;
+  constexpr int kStores = kLines ? kTileStores : 0;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + (kLines ? kStoreLds : 0)];
   __shared__ uint32_t top[MODE == kUp ? 2 * 4 * S::BM : 1];
   __shared__ Groups g;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
@@ -376,13 +381,17 @@ __global__ __launch_bounds__(Tile256::kThreads) void rows256_kernel(RowArgs p) {
   start(unit);
   for (int round = 1;; ++round) {
     v16f acc[2][4];
-    product256(acc, pipe, u.rows);
+    product256<kStores>(acc, pipe, u.rows, round > 1);
     lds_barrier();                                           // the stages are free
     const RowTile done = u;
     const int done_n0 = n0;
     unit = unit_of_round(round);
     if (unit < units) start(unit);
-    epilogue<MODE, 4, S::BM>(p, done, done_n0, S::wn(wave), lane, acc, [&](int j) { return S::row(wave, j, 0); }, top);
+    if constexpr (kLines)
+      store_tile256(acc, (lds_u8 *)smem + S::kLds, p.out + (done.row0 * p.n + done_n0) * 2, (int64_t)p.n * 2, done.rows,
+                    p.n - done_n0, wave, lane);
+    else
+      epilogue<MODE, 4, S::BM>(p, done, done_n0, S::wn(wave), lane, acc, [&](int j) { return S::row(wave, j, 0); }, top);
     if (unit >= units) return;
   }
 #endif
@@ -405,10 +414,9 @@ struct WeightArgs {
 __global__ __launch_bounds__(Tile256::kThreads) void weights256_kernel(WeightArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   typedef Tile256 S;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds + kStoreLds];
   __shared__ Groups g;
   const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave);
-  const int half = lane >> 5, wn = S::wn(wave);
   order_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count);
   auto tiles = [](int n) { return (n + 255) / 256; };
   const int per0 = tiles(p.of[0].nr) * tiles(p.of[0].nc), per = per0 + tiles(p.of[1].nr) * tiles(p.of[1].nc);
@@ -448,21 +456,13 @@ __global__ __launch_bounds__(Tile256::kThreads) void weights256_kernel(WeightArg
   start(unit);
   for (int round = 1;; ++round) {
     v16f acc[2][4];
-    product256(acc, pipe, rows_out);
+    product256<kTileStores>(acc, pipe, rows_out, round > 1);
     lds_barrier();
     const int done_nc = nc, done_c0 = c0, done_rows = rows_out;
-    char *out = (which ? p.of[1].out : p.of[0].out) + ((int64_t)e * nr + r0) * nc * 2;
+    char *out = (which ? p.of[1].out : p.of[0].out) + (((int64_t)e * nr + r0) * nc + c0) * 2;
     unit = unit_of_round(round);
     if (unit < units) start(unit);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = done_c0 + (wn * 2 + i) * 32, cols = done_nc - n;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = S::row(wave, j, lane & 31);
-        store_bf16(out + ((int64_t)at * done_nc + n) * 2, half, at < done_rows ? cols : 0, [&](int q) { return acc[i][j][q]; });
-      }
-    }
+    store_tile256(acc, (lds_u8 *)smem + S::kLds, out, (int64_t)done_nc * 2, done_rows, done_nc - done_c0, wave, lane);
     if (unit >= units) return;
   }
 #endif

@@ -20,6 +20,7 @@
 
 #include "common.hpp"
 #include "formats.hpp"
+#include "ring.hpp"
 
 namespace ep {
 
@@ -647,12 +648,12 @@ struct Pipe256 {
   }
 
   // The fetches of quarter q of stage t, j = 0, 1.
-  // LAST: t may be one of the last two stages.
-  template <bool LAST>
+  // EDGE: t may be one of the last two stages.
+  template <bool EDGE>
   __device__ __forceinline__ void fetch(int t, int q, int j) const {
     if (q == 0) {
-      if (!LAST || t + 1 < steps) load_r(t + 1, 1, j);
-    } else if (!LAST || t + 2 < steps) {
+      if (!EDGE || t + 1 < steps) load_r(t + 1, 1, j);
+    } else if (!EDGE || t + 2 < steps) {
       if (q == 1) load_r(t + 2, 0, j);
       else load_c(t + 2, q - 2, j);
     }
@@ -676,22 +677,43 @@ struct Pipe256 {
       }
     }
   }
-  template <int EXTRA>
-  __device__ __forceinline__ void meet0() const {
-    if (steps > 1) wait_stage<8 + EXTRA>();
-    else wait_stage<2>();
+  // STORES: memory instructions that the wave issued between begin() and
+  // meet0() and that need not be waited for yet (`after`: whether it did).
+  template <int EXTRA, int STORES>
+  __device__ __forceinline__ void meet0(bool after) const {
+    if (STORES && after) {
+      if (steps > 1) wait_stage<8 + EXTRA + STORES>();
+      else wait_stage<2 + STORES>();
+    } else if (steps > 1) {
+      wait_stage<8 + EXTRA>();
+    } else {
+      wait_stage<2>();
+    }
   }
   // The meetings before quarters 1 and 3: loads that may still be in flight are
   // those issued after the ones waited for.
-  template <int EXTRA, bool LAST>
-  __device__ __forceinline__ void meet1(int t) const {
-    if (!LAST || t + 1 < steps) wait_stage<8 + EXTRA>();
-    else wait_stage<0>();
+  // EDGE: t may be the first stage or one of the last two.
+  template <int EXTRA, bool EDGE, int STORES>
+  __device__ __forceinline__ void meet1(int t, bool after) const {
+    if (EDGE && STORES && after && t == 0) {
+      if (t + 1 < steps) wait_stage<8 + EXTRA + STORES>();
+      else wait_stage<STORES>();
+    } else if (!EDGE || t + 1 < steps) {
+      wait_stage<8 + EXTRA>();
+    } else {
+      wait_stage<0>();
+    }
   }
-  template <int EXTRA, bool LAST>
-  __device__ __forceinline__ void meet3(int t) const {
-    if (!LAST || t + 2 < steps) wait_stage<6 + EXTRA>();
-    else if (t + 1 < steps) wait_stage<2>();
+  template <int EXTRA, bool EDGE, int STORES>
+  __device__ __forceinline__ void meet3(int t, bool after) const {
+    if (EDGE && STORES && after && t == 0) {
+      if (t + 2 < steps) wait_stage<6 + EXTRA + STORES>();
+      else if (t + 1 < steps) wait_stage<2 + STORES>();
+    } else if (!EDGE || t + 2 < steps) {
+      wait_stage<6 + EXTRA>();
+    } else if (t + 1 < steps) {
+      wait_stage<2>();
+    }
   }
 };
 
@@ -759,6 +781,55 @@ __device__ __forceinline__ void store_bf16_pair(char *dst, int lane, int cols, c
 }
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Stores a 256 x 256 tile of bf16 in whole lines: a wave's 64 columns of 16
+// rows pass through 2 KB of its own LDS, so that eight lanes write 128
+// consecutive bytes (in fragment order every store instruction would touch 32
+// lines with 32 bytes each: the weight gradients of 64 experts of 129 rows spent
+// 100 of 241 us on them).  Rows and columns past the tile's are out of the
+// descriptor's range: always kTileStores instructions.
+constexpr int kTileStores = 16;
+constexpr int kStoreLds = 8 * 2048;
+template <class Acc>
+__device__ __forceinline__ void store_tile256(const Acc &acc, lds_u8 *lds, char *out, int64_t pitch, int rows, int cols,
+                                              int wave, int lane) {
+  typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+  lds_u8 *mine = lds + wave * 2048;
+  const int wn = Tile256::wn(wave), half = lane >> 5, r = lane & 15;
+  const __amdgpu_buffer_rsrc_t d =
+      __builtin_amdgcn_make_buffer_rsrc(out, 0, (uint32_t)((int64_t)rows * pitch), 0x00020000);
+  const int to = wn * 64 < cols ? Tile256::row(wave, 0, lane >> 3) * (int)pitch + (wn * 64 + (lane & 7) * 8) * 2 : 0x7ffffff0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    u32x4 q[4];                                              // chunks 4 i + 2 p + half
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const v16f &a = acc[i][j];
+        uint32_t x0 = pack_bf16x2(a[8 * p], a[8 * p + 1]), x1 = pack_bf16x2(a[8 * p + 2], a[8 * p + 3]);
+        uint32_t y0 = pack_bf16x2(a[8 * p + 4], a[8 * p + 5]), y1 = pack_bf16x2(a[8 * p + 6], a[8 * p + 7]);
+        swap_halves(x0, y0);
+        swap_halves(x1, y1);
+        q[2 * i + p] = u32x4{x0, x1, y0, y1};
+      }
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      wave_lds_fence();
+      if (((lane >> 4) & 1) == pass) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) *(lds_u32x4 *)(mine + r * 128 + ((2 * c + half) ^ (r & 7)) * 16) = q[c];
+      }
+      wave_lds_fence();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = (lane >> 3) + 8 * k;
+        const u32x4 v = *(const lds_u32x4 *)(mine + row * 128 + ((lane & 7) ^ (row & 7)) * 16);
+        __builtin_amdgcn_raw_buffer_store_b128(v, d, to + (j * 64 + pass * 16 + k * 8) * (int)pitch, 0, 0);
+      }
+    }
+  }
+}
 
 // Bits of the largest magnitude of a lane's 16 values and of its row's other
 // 16 (as integers: a value that is not a number counts as the largest).

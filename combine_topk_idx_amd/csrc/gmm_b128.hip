@@ -111,7 +111,7 @@ __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, false, 
         area + (t & 3) * 1024 + (q * 64 + wm * 32 + f * 16 + (lane & 15)) * 4);
     return BYTES ? e8m0_decode(v) : __uint_as_float(v);
   };
-  p.template meet0<1>();
+  p.template meet0<1, 0>(false);
   v8i fc[4], fr[2][2];
   float sr[2][2], coef[2][2];
   v4f part[2][2];
@@ -134,15 +134,15 @@ __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, false, 
       a = pin(a);                                            // here, not after the loop's branches
     }
   };
-  auto step = [&](int t, auto last) {
-    constexpr bool kLast = decltype(last)::value;
-    const int next_t = kLast ? min(t + 1, p.steps - 1) : t + 1;
+  auto step = [&](int t, auto edge) {
+    constexpr bool kEdge = decltype(edge)::value;
+    const int next_t = kEdge ? min(t + 1, p.steps - 1) : t + 1;
     const float wn[2] = {sw[next_t * step_w], SPLIT ? sw[next_t * step_w + up] : 0.0f};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (q == 1) p.template meet1<1, kLast>(t);
-      if (q == 3) p.template meet3<1, kLast>(t);
-      const bool next = !kLast || t + 1 < p.steps;
+      if (q == 1) p.template meet1<1, kEdge, 0>(t, false);
+      if (q == 3) p.template meet3<1, kEdge, 0>(t, false);
+      const bool next = !kEdge || t + 1 < p.steps;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -165,8 +165,8 @@ __device__ __forceinline__ void product256(Acc &acc, const Pipe256<CSTR, false, 
             fr[0][i] = p.read_r8(t + 1, 0, i);
             sr[0][i] = row_scale(t + 1, 0, i);
           }
-          p.template fetch<kLast>(t, q, i);
-        } else if (i == 2 && q == 1 && (!kLast || t + 2 < p.steps)) {
+          p.template fetch<kEdge>(t, q, i);
+        } else if (i == 2 && q == 1 && (!kEdge || t + 2 < p.steps)) {
           fetch_scales(t + 2);
         }
         // this stage's column fragment has been used for the last time
