@@ -397,6 +397,95 @@ __global__ __launch_bounds__(Tile256::kThreads) void rows256_kernel(RowArgs p) {
 #endif
 }
 
+// Few rows an expert (kUp without an 8-bit checkpoint, kDown): sums joined over
+// the waves, wave w then has columns 8 w + 4 (l / 32) + 0..3 of row l % 32.
+template <int MODE>
+__global__ __launch_bounds__(TileFew::kThreads) void few_kernel(RowArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__
+  typedef TileFew S;
+  constexpr bool kSplit = MODE == kUp;
+  constexpr int kCols = kSplit ? 32 : 64;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
+  __shared__ Groups g;
+  lds_u8 *lds = (lds_u8 *)smem;
+  const int lane = threadIdx.x & (kWave - 1), wave = uniform((int)threadIdx.x / kWave), half = lane >> 5;
+  scan_rows<S::kThreads>(g, p.E, p.offsets, p.recv_count, S::BM);
+  const int nc = (p.n + kCols - 1) / kCols;
+  const int units = uniform(g.first[p.E]) * nc;
+  PipeFew<2> pipe;
+  RowTile u;
+  int n0;
+  auto none = [](int, int) {};
+  auto start = [&](int unit) {
+    u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
+    n0 = u.tc * kCols;
+    const Source lo = weights_of<MODE>(p, u.e, n0, false, 32);
+    const Source hi = kSplit ? weights_of<MODE>(p, u.e, n0, true, 32) : Source{lo.base + 32 * lo.pitch, lo.pitch, 32};
+    pipe.init(lo, hi, Source{p.r + u.row0 * p.k * 2, (int64_t)p.k * 2, u.rows}, p.k, lds, wave, lane);
+    pipe.begin(none);
+  };
+  int unit = unit_of_round(0);
+  if (unit >= units) return;
+  start(unit);
+  for (int round = 1;; ++round) {
+    v16f acc[2] = {};
+    for (int i = 0; i < pipe.steps; ++i) {
+      pipe.next<0>(i, none);
+      const lds_u8 *at = pipe.stage(i);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bf16x8 r = pipe.rd.bf16(at + 64 * kKBytes, 0, 0, s);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pipe.rd.bf16(at, 0, c * 32, s), r, acc[c], 0, 0, 0);
+      }
+    }
+    wait_lds();
+    const RowTile done = u;
+    const int done_n0 = n0;
+    unit = unit_of_round(round);
+    if (unit < units) start(unit);                           // into the wave's own first two buffers
+    typedef __attribute__((address_space(3))) v4f lds_v4f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *(lds_v4f *)(lds + wave * S::kMine + S::kJoin + ((c * 4 + b) * kWave + lane) * 16) =
+            v4f{acc[c][4 * b], acc[c][4 * b + 1], acc[c][4 * b + 2], acc[c][4 * b + 3]};
+    lds_barrier();
+    v4f sum[2] = {};
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int w = 0; w < S::kWaves; ++w)
+        sum[c] += *(const lds_v4f *)(lds + w * S::kMine + S::kJoin + ((c * 4 + wave) * kWave + lane) * 16);
+    lds_barrier();                                           // before a third stage goes there
+    const int64_t row = done.row0 + (lane & 31);
+    if ((lane & 31) < done.rows) {
+      auto store4 = [](char *dst, const v4f &v) { *(u32x2 *)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
+      const int n = done_n0 + 8 * wave + 4 * half;
+      if constexpr (kSplit) {
+        v4f a;
+        with_act(p.act, [&](auto kind) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = act<decltype(kind)::value>(sum[0][i]) * sum[1][i];
+        });
+        store4(p.out + (row * p.n + n) * 2, a);
+        if (p.ck_form == kCkBf16) {
+          char *q = p.ck + (row * 2 * p.n + n) * 2;
+          store4(q, sum[0]);
+          store4(q + (int64_t)p.n * 2, sum[1]);
+        }
+      } else {
+        store4(p.out + (row * p.n + n) * 2, sum[0]);
+        store4(p.out + (row * p.n + n + 32) * 2, sum[1]);
+      }
+    }
+    if (unit >= units) return;
+  }
+#endif
+}
+
 struct WeightArgs {
   const int *offsets;
   const int64_t *recv_count;
@@ -482,15 +571,24 @@ struct ShapeOf<256> : Tile256 {};
 template <int MODE>
 hipError_t rows_launch(const RowArgs &p, int64_t pairs, hipStream_t s) {
   const int cols = MODE == kUp ? 128 : 256;
-  const int64_t nc = (p.n + cols - 1) / cols;
-  return with_height(pairs, p.E, nc, [&](auto bm) {
+  const int64_t nc = (p.n + cols - 1) / cols, used = p.E < pairs ? p.E : pairs;
+  // (a checkpoint's scale takes 128 columns of a tile)
+  const bool few = MODE == kDown || (MODE == kUp && p.ck_form != kCkFp8);
+  return with_height(pairs, p.E, nc, few, [&](auto bm) {
     constexpr int BM = decltype(bm)::value;
-    typedef ShapeOf<BM> S;
-    const int64_t tiles = (pairs + BM - 1) / BM + (p.E < pairs ? p.E : pairs);
-    // 256-row tiles may be cut in 4
-    const dim3 grid((unsigned)persistent_grid(tiles * nc * (BM == 256 ? 4 : 1))), block(S::kThreads);
-    if constexpr (BM == 256) hipLaunchKernelGGL(rows256_kernel<MODE>, grid, block, 0, s, p);
-    else hipLaunchKernelGGL((rows_kernel<S, MODE>), grid, block, 0, s, p);
+    if constexpr (BM == 0) {
+      if constexpr (MODE == kDown || MODE == kUp) {
+        const int64_t units = (pairs / 32 + used) * (p.n / (MODE == kUp ? 32 : 64));
+        hipLaunchKernelGGL(few_kernel<MODE>, dim3((unsigned)persistent_grid(units)), dim3(TileFew::kThreads), 0, s, p);
+      }
+    } else {
+      typedef ShapeOf<BM> S;
+      const int64_t tiles = (pairs + BM - 1) / BM + used;
+      // 256-row tiles may be cut in 4
+      const dim3 grid((unsigned)persistent_grid(tiles * nc * (BM == 256 ? 4 : 1))), block(S::kThreads);
+      if constexpr (BM == 256) hipLaunchKernelGGL(rows256_kernel<MODE>, grid, block, 0, s, p);
+      else hipLaunchKernelGGL((rows_kernel<S, MODE>), grid, block, 0, s, p);
+    }
     return hipGetLastError();
   });
 }

@@ -181,9 +181,11 @@ __device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *_
 // of 127 rows, 2 column tiles: 17, 21, 30, 27 us, by the CUs that have a unit.
 // Many rows an expert: 256-row tiles (half the bytes a product), whose
 // leftover ones are cut.
+// Up to 32 rows an expert, `few`: TileFew (launch(Int<0>())).
 template <class F>
-__host__ inline hipError_t with_height(int64_t pairs, int64_t E, int64_t nc, F launch) {
+__host__ inline hipError_t with_height(int64_t pairs, int64_t E, int64_t nc, bool few, F launch) {
   const int64_t used = E < pairs ? E : pairs, mean = pairs / used;
+  if (mean <= 32 && few) return launch(Int<0>());
   auto units = [&](int bm) { return (pairs / bm + (used + 1) / 2) * nc; };
   if (mean > 192) return launch(Int<256>());
   if (mean > 32 && units(128) >= 640) return launch(Int<128>());
@@ -381,9 +383,10 @@ __device__ __forceinline__ void wait_waves() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // A barrier that orders LDS accesses alone: loads in flight stay there.
 __device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  wait_lds();
   wait_waves();
 }
 template <int N>
@@ -461,6 +464,72 @@ struct PipeN {
     else wait_loads<kLoads * (N - 2)>();
     wait_waves();
     if (t + N - 1 < steps) fetch(t + N - 1, extra);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// few rows: 64 columns x 32 rows, k split over the waves
+// ---------------------------------------------------------------------------
+//
+// With a few rows an expert a launch is the weights' way through the chip.
+// Each of four waves takes every fourth stage of k through three buffers of
+// its own, so nothing but its own loads holds it up; the sums are joined in
+// wave order through LDS.  64 columns (gated: 32 gate rows and the same 32 up
+// rows) make units enough for the whole card in small models.  k contiguous
+// operands.
+struct TileFew {
+  static constexpr int BN = 64, BM = 32, kWaves = 4, kThreads = kWaves * kWave;
+  static constexpr int kStage = (BN + BM) * kKBytes, kBuffers = 3;
+  static constexpr int kMine = kBuffers * kStage, kLds = kWaves * kMine;
+  // where the sums are joined: each wave's last buffer, which the next unit's
+  // first two stages leave alone
+  static constexpr int kJoin = 2 * kStage;
+};
+
+template <int EB>
+struct PipeFew {
+  static constexpr int kSteps = kKBytes / EB, kLoads = TileFew::kStage / 1024;
+  static constexpr int kCFrags = EB == 2 ? 2 : 4, kRFrags = EB == 2 ? 1 : 2, kWide = EB == 2 ? 32 : 16;
+  typedef Loader<32, false, EB, 1, false> L;                 // 32 rows, 4 loads
+  Source c[2], r;                                            // columns 0..31, 32..63
+  L lc, lr;
+  Reader<32, false, EB, 1> rd;
+  int steps, first;                                          // the wave's stages: first, first + 4, ..
+  lds_u8 *mine;
+
+  __device__ __forceinline__ void init(const Source &lo, const Source &hi, const Source &rs, int k, lds_u8 *lds, int wave,
+                                       int lane) {
+    c[0] = lo;
+    c[1] = hi;
+    r = rs;
+    lc.init(0, lane, lo);
+    lr.init(0, lane, rs);
+    rd.init(lane, 0, [](int) { return 0; });
+    first = wave;
+    const int all = k / kSteps;
+    steps = all > wave ? (all - wave + TileFew::kWaves - 1) / TileFew::kWaves : 0;
+    mine = lds + wave * TileFew::kMine;
+  }
+  __device__ __forceinline__ lds_u8 *stage(int i) const { return mine + i % TileFew::kBuffers * TileFew::kStage; }
+  template <class F>
+  __device__ __forceinline__ void fetch(int i, F extra) const {
+    const int t = first + i * TileFew::kWaves;
+    lds_u8 *at = stage(i);
+    lc.load(at, c[0], t, kSteps);
+    lc.load(at + 32 * kKBytes, c[1], t, kSteps);
+    lr.load(at + 64 * kKBytes, r, t, kSteps);
+    extra(t, i);
+  }
+  template <class F>
+  __device__ __forceinline__ void begin(F extra) const {
+    for (int i = 0; i < 2 && i < steps; ++i) fetch(i, extra);
+  }
+  // The wave's stage i is there; stage i + 2 is fetched over stage i - 1.
+  template <int EXTRA, class F>
+  __device__ __forceinline__ void next(int i, F extra) const {
+    if (i + 1 < steps) wait_loads<kLoads + EXTRA>();
+    else wait_loads<0>();
+    if (i + 2 < steps) fetch(i + 2, extra);
   }
 };
 
