@@ -720,20 +720,18 @@ def ep_moe_gmm_b128(handle: ep_handle_t, a_buf, a_quant, k: int, n: int, w, w_sc
     out bf16 [max_rows, n]; "silu" / "gelu": rows [0, n/2) of w are the gate's
     and [n/2, n) the up's, out is a receive buffer of width n/2 in out_quant
     ("none" or a per-128 mode)."""
-    E = handle.num_experts
-    if isinstance(w, torch.Tensor) and w.dtype not in (torch.uint8, torch.float8_e4m3fn):
+    E, aq, oq, kind = handle.num_experts, _quant(a_quant), _quant(out_quant), _act(act)
+    if isinstance(w, torch.Tensor) and w.dtype is not torch.uint8 and w.dtype is not torch.float8_e4m3fn:
         raise EpError(EP_ERR_INVALID_ARG, f"w must be uint8 or float8_e4m3fn (got {w.dtype})")
-    shape = (k, n) if transposed else (n, k)
-    width = n // 2 if _act(act) != ACT["none"] else n
+    wn, wk = (k, n) if transposed else (n, k)
+    rows_out = (torch.bfloat16, handle.max_rows * (n if kind < 0 else n // 2)) if oq == 0 else (None, None)
     stream = _check_here(
-        stream, (a_buf, "a_buf", None, None, None), (w, "w", None, (E, *shape), None),
-        (w_scales, "w_scales", torch.float32, (E, shape[0] // 128, shape[1] // 128), None),
-        (out, "out", torch.bfloat16 if _quant(out_quant) == 0 else None, None,
-         handle.max_rows * width if _quant(out_quant) == 0 else None),
+        stream, (a_buf, "a_buf", None, None, None), (w, "w", None, (E, wn, wk), None),
+        (w_scales, "w_scales", torch.float32, (E, wn // 128, wk // 128), None), (out, "out", rows_out[0], None, rows_out[1]),
         (recv_count, "recv_count", torch.int64, None, E))
-    _check(_lib.ep_moe_gmm_b128(ctypes.byref(handle), _ptr(recv_count), _ptr(a_buf), _nbytes(a_buf), _quant(a_quant), k,
-                                n, _ptr(w), _ptr(w_scales), int(bool(transposed)), _act(act), _quant(out_quant),
-                                _ptr(out), _nbytes(out), stream))
+    _check(_lib.ep_moe_gmm_b128(ctypes.byref(handle), _ptr(recv_count), a_buf.data_ptr(), _nbytes(a_buf), aq, k, n,
+                                _ptr(w), _ptr(w_scales), int(bool(transposed)), kind, oq, out.data_ptr(), _nbytes(out),
+                                stream))
 
 
 def ep_read_status(handle: ep_handle_t, stream=None) -> int:
