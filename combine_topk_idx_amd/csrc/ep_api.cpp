@@ -732,6 +732,12 @@ ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, co
 
 namespace {
 
+// Whether a launch's tiles of `rows` rows and `n` columns can be counted in
+// 32 bits, four pieces a tile (more would not fit the memory either).
+bool tiles_fit(int64_t rows, int64_t experts, int64_t n) {
+  return (rows / 256 + experts) * (n / 128 + 1) < ((int64_t)1 << 28);
+}
+
 // what ep_ffn and ep_ffn_backward have in common
 ep_status_t check_ffn(const char *fn, const ep_handle_t *handle, const int64_t *recv_count, const void *x_buf,
                       size_t x_buf_bytes, int32_t hidden, int32_t inter, int act, const void *w1, const void *w2,
@@ -744,6 +750,9 @@ ep_status_t check_ffn(const char *fn, const ep_handle_t *handle, const int64_t *
                 inter);
   if (hidden > kMaxHidden || inter > kMaxHidden)
     return fail(EP_ERR_UNSUPPORTED, "%s: hidden / inter above %d", fn, kMaxHidden);
+  if (!tiles_fit(handle->max_rows, handle->num_experts, hidden > 2 * inter ? hidden : 2 * inter))
+    return fail(EP_ERR_UNSUPPORTED, "%s: %lld rows of %d and %d columns are more than a launch counts", fn,
+                (long long)handle->max_rows, hidden, inter);
   if (act != EP_ACT_SILU && act != EP_ACT_GELU)
     return fail(EP_ERR_INVALID_ARG, "%s: act must be EP_ACT_SILU or EP_ACT_GELU (got %d)", fn, act);
   if (ck_quant != EP_QUANT_NONE && ck_quant != EP_QUANT_FP8_B128)
@@ -852,6 +861,9 @@ ep_status_t ep_moe_gmm_b128(const ep_handle_t *handle, const int64_t *recv_count
   if (k <= 0 || k % 128 != 0 || n <= 0 || n % (gated ? 256 : 128) != 0)
     return fail(EP_ERR_INVALID_ARG, "%s: need k %% 128 == 0 and n %% %d == 0 (got %d, %d)", fn, gated ? 256 : 128, k, n);
   if (k > kMaxHidden || n > kMaxHidden) return fail(EP_ERR_UNSUPPORTED, "%s: k / n above %d", fn, kMaxHidden);
+  if (!tiles_fit(handle->max_rows, handle->num_experts, n))
+    return fail(EP_ERR_UNSUPPORTED, "%s: %lld rows of %d columns are more than a launch counts", fn,
+                (long long)handle->max_rows, n);
   if (transposed != 0 && transposed != 1) return fail(EP_ERR_INVALID_ARG, "%s: transposed must be 0 or 1", fn);
   if (transposed && gated) return fail(EP_ERR_INVALID_ARG, "%s: the transposed product takes no act", fn);
   if (out_quant != EP_QUANT_NONE && !(gated && ep::is_b128(out_quant)))

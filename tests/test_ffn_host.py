@@ -54,7 +54,7 @@ BOTH_BAD = [
     (dict(out=FAKE + 5 * GAP + 2), 1), (dict(ob=ROWS - 1), 3), (dict(out=FAKE), 1), (dict(out=FAKE + ROWS - 16), 1),
     (dict(hargs=dict(E=513)), 1), (dict(hargs=dict(k=17)), 1), (dict(hargs=dict(max_rows=9)), 1),
     (dict(hargs=dict(align=16), count=None), 1), (dict(hargs=dict(cap=8), count=None), 1),
-    (dict(hargs=dict(offsets=None)), 1),
+    (dict(hargs=dict(offsets=None)), 1), (dict(hargs=dict(T=1 << 30, tmax=1 << 30, k=1), H=65536), 2),
 ]
 
 
@@ -115,6 +115,7 @@ GMM_BAD = [
     (dict(ob=8 * 256 - 1, act=0), 3), (dict(ob=8 * 128 + 31, act=1, oq=2), 3), (dict(out=FAKE), 1),
     (dict(out=FAKE + 1024), 1), (dict(count=FAKE + 4), 1), (dict(hargs=dict(align=16), count=None), 1),
     (dict(hargs=dict(cap=4), count=None), 1), (dict(hargs=dict(E=0)), 1),
+    (dict(hargs=dict(T=1 << 30, tmax=1 << 30, k=1), n=65536), 2),
 ]
 
 

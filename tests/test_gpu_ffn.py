@@ -378,3 +378,106 @@ def test_rows_past_32_bits(ep):
         if at is not None:
             within(f64(gw1[e]), want["grad_w1"], f"grad_w1 {e}")
             within(f64(gw2[e]), want["grad_w2"], f"grad_w2 {e}")
+
+
+class Counted(Rows):
+    """A layout whose experts have the given numbers of rows, tokens in a random order."""
+
+    def __init__(self, ep, counts, seed=0, **layout):
+        g = np.random.default_rng(seed)
+        ids = g.permutation(np.repeat(np.arange(len(counts)), counts))
+        E, T = len(counts), int(sum(counts))
+        row_align = layout.get("row_align", 1)
+        self.idx, self.tmax = ids.reshape(-1, 1), T
+        self.ws = torch.full((ep.ep_workspace_bytes_ex(T, 1, E, row_align, 0),), 0xA5, dtype=torch.uint8, device=DEV)
+        self.count = torch.full((E,), -1, dtype=torch.int64, device=DEV)
+        self.h = ep.ep_layout_ex(torch.from_numpy(self.idx).to(DEV), E, T, row_align, 0, self.count, self.ws)
+        block = -(-np.array(counts) // row_align) * row_align
+        start = np.cumsum(block) - block
+        self.spans = [(e, int(start[e]), int(n)) for e, n in enumerate(counts)]
+        self.held = np.zeros(self.h.max_rows, bool)
+        for _, a, n in self.spans:
+            self.held[a:a + n] = True
+
+
+# rows by expert: last tiles of every height of a 256-row tile (and none), whole tiles only, tiles cut into pieces, sums
+# of one, two, three and more stages
+HEIGHTS = [
+    ([257, 321, 385, 449, 0, 512, 256, 300], 64, 64),
+    ([257, 321, 385, 449, 0, 512, 256, 300], 192, 128),
+    ([255, 256, 193, 254], 320, 192),
+    ([1030], 64, 128),
+    ([4099], 128, 64),
+    ([700, 0, 0, 1], 128, 320),
+    # more units than workgroups, the last round half empty or less: its tiles in 2 pieces
+    ([9001, 8300], 64, 640),
+    # over 32 rows in some experts of a launch of few
+    ([100] + [1] * 14, 192, 128),
+    ([33, 0, 65, 31, 32, 1], 1024, 64),
+]
+
+
+@pytest.mark.parametrize("quant", ["none", "fp8_b128"])
+@pytest.mark.parametrize("i", range(len(HEIGHTS)))
+def test_tile_heights(ep, i, quant):
+    counts, H, I = HEIGHTS[i]
+    if quant != "none":
+        I = -(-I // 128) * 128
+    c = Case(ep, Counted(ep, counts, i, row_align=1 if i % 2 else 16), H, I, "silu", quant, seed=i)
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    c.check_forward()
+    c.check_backward()
+
+
+def test_two_graphs_in_turn(ep):
+    """Two captured steps of different sizes with a workspace each, replayed in turn and together on two streams."""
+    cases = [Case(ep, Rows(ep, 3, T=300, k=2, E=3), 128, 128, "silu", "none"),
+             Case(ep, Rows(ep, 4, T=20, k=2, E=5), 192, 64, "gelu", "none")]
+    outs = lambda c: (c.out, c.gx, c.gw1, c.gw2)   # noqa: E731
+    want, graphs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for c, s in zip(cases, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            c.forward()
+            c.backward()
+            s.synchronize()
+            want.append([t.clone() for t in outs(c)])
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                c.forward()
+                c.backward()
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for turn in range(4):
+        for c in cases:
+            for t in outs(c):
+                t.fill_(CANARY)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s if turn % 2 else streams[0]):
+                g.replay()
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(outs(c), w))
+
+
+def test_many_experts_and_the_same_expert_twice(ep):
+    """512 experts, most without rows; a token routed to one expert twice has two rows."""
+    idx = np.full((40, 2), 7)
+    idx[10:, 1] = np.arange(30) * 17 % 512
+    r = Rows.__new__(Rows)
+    r.ws = torch.zeros(ep.ep_workspace_bytes(40, 2, 512), dtype=torch.uint8, device=DEV)
+    r.count = torch.zeros(512, dtype=torch.int64, device=DEV)
+    r.idx = idx
+    r.h = ep.ep_layout(torch.from_numpy(idx).to(DEV), 512, 40, r.count, r.ws)
+    n = np.bincount(idx.ravel(), minlength=512)
+    start = np.cumsum(n) - n
+    r.spans, r.held = [(e, int(start[e]), int(n[e])) for e in range(512)], np.ones(80, bool)
+    c = Case(ep, r, 64, 64, "silu", "none")
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    c.check_forward()
+    c.check_backward()

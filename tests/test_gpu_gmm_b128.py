@@ -8,7 +8,7 @@ import torch
 from oracle import codecs, ffn as OF
 from tests import moe_bounds as MB
 from tests.hip_path import DEV
-from tests.test_gpu_ffn import BF, CANARY, Rows, f64, within
+from tests.test_gpu_ffn import BF, CANARY, Counted, Rows, f64, within
 
 pytestmark = pytest.mark.gpu
 
@@ -226,3 +226,42 @@ def test_side_stream_and_graph(ep):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(c.out.view(torch.int16), want.view(torch.int16))
+
+
+HEIGHTS = [
+    ([257, 321, 385, 449, 0, 256], 128, 128),
+    ([255, 193, 254], 256, 384),
+    ([700], 384, 512),
+    ([200, 0, 330], 640, 256),
+    ([100] + [1] * 14, 1152, 256),
+    ([33, 0, 65, 31, 32, 1], 256, 128),
+]
+
+
+@pytest.mark.parametrize("form", ["plain", "transposed", "gated"])
+@pytest.mark.parametrize("mode", ["fp8_b128", "fp8_b128_ue8m0"])
+@pytest.mark.parametrize("i", range(len(HEIGHTS)))
+def test_tile_heights(ep, i, mode, form):
+    """Last tiles of every height, tiles cut into pieces, sums of one to nine blocks."""
+    counts, K, N = HEIGHTS[i]
+    c = Case(ep, Counted(ep, counts, i, row_align=1 if i % 2 else 16), K, N if form != "gated" else -(-N // 256) * 256, mode,
+             transposed=form == "transposed", act="silu" if form == "gated" else "none", seed=i)
+    c.run()
+    torch.cuda.synchronize()
+    c.check()
+
+
+@pytest.mark.parametrize("T", [60, 500])
+def test_nan_codes_and_scales_stay_in_their_rows(ep, T):
+    c = Case(ep, Rows(ep, 6, T=T, k=1, E=2), 256, 256, "fp8_b128")
+    c.run()
+    want = c.out.clone()
+    E, R, K, N = c.dims
+    c.buf[3 * K + 5] = 0x7F                                    # a NaN code in row 3
+    at = ep.ep_buffer_bytes(R, K, "fp8_b128")[1]
+    c.buf[at + (R - 2) * 8: at + (R - 2) * 8 + 4].view(torch.float32).fill_(float("inf"))
+    c.run()
+    bad = torch.zeros(R + 1, dtype=torch.bool, device=DEV)
+    bad[3] = bad[R - 2] = True
+    assert torch.equal(c.out[~bad], want[~bad])
+    assert c.out[3].isnan().all() and not torch.isfinite(c.out[R - 2]).any()
