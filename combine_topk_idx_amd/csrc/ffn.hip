@@ -5,6 +5,22 @@
 // Every product runs on the core of gemm_core.hpp: both projections, the
 // activation, the product of the two and the checkpoint in one launch; the
 // activation's gradient in the epilogue of dy W2.
+//
+// Roundings to bf16: a, dg and du, because they are the next product's operands
+// on the matrix cores; the checkpoint (or e4m3 with a scale per 128); the
+// outputs.  Sums, the activation and its gradient are float32.
+//
+// Launches: forward 2, backward 3 (dy W2 with a, dg, du; dx; both weight
+// gradients).  What bounds them, and what they take:
+//   few rows an expert    the weights' bytes (figures at TileFew)
+//   32 to 192 rows        a few tiles a CU: the last round and the stages' latency.
+//                         64 experts of 129 rows, 2048 -> 2 x 768, 8-bit checkpoint:
+//                         gate and up 157 us, down 63, dy W2 74, dx 108, weights 207
+//   many                  the matrix cores at the clock that the power limit leaves.
+//                         32768 rows in 32 experts, 7168 -> 2 x 2048: gate and up
+//                         1.60 ms (1.20 PFLOP/s), down 0.87 (1.10), dy W2 1.12 (0.86:
+//                         its epilogue reads and writes 540 MB), dx 1.76 (1.10),
+//                         weights 2.83 (1.02: sums of 1024 rows, 2.8 GB written)
 #include "ffn.hpp"
 #include "gemm_core.hpp"
 
@@ -399,6 +415,7 @@ __global__ __launch_bounds__(Tile256::kThreads) void rows256_kernel(RowArgs p) {
 
 // Few rows an expert (kUp without an 8-bit checkpoint, kDown): sums joined over
 // the waves, wave w then has columns 8 w + 4 (l / 32) + 0..3 of row l % 32.
+// Bounded by the weights' bytes, in small models by the launch (at TileFew).
 template <int MODE>
 __global__ __launch_bounds__(TileFew::kThreads) void few_kernel(RowArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -499,7 +516,13 @@ struct WeightArgs {
 
 // out[e] = R_e^T C_e over the rows of expert e (zeros without rows), for both
 // weights in one launch: fewer units left over, and the last units, where
-// they would fill less than half of a round, are cut into 2 or 4 pieces.
+// they would fill at most half of a round, are cut into 2 or 4 pieces.  Both
+// operands are k strided and are read through the transposing LDS reads.  A sum
+// is as long as an expert's rows, so short ones are bounded by the gradients'
+// bytes: 64 experts of 129 rows, 2048 x 2 x 768 and 768 x 2048: 604 MB written
+// in 207 us (240 before the stores left in whole lines, unwaited).  One expert
+// of 8192 rows, 4096 x 2 x 1408 and 1408 x 4096: 320 us, 886 TFLOP/s (272 tiles
+// on 256 CUs).
 __global__ __launch_bounds__(Tile256::kThreads) void weights256_kernel(WeightArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__
   typedef Tile256 S;
