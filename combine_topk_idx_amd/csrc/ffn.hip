@@ -430,76 +430,75 @@ __global__ __launch_bounds__(TileFew::kThreads) void few_kernel(RowArgs p) {
   const int nc = (p.n + kCols - 1) / kCols;
   const int units = uniform(g.first[p.E]) * nc;
   PipeFew<2> pipe;
-  RowTile u;
-  int n0;
-  auto none = [](int, int) {};
-  auto start = [&](int unit) {
-    u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
-    n0 = u.tc * kCols;
-    const Source lo = weights_of<MODE>(p, u.e, n0, false, 32);
-    const Source hi = kSplit ? weights_of<MODE>(p, u.e, n0, true, 32) : Source{lo.base + 32 * lo.pitch, lo.pitch, 32};
-    pipe.init(lo, hi, Source{p.r + u.row0 * p.k * 2, (int64_t)p.k * 2, u.rows}, p.k, lds, wave, lane);
-    pipe.begin(none);
+  pipe.init((int64_t)p.k * 2, (int64_t)p.k * 2, p.k, lds, wave, lane);
+  struct Unit {
+    RowTile u;
+    int n0;
   };
-  int unit = unit_of_round(0);
-  if (unit >= units) return;
-  start(unit);
-  for (int round = 1;; ++round) {
-    v16f acc[2] = {};
-    for (int i = 0; i < pipe.steps; ++i) {
-      pipe.next<0>(i, none);
-      const lds_u8 *at = pipe.stage(i);
+  v16f acc[2];
+  few_units<2, 0>(
+      pipe, units,
+      [&](int unit) {
+        Unit x{row_tile(g, p.E, p.offsets, unit, nc, S::BM), 0};
+        x.n0 = x.u.tc * kCols;
+        pipe.c[0] = weights_of<MODE>(p, x.u.e, x.n0, false, 32);
+        pipe.c[1] = kSplit ? weights_of<MODE>(p, x.u.e, x.n0, true, 32)
+                           : Source{pipe.c[0].base + 32 * pipe.c[0].pitch, pipe.c[0].pitch, 32};
+        pipe.r = Source{p.r + x.u.row0 * p.k * 2, (int64_t)p.k * 2, x.u.rows};
+        return x;
+      },
+      [](int, int) {}, [&](const Unit &) { acc[0] = acc[1] = v16f{}; },
+      [&](const Unit &, int, int b) {
+        const lds_u8 *at = pipe.stage(b);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const bf16x8 r = pipe.rd.bf16(at + 64 * kKBytes, 0, 0, s);
+        for (int s = 0; s < 4; ++s) {
+          const bf16x8 r = pipe.rd.bf16(at + 64 * kKBytes, 0, 0, s);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pipe.rd.bf16(at, 0, c * 32, s), r, acc[c], 0, 0, 0);
+        }
+      },
+      [&](const Unit &done, auto join) {
+        typedef __attribute__((address_space(3))) v4f lds_v4f;
+        const int own = join(wave);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          acc[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(pipe.rd.bf16(at, 0, c * 32, s), r, acc[c], 0, 0, 0);
-      }
-    }
-    wait_lds();
-    const RowTile done = u;
-    const int done_n0 = n0;
-    unit = unit_of_round(round);
-    if (unit < units) start(unit);                           // into the wave's own first two buffers
-    typedef __attribute__((address_space(3))) v4f lds_v4f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+          for (int b = 0; b < 4; ++b)
+            *(lds_v4f *)(lds + own + ((c * 4 + b) * kWave + lane) * 16) =
+                v4f{acc[c][4 * b], acc[c][4 * b + 1], acc[c][4 * b + 2], acc[c][4 * b + 3]};
+        lds_barrier();
+        v4f sum[2] = {};
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *(lds_v4f *)(lds + wave * S::kMine + S::kJoin + ((c * 4 + b) * kWave + lane) * 16) =
-            v4f{acc[c][4 * b], acc[c][4 * b + 1], acc[c][4 * b + 2], acc[c][4 * b + 3]};
-    lds_barrier();
-    v4f sum[2] = {};
+        for (int w = 0; w < S::kWaves; ++w) {
+          const int at = join(w);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int w = 0; w < S::kWaves; ++w)
-        sum[c] += *(const lds_v4f *)(lds + w * S::kMine + S::kJoin + ((c * 4 + wave) * kWave + lane) * 16);
-    lds_barrier();                                           // before a third stage goes there
-    const int64_t row = done.row0 + (lane & 31);
-    if ((lane & 31) < done.rows) {
-      auto store4 = [](char *dst, const v4f &v) { *(u32x2 *)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
-      const int n = done_n0 + 8 * wave + 4 * half;
-      if constexpr (kSplit) {
-        v4f a;
-        with_act(p.act, [&](auto kind) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = act<decltype(kind)::value>(sum[0][i]) * sum[1][i];
-        });
-        store4(p.out + (row * p.n + n) * 2, a);
-        if (p.ck_form == kCkBf16) {
-          char *q = p.ck + (row * 2 * p.n + n) * 2;
-          store4(q, sum[0]);
-          store4(q + (int64_t)p.n * 2, sum[1]);
+          for (int c = 0; c < 2; ++c) sum[c] += *(const lds_v4f *)(lds + at + ((c * 4 + wave) * kWave + lane) * 16);
         }
-      } else {
-        store4(p.out + (row * p.n + n) * 2, sum[0]);
-        store4(p.out + (row * p.n + n + 32) * 2, sum[1]);
-      }
-    }
-    if (unit >= units) return;
-  }
+        lds_barrier();                                       // before a stage goes there
+        const int64_t row = done.u.row0 + (lane & 31);
+        if ((lane & 31) >= done.u.rows) return;
+        auto store4 = [](char *dst, const v4f &v) {
+          *(u32x2 *)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        };
+        const int n = done.n0 + 8 * wave + 4 * half;
+        if constexpr (kSplit) {
+          v4f a;
+          with_act(p.act, [&](auto kind) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = act<decltype(kind)::value>(sum[0][i]) * sum[1][i];
+          });
+          store4(p.out + (row * p.n + n) * 2, a);
+          if (p.ck_form == kCkBf16) {
+            char *q = p.ck + (row * 2 * p.n + n) * 2;
+            store4(q, sum[0]);
+            store4(q + (int64_t)p.n * 2, sum[1]);
+          }
+        } else {
+          store4(p.out + (row * p.n + n) * 2, sum[0]);
+          store4(p.out + (row * p.n + n + 32) * 2, sum[1]);
+        }
+      });
 #endif
 }
 

@@ -481,65 +481,119 @@ struct PipeN {
 // wave order through LDS.  64 columns (gated: 32 gate rows and the same 32 up
 // rows) make units enough for the whole card in small models.  k contiguous
 // operands.  Measured: 5 tokens, two of 8 experts 1024 -> 2 x 512, bf16 gate and
-// up 6.8 us, down 5.5 (together 19 with common stages): launch, first load and
-// join; 128 tokens, 6 of 64 experts 2048 -> 2 x 768: 403 MB of
-// gate and up weights in 84 us, 4.8 TB/s; 128 tokens, 8 of 256 e4m3 experts
-// 7168 -> 2 x 2048: 7.4 GB in 1180 us, 6.3 TB/s, the card's rate of reads.
+// up 7.7 us, down 5.7 (together 19 with common stages): launch, first load and
+// join; 128 tokens, 6 of 64 experts 2048 -> 2 x 768: 403 MB of gate and up
+// weights in 82 us, 4.9 TB/s, 201 MB of down weights in 45 (85 and 49 when a
+// unit's first stages were fetched after the last of the one before had
+// arrived); 128 tokens, 8 of 256 e4m3 experts 7168 -> 2 x 2048: 7.4 GB in 1165
+// us, 6.35 TB/s, the card's rate of reads.
 struct TileFew {
   static constexpr int BN = 64, BM = 32, kWaves = 4, kThreads = kWaves * kWave;
   static constexpr int kStage = (BN + BM) * kKBytes, kBuffers = 3;
   static constexpr int kMine = kBuffers * kStage, kLds = kWaves * kMine;
-  // where the sums are joined: each wave's last buffer, which the next unit's
-  // first two stages leave alone
-  static constexpr int kJoin = 2 * kStage;
 };
 
+// A wave's stages run through its buffers in turn, from one unit into the next:
+// two are in flight at any time, also while a unit's sums are joined and
+// written.  The sums are joined in the buffer that each wave read last, which is
+// the one that no stage in flight goes to.
 template <int EB>
 struct PipeFew {
   static constexpr int kSteps = kKBytes / EB, kLoads = TileFew::kStage / 1024;
-  static constexpr int kCFrags = EB == 2 ? 2 : 4, kRFrags = EB == 2 ? 1 : 2, kWide = EB == 2 ? 32 : 16;
   typedef Loader<32, false, EB, 1, false> L;                 // 32 rows, 4 loads
-  Source c[2], r;                                            // columns 0..31, 32..63
+  Source c[2], r;                                            // columns 0..31, 32..63, of the unit being fetched
   L lc, lr;
   Reader<32, false, EB, 1> rd;
-  int steps, first;                                          // the wave's stages: first, first + 4, ..
+  int all, steps, first;                                     // stages of a unit; the wave's: first, first + 4, ..
+  int fetched, flying, to, from;                             // of that unit; in flight; buffers fetched to, read from
   lds_u8 *mine;
 
-  __device__ __forceinline__ void init(const Source &lo, const Source &hi, const Source &rs, int k, lds_u8 *lds, int wave,
-                                       int lane) {
-    c[0] = lo;
-    c[1] = hi;
-    r = rs;
-    lc.init(0, lane, lo);
-    lr.init(0, lane, rs);
+  // the waves' stages of a unit
+  __device__ __forceinline__ int steps_of(int wave) const { return (all - wave + TileFew::kWaves - 1) / TileFew::kWaves; }
+  __device__ __forceinline__ void init(int64_t c_pitch, int64_t r_pitch, int k, lds_u8 *lds, int wave, int lane) {
+    lc.init(0, lane, Source{nullptr, c_pitch, 32});
+    lr.init(0, lane, Source{nullptr, r_pitch, 32});
     rd.init(lane, 0, [](int) { return 0; });
     first = wave;
-    const int all = k / kSteps;
-    steps = all > wave ? (all - wave + TileFew::kWaves - 1) / TileFew::kWaves : 0;
+    all = k / kSteps;
+    steps = steps_of(wave);
+    fetched = flying = to = from = 0;
     mine = lds + wave * TileFew::kMine;
   }
-  __device__ __forceinline__ lds_u8 *stage(int i) const { return mine + i % TileFew::kBuffers * TileFew::kStage; }
+  static __device__ __forceinline__ int after(int buffer) { return buffer + 1 == TileFew::kBuffers ? 0 : buffer + 1; }
+  __device__ __forceinline__ lds_u8 *stage(int buffer) const { return mine + buffer * TileFew::kStage; }
+  // the next stage of the unit being fetched; extra(t, buffer)
   template <class F>
-  __device__ __forceinline__ void fetch(int i, F extra) const {
-    const int t = first + i * TileFew::kWaves;
-    lds_u8 *at = stage(i);
+  __device__ __forceinline__ void fetch(F extra) {
+    const int t = first + fetched * TileFew::kWaves;
+    lds_u8 *at = stage(to);
     lc.load(at, c[0], t, kSteps);
     lc.load(at + 32 * kKBytes, c[1], t, kSteps);
     lr.load(at + 64 * kKBytes, r, t, kSteps);
-    extra(t, i);
+    extra(t, to);
+    to = after(to);
+    ++fetched;
+    ++flying;
   }
-  template <class F>
-  __device__ __forceinline__ void begin(F extra) const {
-    for (int i = 0; i < 2 && i < steps; ++i) fetch(i, extra);
-  }
-  // The wave's stage i is there; stage i + 2 is fetched over stage i - 1.
-  template <int EXTRA, class F>
-  __device__ __forceinline__ void next(int i, F extra) const {
-    if (i + 1 < steps) wait_loads<kLoads + EXTRA>();
+  // The oldest stage in flight is there: in the buffer returned.
+  template <int EXTRA>
+  __device__ __forceinline__ int arrived() {
+    if (flying > 1) wait_loads<kLoads + EXTRA>();
     else wait_loads<0>();
-    if (i + 2 < steps) fetch(i + 2, extra);
+    --flying;
+    const int b = from;
+    from = after(from);
+    return b;
+  }
+  // Where wave w has its sums, `units`: how many have been read (mod 3).
+  __device__ __forceinline__ int join_of(int w, int units) const {
+    return w * TileFew::kMine + (units * steps_of(w) + TileFew::kBuffers - 1) % TileFew::kBuffers * TileFew::kStage;
   }
 };
+
+// The units of a workgroup on that pipe, one after the other.
+//   open(unit)        sets the pipe's sources to a unit's, returns what finish() needs
+//   extra(t, buffer)  issues EXTRA more loads with a stage
+//   work(now, i, b)   the wave's i-th stage of the unit `now`, in buffer b
+//   finish(now, join) the unit's sums are complete in registers; join(w): wave w's place
+template <int EB, int EXTRA, class Open, class Extra, class Begin, class Work, class Finish>
+__device__ __forceinline__ void few_units(PipeFew<EB> &p, int units, Open open, Extra extra, Begin begin, Work work,
+                                          Finish finish) {
+  int next = unit_of_round(0);
+  if (next >= units) return;                                 // uniform; later rounds only have larger units
+  auto now = open(next);
+  next = unit_of_round(1);
+  auto coming = now;
+  bool opened = false;                                       // the next unit, which stages are fetched of
+  auto fetch = [&] {
+    if (p.fetched == p.steps) {
+      if (opened || next >= units || p.steps == 0) return;
+      coming = open(next);
+      p.fetched = 0;
+      opened = true;
+    }
+    p.fetch(extra);
+  };
+  for (int round = 2, done = 1;; ++round, done = done == 2 ? 0 : done + 1) {
+    begin(now);
+    while (p.flying < 2 && p.fetched < p.steps) fetch();     // before the first unit
+    for (int i = 0; i < p.steps; ++i) {
+      const int b = p.template arrived<EXTRA>();
+      if (p.flying < 2) fetch();
+      work(now, i, b);
+    }
+    wait_lds();
+    finish(now, [&](int w) { return p.join_of(w, done); });
+    if (next >= units) return;
+    if (!opened) {                                           // a wave without stages
+      coming = open(next);
+      p.fetched = 0;
+    }
+    now = coming;
+    opened = false;
+    next = unit_of_round(round);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // the 256 x 256 tile

@@ -406,95 +406,98 @@ __global__ __launch_bounds__(TileFew::kThreads) void few_kernel(GmmArgs p) {
   const int nc = (p.n + kCols - 1) / kCols;
   const int units = uniform(g.first[p.E]) * nc;
   PipeFew<1> pipe;
-  RowTile u;
-  int n0;
-  u32x4 scales;
+  pipe.init(p.k, p.k, p.k, lds, wave, lane);
+  struct Unit {
+    RowTile u;
+    int n0;
+    const_floats sw;                                         // the unit's weight scales by block of k
+  };
+  u32x4 scales;                                              // row scales of the unit being fetched
   const lds_u8 *area = lds + S::kLds + wave * S::kBuffers * kArea;
   const uint32_t area_to = (uint32_t)(uintptr_t)area;
   const int scale_row = lane * kb * kScale;                  // rows past the tile's are past the range
-  auto fetch_scales = [&](int t, int i) {
-    load_lds4<BYTES>(area_to + i % S::kBuffers * kArea, scale_row, scales, t * kScale);
-  };
-  auto start = [&](int unit) {
-    u = row_tile(g, p.E, p.offsets, unit, nc, S::BM);
-    n0 = u.tc * kCols;
-    scales = descriptor(p.r_scales + u.row0 * kb * kScale, (uint32_t)(u.rows * kb * kScale));
-    const Source lo = weights_of<false, GATED>(p, u.e, n0, false, 32);
-    const Source hi = GATED ? weights_of<false, GATED>(p, u.e, n0, true, 32) : Source{lo.base + 32 * lo.pitch, lo.pitch, 32};
-    pipe.init(lo, hi, Source{p.r + u.row0 * p.k, p.k, u.rows}, p.k, lds, wave, lane);
-    pipe.begin(fetch_scales);
-  };
-  int unit = unit_of_round(0);
-  if (unit >= units) return;
-  start(unit);
-  for (int round = 1;; ++round) {
-    v4f acc[4][2] = {};
-    // 64 columns lie in one block of 128 (gated: 32 gate and 32 up columns)
-    const int nb_all = GATED ? 2 * p.n / 128 : p.n / 128;
-    const const_floats sw = (const_floats)(p.c_scales + ((int64_t)u.e * nb_all + n0 / 128) * kb);
-    const int64_t up = GATED ? (int64_t)(p.n / 128) * kb : 0;
-    for (int i = 0; i < pipe.steps; ++i) {
-      const int t = pipe.first + i * S::kWaves;
-      const float w[2] = {sw[t], GATED ? sw[t + up] : 0.0f};
-      pipe.next<1>(i, fetch_scales);
-      const lds_u8 *at = pipe.stage(i);
-      v8i fr[2];
-      float sr[2];
+  // 64 columns lie in one block of 128 (gated: 32 gate and 32 up columns)
+  const int nb_all = GATED ? 2 * p.n / 128 : p.n / 128;
+  const int64_t up = GATED ? (int64_t)(p.n / 128) * kb : 0;
+  v4f acc[4][2];
+  few_units<1, 1>(
+      pipe, units,
+      [&](int unit) {
+        Unit x{row_tile(g, p.E, p.offsets, unit, nc, S::BM), 0, nullptr};
+        x.n0 = x.u.tc * kCols;
+        x.sw = (const_floats)(p.c_scales + ((int64_t)x.u.e * nb_all + x.n0 / 128) * kb);
+        scales = descriptor(p.r_scales + x.u.row0 * kb * kScale, (uint32_t)(x.u.rows * kb * kScale));
+        pipe.c[0] = weights_of<false, GATED>(p, x.u.e, x.n0, false, 32);
+        pipe.c[1] = GATED ? weights_of<false, GATED>(p, x.u.e, x.n0, true, 32)
+                          : Source{pipe.c[0].base + 32 * pipe.c[0].pitch, pipe.c[0].pitch, 32};
+        pipe.r = Source{p.r + x.u.row0 * p.k, p.k, x.u.rows};
+        return x;
+      },
+      [&](int t, int b) { load_lds4<BYTES>(area_to + b * kArea, scale_row, scales, t * kScale); },
+      [&](const Unit &) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        fr[j] = pipe.rd.fp8(at + 64 * kKBytes, 0, j * 16);
-        const uint32_t v = *(const __attribute__((address_space(3))) uint32_t *)(
-            area + i % S::kBuffers * kArea + (j * 16 + (lane & 15)) * 4);
-        sr[j] = BYTES ? e8m0_decode(v) : __uint_as_float(v);
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const v8i fc = pipe.rd.fp8(at, 0, c * 16);
+        for (int c = 0; c < 4; ++c) acc[c][0] = acc[c][1] = v4f{};
+      },
+      [&](const Unit &now, int i, int b) {
+        const int t = pipe.first + i * S::kWaves;
+        const float w[2] = {now.sw[t], GATED ? now.sw[t + up] : 0.0f};
+        const lds_u8 *at = pipe.stage(b);
+        v8i fr[2];
+        float sr[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const v4f q = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fc, fr[j], v4f{}, 0, 0, 0, 0, 0, 0);
-          const float by = sr[j] * w[GATED ? c >> 1 : 0];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) acc[c][j][x] = __builtin_fmaf(q[x], by, acc[c][j][x]);
+          fr[j] = pipe.rd.fp8(at + 64 * kKBytes, 0, j * 16);
+          const uint32_t v =
+              *(const __attribute__((address_space(3))) uint32_t *)(area + b * kArea + (j * 16 + (lane & 15)) * 4);
+          sr[j] = BYTES ? e8m0_decode(v) : __uint_as_float(v);
         }
-      }
-    }
-    wait_lds();
-    const RowTile done = u;
-    const int done_n0 = n0;
-    unit = unit_of_round(round);
-    if (unit < units) start(unit);                           // into the wave's own first two buffers
-    typedef __attribute__((address_space(3))) v4f lds_v4f;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          const v8i fc = pipe.rd.fp8(at, 0, c * 16);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *(lds_v4f *)(lds + wave * S::kMine + S::kJoin + ((c * 2 + j) * kWave + lane) * 16) = acc[c][j];
-    lds_barrier();
-    // gated: gate and up of one fragment; else one column fragment, both row fragments
-    const int first = GATED ? (wave & 1) * 2 + (wave >> 1) : wave * 2, second = GATED ? first + 4 : first + 1;
-    v4f a = {}, b = {};
+          for (int j = 0; j < 2; ++j) {
+            const v4f q = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fc, fr[j], v4f{}, 0, 0, 0, 0, 0, 0);
+            const float by = sr[j] * w[GATED ? c >> 1 : 0];
 #pragma unroll
-    for (int w = 0; w < S::kWaves; ++w) {
-      a += *(const lds_v4f *)(lds + w * S::kMine + S::kJoin + (first * kWave + lane) * 16);
-      b += *(const lds_v4f *)(lds + w * S::kMine + S::kJoin + (second * kWave + lane) * 16);
-    }
-    lds_barrier();                                           // before a third stage goes there
-    auto store4 = [](char *dst, const v4f &v) { *(u32x2 *)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}; };
-    const int row = (lane & 15) + (GATED ? wave >> 1 : 0) * 16, n = done_n0 + (GATED ? wave & 1 : wave) * 16 + 4 * (lane >> 4);
-    char *dst = p.out + ((done.row0 + row) * p.n + n) * 2;
-    if constexpr (GATED) {
-      with_act(p.act, [&](auto kind) {
+            for (int x = 0; x < 4; ++x) acc[c][j][x] = __builtin_fmaf(q[x], by, acc[c][j][x]);
+          }
+        }
+      },
+      [&](const Unit &done, auto join) {
+        typedef __attribute__((address_space(3))) v4f lds_v4f;
+        const int own = join(wave);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = act<decltype(kind)::value>(a[i]) * b[i];
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) *(lds_v4f *)(lds + own + ((c * 2 + j) * kWave + lane) * 16) = acc[c][j];
+        lds_barrier();
+        // gated: gate and up of one fragment; else one column fragment, both row fragments
+        const int first = GATED ? (wave & 1) * 2 + (wave >> 1) : wave * 2, second = GATED ? first + 4 : first + 1;
+        v4f a = {}, b = {};
+#pragma unroll
+        for (int w = 0; w < S::kWaves; ++w) {
+          const int at = join(w);
+          a += *(const lds_v4f *)(lds + at + (first * kWave + lane) * 16);
+          b += *(const lds_v4f *)(lds + at + (second * kWave + lane) * 16);
+        }
+        lds_barrier();                                       // before a stage goes there
+        auto store4 = [](char *dst, const v4f &v) {
+          *(u32x2 *)dst = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        };
+        const int row = (lane & 15) + (GATED ? wave >> 1 : 0) * 16;
+        const int n = done.n0 + (GATED ? wave & 1 : wave) * 16 + 4 * (lane >> 4);
+        char *dst = p.out + ((done.u.row0 + row) * p.n + n) * 2;
+        if constexpr (GATED) {
+          with_act(p.act, [&](auto kind) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = act<decltype(kind)::value>(a[i]) * b[i];
+          });
+          if (row < done.u.rows) store4(dst, a);
+        } else {
+          if (row < done.u.rows) store4(dst, a);
+          if (row + 16 < done.u.rows) store4(dst + (int64_t)16 * p.n * 2, b);
+        }
       });
-      if (row < done.rows) store4(dst, a);
-    } else {
-      if (row < done.rows) store4(dst, a);
-      if (row + 16 < done.rows) store4(dst + (int64_t)16 * p.n * 2, b);
-    }
-    if (unit >= units) return;
-  }
 #endif
 }
 

@@ -431,6 +431,30 @@ def test_tile_heights(ep, i, quant):
     c.check_backward()
 
 
+def few_rows(E, seed):
+    """Rows by expert: none to three, 20 and 45 in some."""
+    n = np.random.default_rng(seed).integers(0, 4, size=E)
+    n[:: 9], n[4:: 31] = 20, 45
+    return n
+
+
+# H and I: from one stage of 64 to eleven, so that waves have none, one and more of them
+@pytest.mark.parametrize("ck", [False, True])
+@pytest.mark.parametrize("H, I", [(64, 640), (128, 704), (192, 576), (320, 512), (1344, 64), (1088, 128), (1024, 192),
+                                  (576, 320)])
+def test_few_rows_many_units_a_workgroup(ep, H, I, ck):
+    c = Case(ep, Counted(ep, few_rows(150, H)), H, I, "gelu", "none", seed=I)
+    assert (c.rows.held.sum() + 149) // 150 <= 32
+    c.forward()                                              # fills the checkpoint that check_forward reads
+    if not ck:
+        first = c.out.clone()
+        c.out.fill_(CANARY)
+        c.forward(ck=False)
+        assert torch.equal(first, c.out)
+    torch.cuda.synchronize()
+    c.check_forward()
+
+
 def test_two_graphs_in_turn(ep):
     """Two captured steps of different sizes with a workspace each, replayed in turn and together on two streams."""
     cases = [Case(ep, Rows(ep, 3, T=300, k=2, E=3), 128, 128, "silu", "none"),

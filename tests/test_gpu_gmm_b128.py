@@ -8,7 +8,7 @@ import torch
 from oracle import codecs, ffn as OF
 from tests import moe_bounds as MB
 from tests.hip_path import DEV
-from tests.test_gpu_ffn import BF, CANARY, Counted, Rows, f64, within
+from tests.test_gpu_ffn import BF, CANARY, Counted, Rows, f64, few_rows, within
 
 pytestmark = pytest.mark.gpu
 
@@ -246,6 +246,16 @@ def test_tile_heights(ep, i, mode, form):
     counts, K, N = HEIGHTS[i]
     c = Case(ep, Counted(ep, counts, i, row_align=1 if i % 2 else 16), K, N if form != "gated" else -(-N // 256) * 256, mode,
              transposed=form == "transposed", act="silu" if form == "gated" else "none", seed=i)
+    c.run()
+    torch.cuda.synchronize()
+    c.check()
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("mode", ["fp8_b128", "fp8_b128_ue8m0"])
+@pytest.mark.parametrize("K", [128, 256, 384, 640, 1152])
+def test_few_rows_many_units_a_workgroup(ep, K, mode, act):
+    c = Case(ep, Counted(ep, few_rows(60, K)), K, 1024, mode, act=act, seed=K)
     c.run()
     torch.cuda.synchronize()
     c.check()
