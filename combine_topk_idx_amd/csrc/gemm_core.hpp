@@ -1052,16 +1052,22 @@ __device__ __forceinline__ void store_codes_pair(char *dst, int lane, bool ok, c
 // e^z as 2^(z log2 e): the product's rounding costs |z| 2^-24 of the value
 __device__ __forceinline__ float fast_exp(float z) { return __builtin_amdgcn_exp2f(z * 1.44269504f); }
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-z)); }
-// The normal distribution by Abramowitz and Stegun 7.1.26 (the error function
-// within 1.5e-7), at a sixth of erfcf's instructions; tail: e^(-z^2 / 2), which
-// the density needs too.
+// The normal distribution: Phi(-|z|) = tail t P(t) with t = 1 / (1 + 0.3625 |z|)
+// and P the polynomial of degree 6 with the smallest largest relative error
+// (8e-7) over |z| <= 13.6, below which Phi is no float32; tail: e^(-z^2 / 2),
+// which the density needs too.  Relative to the value also far below zero,
+// where the up value may be large: within 2^-18 + z^2 2^-23.  (7.1.26 of
+// Abramowitz and Stegun, two multiply-adds shorter, bounds the absolute error
+// alone: 0.36 % off at z = -6, a bf16 step, and 3.4 % at -12.5.)
 __device__ __forceinline__ float normal_cdf(float z, float tail) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.23164189f, 1.0f));
-  float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
-  q = __builtin_fmaf(t, q, 1.421413741f);
-  q = __builtin_fmaf(t, q, -0.284496736f);
-  q = __builtin_fmaf(t, q, 0.254829592f);
-  q = 0.5f * t * q * tail;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.3625f, 1.0f));
+  float q = __builtin_fmaf(t, 0.04806285f, -0.17974226f);
+  q = __builtin_fmaf(t, q, 0.17510378f);
+  q = __builtin_fmaf(t, q, 0.02968257f);
+  q = __builtin_fmaf(t, q, 0.13925666f);
+  q = __builtin_fmaf(t, q, 0.14293639f);
+  q = __builtin_fmaf(t, q, 0.14470038f);
+  q = t * q * tail;
   return z > 0.0f ? 1.0f - q : q;
 }
 
