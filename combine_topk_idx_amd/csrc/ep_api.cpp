@@ -47,11 +47,11 @@ bool valid_quant(int q) {
 
 constexpr int32_t kMaxHidden = 65536;
 
-ep_status_t check_hidden(int32_t hidden, int quant, const char *fn) {
+ep_status_t check_hidden(int32_t hidden, int quant, const char *fn, int32_t most = kMaxHidden) {
   if (!valid_quant(quant)) return fail(EP_ERR_INVALID_ARG, "%s: unknown quant mode %d", fn, quant);
   if (hidden <= 0 || hidden % 32 != 0)
     return fail(EP_ERR_INVALID_ARG, "%s: hidden must be a positive multiple of 32 (got %d)", fn, hidden);
-  if (hidden > kMaxHidden) return fail(EP_ERR_UNSUPPORTED, "%s: hidden %d exceeds %d", fn, hidden, kMaxHidden);
+  if (hidden > most) return fail(EP_ERR_UNSUPPORTED, "%s: hidden %d exceeds %d", fn, hidden, most);
   if (ep::is_b128(quant & ep::kQuantMask) && hidden % 128 != 0)
     return fail(EP_ERR_INVALID_ARG, "%s: per-128 e4m3 needs hidden %% 128 == 0 (got %d)", fn, hidden);
   return EP_OK;
@@ -110,7 +110,8 @@ size_t ep_workspace_bytes_ex(int64_t num_max_dispatch_tokens, int32_t num_topk, 
 ep_status_t ep_buffer_bytes(int64_t rows, int32_t hidden, ep_quant_t quant, size_t *total_bytes,
                             size_t *scale_offset) {
   if (rows < 0 || rows > INT32_MAX) return fail(EP_ERR_INVALID_ARG, "ep_buffer_bytes: rows out of range");
-  const ep_status_t st = check_hidden(hidden, quant, "ep_buffer_bytes");
+  // (a feed-forward checkpoint is two inner sizes wide)
+  const ep_status_t st = check_hidden(hidden, quant, "ep_buffer_bytes", 2 * kMaxHidden);
   if (st != EP_OK) return st;
   const size_t total = buffer_bytes(rows, hidden, quant, scale_offset);
   if (total_bytes) *total_bytes = total;

@@ -154,7 +154,9 @@ size_t ep_workspace_bytes_ex(int64_t num_max_dispatch_tokens, int32_t num_topk, 
 /* Size of a receive buffer of `rows` rows (format above): writes the total
  * byte count and the scale offset to the host pointers (either may be NULL):
  * the start of the scale region, or for the interleaved form the offset of
- * the scales inside each row (Dq).  Host-only. */
+ * the scales inside each row (Dq).  Rows of tokens are at most 65536 wide;
+ * sizes are given up to 131072, the width of ep_ffn's widest checkpoint.
+ * Host-only. */
 ep_status_t ep_buffer_bytes(int64_t rows, int32_t hidden, ep_quant_t quant, size_t *total_bytes,
                             size_t *scale_offset);
 
