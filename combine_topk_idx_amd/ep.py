@@ -194,7 +194,8 @@ def _quant(q, interleaved: bool = False) -> int:
 
 
 def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+    """Bytes of a tensor; 0 for what is none (the library names a buffer that it misses)."""
+    return t.numel() * t.element_size() if isinstance(t, torch.Tensor) else 0
 
 
 def _check_args(*specs) -> int:
@@ -729,8 +730,8 @@ def ep_moe_gmm_b128(handle: ep_handle_t, a_buf, a_quant, k: int, n: int, w, w_sc
         stream, (a_buf, "a_buf", None, None, None), (w, "w", None, (E, wn, wk), None),
         (w_scales, "w_scales", torch.float32, (E, wn // 128, wk // 128), None), (out, "out", rows_out[0], None, rows_out[1]),
         (recv_count, "recv_count", torch.int64, None, E))
-    _check(_lib.ep_moe_gmm_b128(ctypes.byref(handle), _ptr(recv_count), a_buf.data_ptr(), _nbytes(a_buf), aq, k, n,
-                                _ptr(w), _ptr(w_scales), int(bool(transposed)), kind, oq, out.data_ptr(), _nbytes(out),
+    _check(_lib.ep_moe_gmm_b128(ctypes.byref(handle), _ptr(recv_count), _ptr(a_buf), _nbytes(a_buf), aq, k, n,
+                                _ptr(w), _ptr(w_scales), int(bool(transposed)), kind, oq, _ptr(out), _nbytes(out),
                                 stream))
 
 
