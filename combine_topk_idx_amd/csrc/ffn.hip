@@ -15,12 +15,15 @@
 //   few rows an expert    the weights' bytes (figures at TileFew)
 //   32 to 192 rows        a few tiles a CU: the last round and the stages' latency.
 //                         64 experts of 129 rows, 2048 -> 2 x 768, 8-bit checkpoint:
-//                         gate and up 157 us, down 63, dy W2 74, dx 108, weights 207
+//                         gate and up 161 us, down 63, dy W2 72, dx 108, weights 209
 //   many                  the matrix cores at the clock that the power limit leaves.
 //                         32768 rows in 32 experts, 7168 -> 2 x 2048: gate and up
-//                         1.60 ms (1.20 PFLOP/s), down 0.87 (1.10), dy W2 1.12 (0.86:
-//                         its epilogue reads and writes 540 MB), dx 1.76 (1.10),
-//                         weights 2.83 (1.02: sums of 1024 rows, 2.8 GB written)
+//                         1.61 ms (1.20 PFLOP/s), down 0.90 (1.07), dy W2 1.12 (0.86:
+//                         its epilogue reads and writes 540 MB, and does so in part
+//                         behind the next unit's stages), dx 1.79 (1.08), weights 2.87
+//                         (1.01: sums of 1024 rows, 2.8 GB written)
+// (medians of a profiled run whose inputs change from pass to pass; another
+// card of this kind took 4 to 6 % longer)
 #include "ffn.hpp"
 #include "gemm_core.hpp"
 
@@ -207,9 +210,12 @@ __device__ __forceinline__ void epilogue_up(const RowArgs &p, const RowTile &u, 
   }
 }
 
-// da in acc: dg, du and a to memory.  The checkpoint of the next fragment is
-// on its way while a fragment is worked on; rows and columns past the tile's
-// read its first ones.
+// da in acc: dg, du and a to memory.  The next fragment's checkpoint is asked
+// for before a fragment is worked on; rows and columns past the tile's read its
+// first ones.  On 256-row tiles the kernel needs 11 registers more than there
+// are: those are read back here, each time behind everything in flight (the next
+// unit's first stages, the stores, the checkpoint), so that the loads overlap
+// with the work in part only, and this is the slowest of the row products.
 template <int RF, int ACT, bool FP8, class Acc, class Row>
 __device__ __forceinline__ void epilogue_act(const RowArgs &p, const RowTile &u, int n0, int wn, int lane, Acc &acc,
                                              Row row_of) {
@@ -519,8 +525,8 @@ struct WeightArgs {
 // operands are k strided and are read through the transposing LDS reads.  A sum
 // is as long as an expert's rows, so short ones are bounded by the gradients'
 // bytes: 64 experts of 129 rows, 2048 x 2 x 768 and 768 x 2048: 604 MB written
-// in 207 us (240 before the stores left in whole lines, unwaited).  One expert
-// of 8192 rows, 4096 x 2 x 1408 and 1408 x 4096: 320 us, 886 TFLOP/s (272 tiles
+// in 209 us (240 before the stores left in whole lines, unwaited).  One expert
+// of 8192 rows, 4096 x 2 x 1408 and 1408 x 4096: 326 us, 870 TFLOP/s (272 tiles
 // on 256 CUs).
 __global__ __launch_bounds__(Tile256::kThreads) void weights256_kernel(WeightArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__

@@ -182,6 +182,7 @@ __device__ __forceinline__ RowTile row_tile(const Groups &g, int E, const int *_
 // Many rows an expert: 256-row tiles (half the bytes a product), whose
 // leftover ones are cut.
 // Up to 32 rows an expert, `few`: TileFew (launch(Int<0>())).
+// (640 and 128 units: 2.5 rounds and half a round of 256 CUs.)
 template <class F>
 __host__ inline hipError_t with_height(int64_t pairs, int64_t E, int64_t nc, bool few, F launch) {
   const int64_t used = E < pairs ? E : pairs, mean = pairs / used;
@@ -481,9 +482,9 @@ struct PipeN {
 // wave order through LDS.  64 columns (gated: 32 gate rows and the same 32 up
 // rows) make units enough for the whole card in small models.  k contiguous
 // operands.  Measured: 5 tokens, two of 8 experts 1024 -> 2 x 512, bf16 gate and
-// up 7.7 us, down 5.7 (together 19 with common stages): launch, first load and
+// up 7.7 us, down 5.9 (together 19 with common stages): launch, first load and
 // join; 128 tokens, 6 of 64 experts 2048 -> 2 x 768: 403 MB of gate and up
-// weights in 82 us, 4.9 TB/s, 201 MB of down weights in 45 (85 and 49 when a
+// weights in 82 us, 4.9 TB/s, 201 MB of down weights in 46 (85 and 49 when a
 // unit's first stages were fetched after the last of the one before had
 // arrived); 128 tokens, 8 of 256 e4m3 experts 7168 -> 2 x 2048: 7.4 GB in 1165
 // us, 6.35 TB/s, the card's rate of reads.
@@ -616,10 +617,12 @@ __device__ __forceinline__ void few_units(PipeFew<EB> &p, int units, Open open, 
 // Fragments are read a quarter ahead, between the matrix instructions.
 // Why this tile: a 256 x 256 tile reads 128 products a byte fetched, and 128 KB
 // of stages with 8 waves of 128 accumulators fill LDS and registers of a CU.
-// No LDS bank conflicts are counted; matrix cores are busy 71 % of the CUs'
+// No LDS bank conflicts are counted; matrix cores are busy 71-73 % of the CUs'
 // cycles in bf16 (32768 rows in 32 experts of 7168 -> 2 x 2048: 1.6 ms, 1.2
-// PFLOP/s at the 1.8 GHz that the power limit leaves) and 54 % in e4m3, whose
-// scaled sums take vector instructions beside them.
+// PFLOP/s at the 1.8 GHz that the power limit leaves) and 56 % in e4m3, whose
+// scaled sums take 37 % in vector instructions, hardly any of them under the
+// matrix instructions of the other wave (transposed: 48 and 31 %).  LDS reads are
+// active 28, 25 and 22 %.
 struct Tile256 {
   static constexpr int BN = 256, BM = 256, kThreads = 512, WN = 4, WM = 2;
   static constexpr int kStage = 512 * kKBytes, kLds = 2 * kStage;

@@ -2,7 +2,7 @@
 // with a scale per 128 x 128 block:
 //   out[r][n] = sum over blocks b of s_x[r][b] s_w[n / 128][b] (sum_{k in b} x[r][k] w[n][k])
 // A stage of the core holds exactly one block of 128 k, so the inner sum is
-// two matrix instructions from a zero accumulator, and the running sum takes
+// one matrix instruction from a zero accumulator, and the running sum takes
 // it times the product of the two scales with one fused multiply-add a value.
 // (The matrix cores' own scales are powers of two: they do not hold a float32.)
 //
@@ -10,10 +10,14 @@
 // TileFew); with many the matrix cores and the vector instructions beside them
 // at the clock that the power limit leaves: a pair of matrix instructions
 // takes 64 cycles, its eight fused multiply-adds and two products of scales 40,
-// so a pair is scaled while the next one runs.
-// 32768 rows in 32 experts: gate and up 7168 -> 2 x 2048 977 us (1.97 PFLOP/s),
-// transposed 4096 -> 7168 1070 us (1.80; four transposing reads a fragment for
-// two plain ones).  64 experts of 84 rows, 1408 -> 4096: 105 us, 128-row tiles.
+// so a pair is scaled while the next one runs -- within a wave; counted over a
+// SIMD the two still add up to 93 % of its cycles (56 + 37; transposed 79: 48 + 31).
+// 32768 rows in 32 experts: gate and up 7168 -> 2 x 2048 960-977 us a pass (1.97-2.0
+// PFLOP/s), transposed 4096 -> 7168 1062-1077 us (1.8; four transposing reads a
+// fragment for two plain ones); another card of this kind took 3 % longer.
+// 64 experts of 84 rows, 1408 -> 4096: 102 us a pass, 128-row tiles.
+// The 256-row forms but the plain one with float32 scales keep 8 to 18 registers in
+// memory, read back between two units, each behind the loads in flight.
 // Roundings: the output alone (bf16, or e4m3 with a scale per 128).
 #include "ffn.hpp"
 #include "gemm_core.hpp"
