@@ -530,7 +530,8 @@ ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, co
  *                   multiple of 128 with an 8-bit checkpoint
  *   w1, w2          device bf16 [E, 2I, H] and [E, H, I], 16-byte aligned
  *   checkpoint      device, 16-byte aligned, >= ep_buffer_bytes(max_rows, 2I,
- *                   checkpoint_quant); NULL: none is kept
+ *                   checkpoint_quant), no overlap with x_buf or out_buf; NULL:
+ *                   none is kept
  *   workspace       device, 256-byte aligned, >= ep_ffn_workspace_bytes(
  *                   max_rows, ...); in use as for ep_moe_layer
  *   out_buf         device bf16 [max_rows, H]; may not overlap x_buf.  Rows

@@ -80,7 +80,7 @@ MANY = uneven(40, 65, 400, 4, 232)
 # (rows by expert, H, I, checkpoint): one wide side at a time, reductions of one, two, three and five stages on the other.
 # (Few rows an expert with a bf16 checkpoint have the form of few rows.)
 FFN = []
-for counts, wide in ((LOW, 640), (MIDDLE, 640), (UPPER, 1600), (MANY, 1472)):
+for counts, wide in ((LOW, 640), (MIDDLE, 640), (UPPER, 1600), (MANY, 1344)):
     for i, short in enumerate((64, 128, 192, 320)):
         quant = "none" if i % 2 and counts is not LOW else "fp8_b128"
         FFN.append((counts, short, wide if quant == "none" else up(wide, 128) * 128, quant))
