@@ -521,6 +521,9 @@ ep_status_t ep_lora_backward(const ep_handle_t *handle, const void *grad_out, co
  * float32 scale per 128 (EP_QUANT_FP8_B128, quantised from the float32 sums by
  * dispatch's rule).  With x dispatched anew in the backward pass, 8-bit
  * checkpoints keep 2I + I/16 bytes a row.
+ * Equal calls give equal bits.  The order of a sum follows the launch's shape
+ * (rows an expert on average, sizes, and for few rows whether an 8-bit
+ * checkpoint is kept), so calls of other shapes agree to float32 sums.
  *   handle          host; any of the row arrangements
  *   recv_count      device int64 [E] as the layout wrote it; the rows of block e
  *                   are its first recv_count[e].  NULL: the whole block, for
